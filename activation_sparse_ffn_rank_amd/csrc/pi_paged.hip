@@ -1,0 +1,173 @@
+// pi_paged.hip -- host side of the C ABI declared in include/pi_paged_kv.h: argument checks, the
+// choice of kernel and grid, launches.  As in pi_abi.hip nothing here allocates, frees, synchronizes
+// or issues memset/memcpy nodes, and no C++ exception crosses the ABI.
+#include "pi_paged.hpp"
+
+#include <algorithm>
+#include <cmath>
+
+namespace {
+
+using namespace pik;
+
+constexpr int kMaxHeads = 1024;
+// Key ranges are cut so that about this many workgroups share the work of all requests.
+constexpr int kSplitTarget = 1024;
+
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// log2 of a page size, or -1.
+int page_log(int32_t page) {
+    switch (page) {
+        case 16: return 4;
+        case 32: return 5;
+        case 64: return 6;
+        case 128: return 7;
+        case 256: return 8;
+        default: return -1;
+    }
+}
+
+int check_cache(const pi_kv_cache *c) {
+    if (!c || !c->k_pages || !c->v_pages) return PI_ERR_NULL;
+    if (c->dtype != PI_KV_F16 && c->dtype != PI_KV_BF16) return PI_ERR_DTYPE;
+    if (page_log(c->page) < 0 || c->n_pages < 1 || c->n_kv < 1 || c->n_kv > kMaxHeads) return PI_ERR_SHAPE;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return PI_ERR_SHAPE;
+    if ((int64_t)c->n_pages * c->page > INT32_MAX) return PI_ERR_SHAPE;
+    if (!aligned16(c->k_pages) || !aligned16(c->v_pages)) return PI_ERR_ALIGN;
+    return PI_OK;
+}
+
+int check_batch(const pi_kv_batch *b) {
+    if (!b || !b->block_table || !b->q_start || !b->kv_len) return PI_ERR_NULL;
+    if (b->n_req < 1 || b->n_req > PI_KV_MAX_REQ || b->max_pages < 1 || b->max_pages > PI_KV_MAX_TABLE ||
+        b->table_stride < b->max_pages || b->max_q < 1 || b->max_q > PI_KV_MAX_TOKENS || b->max_kv < 0)
+        return PI_ERR_SHAPE;
+    return PI_OK;
+}
+
+int check_rows(const pi_kv_cache *c, int32_t total_q, int32_t n_q) {
+    if (total_q < 0 || total_q > PI_KV_MAX_TOKENS || n_q < 1 || n_q > kMaxHeads || n_q % c->n_kv != 0) return PI_ERR_SHAPE;
+    return PI_OK;
+}
+
+// Rows of [n][heads][head_dim] with strides in elements: 16-byte rows.
+int check_strides(const void *p, int64_t ts, int64_t hs) {
+    if (ts < 0 || hs < 0) return PI_ERR_SHAPE;
+    if (!aligned16(p) || ts % 8 != 0 || hs % 8 != 0) return PI_ERR_ALIGN;
+    return PI_OK;
+}
+
+struct AttnGeom {
+    int tiles;       // row tiles per kv head, at most
+    int items;       // items per kv head, at most
+    int target;      // split target, 0: no key range is cut
+    size_t part;     // bytes of the split items' partial sums
+};
+
+AttnGeom attn_geom(const pi_kv_cache *c, const pi_kv_batch *b, int total_q, int n_q) {
+    AttnGeom g{};
+    const int64_t group = n_q / c->n_kv;
+    const int64_t by_rows = total_q * group / kKvRowTile + std::min(b->n_req, total_q);
+    const int64_t by_req = b->n_req * ((std::min(b->max_q, total_q) * group + kKvRowTile - 1) / kKvRowTile);
+    g.tiles = (int)std::min(by_rows, by_req);
+    g.items = g.tiles;
+    // enough row tiles to fill the chip, or too few keys for two items: nothing is cut
+    if ((int64_t)g.tiles * c->n_kv < kSplitTarget && b->max_kv > kKvMinChunk) {
+        g.target = kSplitTarget;
+        g.items += kSplitTarget / c->n_kv + 2;      // 2: the device sums the work in fp32
+        g.part = (size_t)g.items * c->n_kv * (16 * c->head_dim + 32) * sizeof(float);
+    }
+    return g;
+}
+
+template <class T, int HD>
+int launch_attn(const KvAttnArgs &a, const AttnGeom &g, hipStream_t st) {
+    hipLaunchKernelGGL((k_kv_rows<T, HD>), dim3((uint32_t)g.items * a.n_kv), dim3(256), 0, st, a);
+    if (hipGetLastError() != hipSuccess) return PI_ERR_HIP;
+    if (!g.target) return PI_OK;
+    hipLaunchKernelGGL((k_kv_join<T, HD>), dim3((uint32_t)g.tiles * a.n_kv), dim3(256), 0, st, a);
+    return hipGetLastError() == hipSuccess ? PI_OK : PI_ERR_HIP;
+}
+
+template <class T>
+int launch_attn_hd(int hd, const KvAttnArgs &a, const AttnGeom &g, hipStream_t st) {
+    if (hd == 64) return launch_attn<T, 64>(a, g, st);
+    if (hd == 128) return launch_attn<T, 128>(a, g, st);
+    return launch_attn<T, 256>(a, g, st);
+}
+
+}  // namespace
+
+extern "C" int pi_kv_step(const pi_kv_tables *t, void *stream) {
+    if (!t || !t->cached || !t->fresh || !t->free_ring || !t->pool || !t->block_table || !t->q_start || !t->kv_len ||
+        !t->cached_next || !t->slots || !t->pool_next || !t->counts)
+        return PI_ERR_NULL;
+    if (t->n_req < 1 || t->n_req > PI_KV_MAX_REQ || page_log(t->page) < 0 || t->n_pages < 1 || t->max_pages < 1 ||
+        t->max_pages > PI_KV_MAX_TABLE || t->max_tokens < 1 || t->max_tokens > PI_KV_MAX_TOKENS ||
+        t->table_stride < t->max_pages || (int64_t)t->n_pages * t->page > INT32_MAX ||
+        (int64_t)t->max_pages * t->page > INT32_MAX)
+        return PI_ERR_SHAPE;
+    KvTablesArgs a{t->n_req, page_log(t->page), t->n_pages, t->max_pages, t->max_tokens, t->table_stride, t->cached, t->fresh,
+                   t->free_ring, t->pool, t->block_table, t->q_start, t->kv_len, t->cached_next, t->slots, t->pool_next, t->counts};
+    // A step in place runs in one workgroup, which reads all of the old state before it writes.
+    const bool in_place = t->cached_next == t->cached || t->pool_next == t->pool;
+    const int groups = in_place ? 1 : std::min(64, std::max((t->max_tokens + 1023) / 1024, (t->n_req + 255) / 256));
+    hipLaunchKernelGGL(k_kv_tables, dim3(groups), dim3(kKvTableThreads), 0, static_cast<hipStream_t>(stream), a);
+    return hipGetLastError() == hipSuccess ? PI_OK : PI_ERR_HIP;
+}
+
+extern "C" int pi_kv_append(const pi_kv_cache *cache, const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                            int64_t v_token_stride, int64_t v_head_stride, const int32_t *slots, int32_t n_tokens,
+                            void *stream) {
+    int rc = check_cache(cache);
+    if (rc) return rc;
+    if (!k || !v || !slots) return PI_ERR_NULL;
+    if (n_tokens < 0 || n_tokens > PI_KV_MAX_TOKENS) return PI_ERR_SHAPE;
+    if ((rc = check_strides(k, k_token_stride, k_head_stride)) || (rc = check_strides(v, v_token_stride, v_head_stride))) return rc;
+    if (n_tokens == 0) return PI_OK;
+    KvAppendArgs a{n_tokens, cache->n_kv, cache->head_dim, page_log(cache->page), cache->n_pages * cache->page,
+                   k_token_stride, k_head_stride, v_token_stride, v_head_stride, static_cast<const uint16_t *>(k),
+                   static_cast<const uint16_t *>(v), slots, static_cast<uint16_t *>(cache->k_pages),
+                   static_cast<uint16_t *>(cache->v_pages)};
+    const size_t lds = (size_t)kKvAppendTokens * (cache->head_dim / 2 + 1) * 4;
+    hipLaunchKernelGGL(k_kv_append, dim3((n_tokens + kKvAppendTokens - 1) / kKvAppendTokens, cache->n_kv), dim3(256), lds,
+                       static_cast<hipStream_t>(stream), a);
+    return hipGetLastError() == hipSuccess ? PI_OK : PI_ERR_HIP;
+}
+
+extern "C" size_t pi_kv_attn_workspace_bytes(const pi_kv_cache *cache, const pi_kv_batch *batch, int32_t total_q, int32_t n_q) {
+    if (check_cache(cache) || check_batch(batch) || check_rows(cache, total_q, n_q)) return 0;
+    return std::max<size_t>(attn_geom(cache, batch, total_q, n_q).part, 16);
+}
+
+extern "C" int pi_kv_attn(const pi_kv_cache *cache, const pi_kv_batch *batch, const void *q, int64_t q_token_stride,
+                          int64_t q_head_stride, void *out, int64_t out_token_stride, int64_t out_head_stride, int32_t total_q,
+                          int32_t n_q, float scale, int32_t window, void *ws, size_t ws_bytes, void *stream) {
+    int rc = check_cache(cache);
+    if (rc || (rc = check_batch(batch))) return rc;
+    if (!q || !out) return PI_ERR_NULL;
+    if ((rc = check_rows(cache, total_q, n_q))) return rc;
+    if (window < 0 || !(scale > 0.f) || !std::isfinite(scale)) return PI_ERR_SHAPE;
+    if ((rc = check_strides(q, q_token_stride, q_head_stride)) || (rc = check_strides(out, out_token_stride, out_head_stride)))
+        return rc;
+    const AttnGeom g = attn_geom(cache, batch, total_q, n_q);
+    if (!ws || ws_bytes < std::max<size_t>(g.part, 16)) return PI_ERR_WORKSPACE;
+    if (!aligned16(ws)) return PI_ERR_ALIGN;
+    if (total_q == 0) return PI_OK;
+    KvAttnArgs a{};
+    a.n_pages = cache->n_pages, a.n_kv = cache->n_kv, a.page_log = page_log(cache->page);
+    a.n_req = batch->n_req, a.max_pages = batch->max_pages, a.max_q = batch->max_q, a.max_kv = batch->max_kv;
+    a.total_q = total_q, a.n_q = n_q, a.group = n_q / cache->n_kv, a.window = window;
+    a.split_target = g.target, a.items = g.items;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.table_stride = batch->table_stride;
+    a.q_ts = q_token_stride, a.q_hs = q_head_stride, a.o_ts = out_token_stride, a.o_hs = out_head_stride;
+    a.k = static_cast<const uint16_t *>(cache->k_pages), a.v = static_cast<const uint16_t *>(cache->v_pages);
+    a.q = static_cast<const uint16_t *>(q), a.out = static_cast<uint16_t *>(out);
+    a.table = batch->block_table, a.q_start = batch->q_start, a.kv_len = batch->kv_len;
+    a.part = static_cast<float *>(ws);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return cache->dtype == PI_KV_F16 ? launch_attn_hd<KvF16>(cache->head_dim, a, g, st)
+                                     : launch_attn_hd<KvBf16>(cache->head_dim, a, g, st);
+}

@@ -1,0 +1,624 @@
+// pi_paged.hpp -- gfx950 kernels of the paged key/value cache: block tables (k_kv_tables), cache
+// append (k_kv_append) and attention over the pages (k_kv_rows, k_kv_join).
+//
+// Both products of attention run on MFMA with the keys along the rows of the first one,
+//   S^T = K Q^T   (A = K: 16 keys x 32 head dims, B = Q^T: 32 head dims x 16 query rows)
+//   O^T = V^T P^T (A = V^T: 16 head dims x 32 keys, B = P^T: 32 keys x 16 query rows),
+// so a lane holds scores and outputs of one query row only (row = lane % 16): the running maximum
+// and sum of the softmax, and every rescaling, are per-lane numbers.  The result of the first product
+// is the operand of the second one as it stands when the 32 keys of a block go to the two 16-key
+// tiles in this order: tile u, tile row 4a + b holds key 8a + 4u + b.  Lane group g = lane / 16 then
+// holds keys 8g .. 8g+7 of its row, which is the B operand's order, and V^T, held transposed in the
+// pages, is read 16 bytes (8 keys) per lane.  No value crosses lanes through LDS.
+#pragma once
+
+#include "pi_kernels.hpp"
+#include "pi_paged_kv.h"
+
+namespace pik {
+
+// ------------------------------------------------------------------------------ element types
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+struct KvF16 {
+    typedef f16 e;
+    typedef f16 v2 __attribute__((ext_vector_type(2)));
+    typedef f16 v8 __attribute__((ext_vector_type(8)));
+    static constexpr uint32_t kExpMask = 0x7c007c00u;   // exponent bits: all ones = infinity or NaN
+    // Weights are held as exp2(s - max + 8): fp16 keeps 8 more binary orders below the largest
+    // weight before it rounds to subnormals; the factor is in the row's sum too and divides out.
+    static constexpr float kShift = 8.f;
+    // The reference may lag the true maximum by this many powers of two (weights stay <= 2^14 < 65504).
+    static constexpr float kLag = 6.f;
+    static __device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+    }
+};
+
+struct KvBf16 {
+    typedef __bf16 e;
+    typedef __bf16 v2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+    static constexpr uint32_t kExpMask = 0x7f807f80u;
+    static constexpr float kShift = 0.f;                // bf16 has fp32's exponents
+    static constexpr float kLag = 6.f;
+    static __device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+    }
+};
+
+// Two values rounded to the element type (to nearest even), first one in the low half.
+template <class T>
+__device__ __forceinline__ uint32_t kv_pack(float a, float b) {
+    const f32x2 x = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, typename T::v2));
+}
+
+// ------------------------------------------------------------------------------ block tables
+
+struct KvTablesArgs {
+    int n_req, page_log, n_pages, max_pages, max_tokens;
+    int64_t table_stride;
+    const int *cached, *fresh;
+    int *ring;
+    const int *pool;
+    int *table, *q_start, *kv_len, *cached_next, *slots, *pool_next, *counts;
+};
+
+constexpr uint32_t kKvRefused = 0x80000000u, kKvEnded = 0x40000000u, kKvNeed = 0x3fffffffu;
+constexpr int kKvTableThreads = 1024;
+constexpr int kKvReqPerThread = PI_KV_MAX_REQ / kKvTableThreads;
+
+// Exclusive block scan of v (unsigned, mod 2^32); *total receives the sum.  part: one word per wave.
+__device__ __forceinline__ uint32_t kv_block_scan(uint32_t v, uint32_t *part, uint32_t *total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const uint32_t incl = (uint32_t)wave_incl_scan((int)v);
+    __syncthreads();                       // part may still be read by the scan before
+    if (lane == 63) part[wave] = incl;
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+    for (int w = 0; w < waves; ++w) {
+        before += w < wave ? part[w] : 0u;
+        all += part[w];
+    }
+    *total = all;
+    return before + incl - v;
+}
+
+// The step of the block tables.  Two scans over the requests (rows; then pages taken and pages given
+// back) that every workgroup makes for itself from the lengths (at most 32 KB from L2), after which
+// the workgroups share out the pages and the rows: nothing waits on another workgroup.  With one
+// workgroup all inputs are read before the first output is written, so a step may run in place.
+// The row sums stay below 2^32: at most 4096 requests of at most 2^19 + 1 counted rows.
+__global__ __launch_bounds__(kKvTableThreads) void k_kv_tables(KvTablesArgs a) {
+    __shared__ uint32_t s_row[PI_KV_MAX_REQ + 1];   // first row
+    __shared__ uint32_t s_need[PI_KV_MAX_REQ];      // pages asked for (ended: given back) by the requests before | flags
+    __shared__ uint32_t s_held[PI_KV_MAX_REQ];      // cached
+    __shared__ uint32_t s_part[kKvTableThreads / 64];
+    __shared__ uint32_t s_taken, s_denied;
+    const int tid = threadIdx.x, n = a.n_req;
+    const int per = (n + (int)blockDim.x - 1) / (int)blockDim.x;
+    const int page = 1 << a.page_log;
+    const int64_t room = (int64_t)a.max_pages << a.page_log;
+    int head = a.pool[0] % a.n_pages;
+    if (head < 0) head += a.n_pages;
+    const int count = min(max(a.pool[1], 0), a.n_pages);
+    if (tid == 0) s_taken = s_denied = 0;
+
+    int c[kKvReqPerThread], f[kKvReqPerThread];
+    uint32_t rows = 0;
+#pragma unroll
+    for (int k = 0; k < kKvReqPerThread; ++k) {
+        const int r = tid * per + k;
+        const bool in = k < per && r < n;
+        c[k] = in ? a.cached[r] : 0;
+        f[k] = in ? a.fresh[r] : 0;
+        rows += (uint32_t)min(max(f[k], 0), a.max_tokens + 1);
+    }
+    uint32_t total_rows, total_need, total_back;
+    uint32_t row = kv_block_scan(rows, s_part, &total_rows);
+    uint32_t need[kKvReqPerThread], back[kKvReqPerThread], need_sum = 0, back_sum = 0;
+    bool fits[kKvReqPerThread];
+#pragma unroll
+    for (int k = 0; k < kKvReqPerThread; ++k) {
+        const int r = tid * per + k;
+        const bool in = k < per && r < n;
+        if (in) s_row[r] = row;
+        row += (uint32_t)min(max(f[k], 0), a.max_tokens + 1);
+        const bool bad = c[k] < 0 || c[k] > room;
+        const int64_t end = (int64_t)c[k] + f[k];
+        const int have = bad ? 0 : (c[k] + page - 1) >> a.page_log;
+        fits[k] = in && f[k] >= 0 && !bad && end <= room && row <= (uint32_t)a.max_tokens;
+        need[k] = fits[k] ? (uint32_t)(((int)end + page - 1) >> a.page_log) - have : 0u;
+        back[k] = in && f[k] < 0 ? (uint32_t)have : 0u;
+        need_sum += need[k];
+        back_sum += back[k];
+    }
+    uint32_t nd = kv_block_scan(need_sum, s_part, &total_need);
+    uint32_t bk = kv_block_scan(back_sum, s_part, &total_back);
+    uint32_t taken = 0, denied = 0;
+#pragma unroll
+    for (int k = 0; k < kKvReqPerThread; ++k) {
+        const int r = tid * per + k;
+        if (k >= per || r >= n) continue;
+        const bool ended = f[k] < 0;
+        const bool ok = fits[k] && (need[k] == 0 || nd + need[k] <= (uint32_t)count);
+        s_need[r] = (ended ? bk | kKvEnded : nd) | (ok || back[k] ? 0u : kKvRefused);
+        s_held[r] = (uint32_t)c[k];
+        if (ok && need[k]) taken = max(taken, nd + need[k]);
+        denied += !ended && !ok;
+        nd += need[k];
+        bk += back[k];
+        if (blockIdx.x == 0) {
+            a.q_start[r + 1] = (int)min(s_row[r] + (uint32_t)min(max(f[k], 0), a.max_tokens + 1), (uint32_t)a.max_tokens);
+            a.kv_len[r] = ok ? c[k] + f[k] : 0;
+            a.cached_next[r] = ended ? 0 : ok ? c[k] + f[k] : c[k];
+        }
+    }
+    if (taken) atomicMax(&s_taken, taken);          // whole numbers: any order gives the same result
+    if (denied) atomicAdd(&s_denied, denied);
+    if (tid == 0) s_row[n] = total_rows;
+    __syncthreads();
+    if (blockIdx.x == 0 && tid == 0) {
+        a.q_start[0] = 0;
+        a.pool_next[0] = (int)(((int64_t)head + s_taken) % a.n_pages);
+        a.pool_next[1] = (int)min((int64_t)count - s_taken + total_back, (int64_t)a.n_pages);
+        a.counts[0] = (int)min(total_rows, (uint32_t)a.max_tokens);
+        a.counts[1] = (int)s_taken;
+        a.counts[2] = (int)total_back;
+        a.counts[3] = (int)s_denied;
+    }
+
+    // pages: a wave per request
+    const int lane = tid & 63;
+    for (int r = blockIdx.x * (blockDim.x >> 6) + (tid >> 6); r < n; r += gridDim.x * (blockDim.x >> 6)) {
+        const uint32_t w = s_need[r];
+        if (w & kKvRefused) continue;
+        int *const row_tab = a.table + (int64_t)r * a.table_stride;
+        if (w & kKvEnded) {
+            const uint32_t first = w & kKvNeed;
+            const int have = ((int)s_held[r] + page - 1) >> a.page_log;
+            for (int j = lane; j < have; j += 64)
+                a.ring[((int64_t)head + count + first + j) % a.n_pages] = row_tab[j];
+            continue;
+        }
+        const int have = ((int)s_held[r] + page - 1) >> a.page_log;
+        const int m = (((int)s_held[r] + (int)(s_row[r + 1] - s_row[r]) + page - 1) >> a.page_log) - have;
+        for (int j = lane; j < m; j += 64)
+            row_tab[have + j] = a.ring[((int64_t)head + (w & kKvNeed) + j) % a.n_pages];
+    }
+
+    // slots: a row per thread, its request by bisection over the first rows
+    for (int t = blockIdx.x * blockDim.x + tid; t < a.max_tokens; t += gridDim.x * blockDim.x) {
+        int slot = -1;
+        if ((uint32_t)t < total_rows) {
+            int lo = 0, hi = n;                      // s_row[lo] <= t < s_row[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s_row[mid] <= (uint32_t)t) lo = mid;
+                else hi = mid;
+            }
+            const uint32_t w = s_need[lo];
+            if (!(w & kKvRefused)) {
+                const int pos = (int)s_held[lo] + (int)((uint32_t)t - s_row[lo]);
+                const int have = ((int)s_held[lo] + page - 1) >> a.page_log, col = pos >> a.page_log;
+                const int id = col < have ? a.table[(int64_t)lo * a.table_stride + col]
+                                          : a.ring[((int64_t)head + (w & kKvNeed) + (col - have)) % a.n_pages];
+                if (id >= 0 && id < a.n_pages) slot = (id << a.page_log) + (pos & (page - 1));
+            }
+        }
+        a.slots[t] = slot;
+    }
+}
+
+// ------------------------------------------------------------------------------ cache append
+
+struct KvAppendArgs {
+    int n_tokens, n_kv, hd, page_log, n_slots;
+    int64_t k_ts, k_hs, v_ts, v_hs;
+    const uint16_t *k, *v;
+    const int *slots;
+    uint16_t *k_pages, *v_pages;
+};
+
+constexpr int kKvAppendTokens = 64;
+
+// 64 tokens of one kv head per workgroup.  Keys: 16-byte copies.  Values go through LDS so that a
+// lane stands for a token on the way out: tokens in neighbouring slots of a page then store
+// neighbouring 2-byte elements of one V^T row.
+__global__ __launch_bounds__(256) void k_kv_append(KvAppendArgs a) {
+    extern __shared__ uint32_t s_v[];                // [64][hd/2 + 1]
+    const int t0 = blockIdx.x * kKvAppendTokens, h = blockIdx.y, tid = threadIdx.x;
+    const int nt = min(kKvAppendTokens, a.n_tokens - t0);
+    const int per = a.hd >> 3, lds_row = (a.hd >> 1) + 1;
+    for (int i = tid; i < nt * per; i += 256) {
+        const int t = i / per, ch = i - t * per;
+        const uint32_t slot = (uint32_t)a.slots[t0 + t];
+        if (slot >= (uint32_t)a.n_slots) continue;
+        const uint4 kx = ld16(a.k + (t0 + t) * a.k_ts + h * a.k_hs + ch * 8);
+        const uint4 vx = ld16(a.v + (t0 + t) * a.v_ts + h * a.v_hs + ch * 8);
+        const int64_t pg = slot >> a.page_log, off = slot & ((1u << a.page_log) - 1);
+        *reinterpret_cast<uint4 *>(a.k_pages + ((((pg * a.n_kv + h) << a.page_log) + off) * a.hd + ch * 8)) = kx;
+        uint32_t *const d = s_v + t * lds_row + ch * 4;
+        d[0] = vx.x, d[1] = vx.y, d[2] = vx.z, d[3] = vx.w;
+    }
+    __syncthreads();
+    const int t = tid & 63;
+    if (t >= nt) return;
+    const uint32_t slot = (uint32_t)a.slots[t0 + t];
+    if (slot >= (uint32_t)a.n_slots) return;
+    const int64_t pg = slot >> a.page_log, off = slot & ((1u << a.page_log) - 1);
+    uint16_t *const vp = a.v_pages + (((pg * a.n_kv + h) * a.hd) << a.page_log) + off;
+    for (int d = (tid >> 6); d < (a.hd >> 1); d += 4) {
+        const uint32_t w = s_v[t * lds_row + d];
+        vp[(int64_t)(2 * d) << a.page_log] = (uint16_t)w;
+        vp[(int64_t)(2 * d + 1) << a.page_log] = (uint16_t)(w >> 16);
+    }
+}
+
+// ------------------------------------------------------------------------------ attention
+
+struct KvAttnArgs {
+    int n_pages, n_kv, page_log;
+    int n_req, max_pages, max_q, max_kv, total_q, n_q, group, window;
+    int split_target;                 // 0: key ranges are not cut
+    int items;                        // items per kv head that the workspace and the grid hold
+    float scale_log2;                 // scale / ln 2, > 0: weights are powers of two
+    int64_t table_stride, q_ts, q_hs, o_ts, o_hs;
+    const uint16_t *k, *v, *q;
+    const int *table, *q_start, *kv_len;
+    uint16_t *out;
+    float *part;                      // per split item: O^T [HD/16][64 lanes][4], then max [16], sum [16]
+};
+
+// Rows and keys of request r: the rows of one kv head are (token, query head of the group), token
+// major; new tokens past max_q and keys past the bounds are left out.
+struct KvReq {
+    int q0, n, m;          // first packed row, new tokens, keys
+    int rows;              // query rows per kv head
+    int lo, hi;            // keys that any of its rows may see
+};
+__device__ __forceinline__ KvReq kv_req(const KvAttnArgs &a, int r) {
+    KvReq x;
+    const int q0 = a.q_start[r], q1 = a.q_start[r + 1];
+    x.q0 = q0;
+    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.total_q;
+    x.n = ok ? q1 - q0 : 0;
+    x.m = max(a.kv_len[r], 0);
+    x.rows = min(x.n, a.max_q) * a.group;
+    x.hi = (int)min((int64_t)min(x.m, a.max_kv), (int64_t)a.max_pages << a.page_log);
+    x.lo = a.window ? min(max(x.m - x.n - a.window + 1, 0), x.hi) & ~63 : 0;
+    return x;
+}
+
+constexpr int kKvRowTile = 16;          // query rows of a k_kv_rows workgroup
+constexpr int kKvMinChunk = 256;        // keys of a split item, at least
+
+// Keys of one split item, from the sum over all requests of row tiles x keys.
+__device__ __forceinline__ int kv_chunk(const KvAttnArgs &a, int lane) {
+    if (!a.split_target) return 0x40000000;
+    float sum = 0.f;
+    for (int r0 = 0; r0 < a.n_req; r0 += 64) {
+        float x = 0.f;
+        if (r0 + lane < a.n_req) {
+            const KvReq q = kv_req(a, r0 + lane);
+            x = (float)((q.rows + kKvRowTile - 1) / kKvRowTile) * (float)(q.hi - q.lo);
+        }
+        sum += wave_sum(x);
+    }
+    const float c = ceilf(sum * (float)a.n_kv / (float)a.split_target / 64.f) * 64.f;
+    return max((int)fminf(c, 1073741824.f), kKvMinChunk);
+}
+
+// Item `want` of one kv head: requests in order, row tiles, key chunks.
+struct KvItem {
+    int r, tile, split, splits;     // r < 0: there is no such item
+    KvReq q;
+};
+template <bool JOIN>                // JOIN: items are row tiles, `first` receives the first split item
+__device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, int chunk, int lane, int *first) {
+    KvItem it;
+    it.r = -1;
+    int base = 0, base_split = 0;
+    for (int r0 = 0; r0 < a.n_req; r0 += 64) {
+        KvReq q{};
+        int tiles = 0, splits = 1;
+        if (r0 + lane < a.n_req) {
+            q = kv_req(a, r0 + lane);
+            tiles = (q.rows + kKvRowTile - 1) / kKvRowTile;
+            splits = max((q.hi - q.lo + chunk - 1) / chunk, 1);
+        }
+        const int items = tiles * splits, mine = JOIN ? tiles : items;
+        const int incl = wave_incl_scan(mine), total = __builtin_amdgcn_readlane(incl, 63);
+        const int incl_split = JOIN ? wave_incl_scan(items) : 0;
+        if (want < base + total) {
+            const uint64_t past = __ballot(incl > want - base);
+            const int l = __builtin_ctzll(past);
+            const int at = want - base - (bcast(incl, l) - bcast(mine, l));
+            it.r = r0 + l;
+            it.splits = bcast(splits, l);
+            it.tile = JOIN ? at : at / it.splits;
+            it.split = JOIN ? 0 : at - it.tile * it.splits;
+            it.q.q0 = bcast(q.q0, l), it.q.n = bcast(q.n, l), it.q.m = bcast(q.m, l);
+            it.q.rows = bcast(q.rows, l), it.q.lo = bcast(q.lo, l), it.q.hi = bcast(q.hi, l);
+            if (JOIN) *first = base_split + bcast(incl_split, l) - bcast(items, l) + at * it.splits;
+            return it;
+        }
+        base += total;
+        if (JOIN) base_split += __builtin_amdgcn_readlane(incl_split, 63);
+    }
+    return it;
+}
+
+// Running state of 16 query rows in one wave: O^T tiles, the reference of the exponents (log2 units)
+// and this lane's share of the row's sum.
+template <int HD>
+struct KvRowState {
+    f32x4 o[HD / 16];
+    float ref, sum;
+};
+
+// The largest of the four lane groups' values, per row.
+__device__ __forceinline__ float kv_row_max(float x) {
+    x = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ __forceinline__ float kv_row_sum(float x) {
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
+
+// One workgroup: one item (16 query rows of one kv head, one key range) of one request; its waves
+// take a part of the range each, 32 keys at a time, straight from the pages into registers.
+template <class T, int HD>
+__global__ __launch_bounds__(256) void k_kv_rows(KvAttnArgs a) {
+    constexpr int kSteps = HD / 32, kTiles = HD / 16, kWaves = 4;
+    __shared__ f32x4 s_o[kWaves / 2][kTiles][64];
+    __shared__ float s_ref[kWaves][16], s_sum[kWaves / 2][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int col = lane & 15, g = lane >> 4;
+    const int h = blockIdx.x % a.n_kv, want = blockIdx.x / a.n_kv;
+    const KvItem it = kv_item<false>(a, want, kv_chunk(a, lane), lane, nullptr);
+    if (it.r < 0) return;
+    const KvReq &rq = it.q;
+
+    // this lane's query row
+    const int row = it.tile * kKvRowTile + col, row_c = min(row, rq.rows - 1);
+    const int tok = row_c / a.group, head = h * a.group + (row_c - tok * a.group);
+    const int pos = rq.m - rq.n + tok;
+    const int see_hi = min(pos + 1, rq.hi), see_lo = a.window ? max(pos - a.window + 1, 0) : 0;
+    uint4 qf[kSteps];
+    {
+        const uint16_t *qp = a.q + (int64_t)(rq.q0 + tok) * a.q_ts + (int64_t)head * a.q_hs + 8 * g;
+#pragma unroll
+        for (int t = 0; t < kSteps; ++t) qf[t] = ld16(qp + 32 * t);
+    }
+    // keys that some row of the tile sees (first and last token), within the item's chunk
+    const int tok_a = it.tile * kKvRowTile / a.group, tok_b = (min(it.tile * kKvRowTile + kKvRowTile, rq.rows) - 1) / a.group;
+    const int pos_a = rq.m - rq.n + tok_a, pos_b = rq.m - rq.n + tok_b;
+    const int tile_hi = min(pos_b + 1, rq.hi), tile_lo = a.window ? max(pos_a - a.window + 1, 0) : 0;
+    // every row of the tile sees keys in [all_lo, all_hi)
+    const int all_hi = min(pos_a + 1, rq.hi), all_lo = a.window ? max(pos_b - a.window + 1, 0) : 0;
+    int lo = max(tile_lo & ~31, rq.lo), hi = tile_hi;
+    if (it.splits > 1) {
+        const int chunk = kv_chunk(a, lane), from = rq.lo + it.split * chunk;
+        lo = max(lo, from);
+        hi = min(hi, from + chunk);
+    }
+    // this wave's part
+    const int part = max((((hi - lo + kWaves - 1) / kWaves) + 31) & ~31, 32);
+    const int k_lo = lo + wave * part, k_hi = min(k_lo + part, hi);
+
+    KvRowState<HD> st;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) st.o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    st.ref = -INFINITY;
+    st.sum = 0.f;
+
+    const int *const tab = a.table + (int64_t)it.r * a.table_stride;
+    const int page = 1 << a.page_log, held = (rq.hi + page - 1) >> a.page_log;
+    int tab0 = 0, ids = -1;
+    for (int kb = k_lo; kb < k_hi; kb += 32) {
+        const int pg = kb >> a.page_log;
+        if (kb == k_lo || pg - tab0 + 1 >= 64) {       // the next 64 table entries, one per lane
+            tab0 = pg;
+            ids = tab0 + lane < held ? tab[tab0 + lane] : -1;
+        }
+        // pages of keys kb..+15 and kb+16..+31 (the same one unless pages hold 16 positions)
+        int id0 = bcast(ids, pg - tab0), id1 = bcast(ids, ((kb + 16) >> a.page_log) - tab0);
+        const bool dead0 = (uint32_t)id0 >= (uint32_t)a.n_pages, dead1 = (uint32_t)id1 >= (uint32_t)a.n_pages;
+        if (dead0 && dead1) continue;
+        if (dead0) id0 = id1;                            // read something in bounds; its keys are masked below
+        if (dead1) id1 = id0;
+        const int in_page = kb & (page - 1), in_page1 = (kb + 16) & (page - 1);
+        const int64_t b0 = (((int64_t)id0 * a.n_kv + h) << a.page_log) * HD;
+        const int64_t b1 = (((int64_t)id1 * a.n_kv + h) << a.page_log) * HD;
+
+        // scores of 32 keys: tile u, row 4a + b is key 8a + 4u + b
+        const int krow = 8 * ((col >> 2) & 1) + (col & 3);
+        const uint16_t *kp = a.k + (col & 8 ? b1 + (int64_t)(in_page1 + krow) * HD : b0 + (int64_t)(in_page + krow) * HD) + 8 * g;
+        uint4 kf[2][kSteps];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int t = 0; t < kSteps; ++t) kf[u][t] = ld16(kp + 4 * u * HD + 32 * t);
+        const int64_t vrow = (g & 2 ? b1 + in_page1 : b0 + in_page) + 8 * (g & 1);
+        const uint16_t *vp = a.v + vrow + ((int64_t)col << a.page_log);
+        uint4 vf[kTiles];
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) vf[t] = ld16(vp + ((int64_t)(16 * t) << a.page_log));
+
+        float s[8];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int t = 0; t < kSteps; ++t) acc = T::mfma16(kf[u][t], qf[t], acc);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[4 * u + i] = acc[i] * a.scale_log2;
+        }
+
+        uint32_t odd_keys = 0;                           // keys of the block with an infinite or NaN value somewhere
+        if (kb < all_lo || kb + 32 > all_hi || dead0 || dead1) {
+            const bool dead = g & 2 ? dead1 : dead0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int j = kb + 8 * g + e;
+                if (dead || j < see_lo || j >= see_hi) s[e] = -INFINITY;
+            }
+            // Values that no row of the tile sees are cleared (0 x infinity would be NaN); those
+            // that some rows see and others do not, and that are not finite, are added row by row.
+            uint32_t odd = 0;
+#pragma unroll
+            for (int e2 = 0; e2 < 4; ++e2) {
+                const int j = kb + 8 * g + 2 * e2;
+                const uint32_t keep = (dead || j < tile_lo || j >= tile_hi ? 0u : 0xffffu) |
+                                      (dead || j + 1 < tile_lo || j + 1 >= tile_hi ? 0u : 0xffff0000u);
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) {
+                    uint32_t &w = e2 == 0 ? vf[t].x : e2 == 1 ? vf[t].y : e2 == 2 ? vf[t].z : vf[t].w;
+                    w &= keep;
+                    if ((w & T::kExpMask & 0xffffu) == (T::kExpMask & 0xffffu)) odd |= 1u << (2 * e2);
+                    if ((w & T::kExpMask & 0xffff0000u) == (T::kExpMask & 0xffff0000u)) odd |= 2u << (2 * e2);
+                }
+            }
+            if (pos_a != pos_b && __any(odd != 0)) {
+#pragma unroll
+                for (int x = 1; x < 16; x <<= 1) odd |= __shfl_xor(odd, x);
+                odd_keys = (uint32_t)bcast((int)odd, 0) | (uint32_t)bcast((int)odd, 16) << 8 |
+                           (uint32_t)bcast((int)odd, 32) << 16 | (uint32_t)bcast((int)odd, 48) << 24;
+#pragma unroll
+                for (int e2 = 0; e2 < 4; ++e2) {
+                    const uint32_t keep = (odd >> (2 * e2) & 1 ? 0u : 0xffffu) | (odd >> (2 * e2) & 2 ? 0u : 0xffff0000u);
+#pragma unroll
+                    for (int t = 0; t < kTiles; ++t) (e2 == 0 ? vf[t].x : e2 == 1 ? vf[t].y : e2 == 2 ? vf[t].z : vf[t].w) &= keep;
+                }
+            }
+        }
+
+        float top = s[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) top = fmaxf(top, s[e]);
+        // The reference moves only when some score of the wave passes it by more than the lag.
+        if (__any(top - T::kShift > st.ref + T::kLag)) {
+            const float ref = fmaxf(kv_row_max(top) - T::kShift, st.ref);
+            const float f = st.ref == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(st.ref - ref);
+            st.sum *= f;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) st.o[t] *= f;
+            st.ref = ref;
+        }
+        const float ref = st.ref == -INFINITY ? 0.f : st.ref;
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            p[e] = __builtin_amdgcn_exp2f(s[e] - ref);
+            st.sum += p[e];
+        }
+        const uint4 pf = make_uint4(kv_pack<T>(p[0], p[1]), kv_pack<T>(p[2], p[3]), kv_pack<T>(p[4], p[5]), kv_pack<T>(p[6], p[7]));
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) st.o[t] = T::mfma16(vf[t], pf, st.o[t]);
+
+        while (odd_keys) {
+            const int j = __builtin_ctz(odd_keys);
+            odd_keys &= odd_keys - 1;
+            float mine = p[0];
+#pragma unroll
+            for (int e = 1; e < 8; ++e) mine = (j & 7) == e ? p[e] : mine;
+            const float w = __shfl(mine, (j >> 3) * 16 + col);
+            if (kb + j < see_lo || kb + j >= see_hi) continue;
+            const uint16_t *x = a.v + (j & 16 ? b1 + in_page1 + (j & 15) : b0 + in_page + j) + ((int64_t)(4 * g) << a.page_log);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    st.o[t][i] += w * (float)__builtin_bit_cast(typename T::e, x[(int64_t)(16 * t + i) << a.page_log]);
+        }
+    }
+
+    // the waves' parts: a common reference per row, then sums in a fixed order
+    if (lane < 16) s_ref[wave][lane] = st.ref;
+    __syncthreads();
+    float ref = s_ref[0][col];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) ref = fmaxf(ref, s_ref[w][col]);
+    const float f = st.ref == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(st.ref - ref);
+    st.sum *= f;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) st.o[t] *= f;
+#pragma unroll
+    for (int half = kWaves / 2; half >= 1; half >>= 1) {
+        if (wave >= half && wave < 2 * half) {
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) s_o[wave - half][t][lane] = st.o[t];
+            s_sum[wave - half][lane] = st.sum;
+        }
+        __syncthreads();
+        if (wave < half) {
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) st.o[t] += s_o[wave][t][lane];
+            st.sum += s_sum[wave][lane];
+        }
+        __syncthreads();
+    }
+    if (wave != 0) return;
+    const float sum = kv_row_sum(st.sum);
+    if (it.splits == 1) {
+        if (row >= rq.rows) return;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        uint16_t *op = a.out + (int64_t)(rq.q0 + tok) * a.o_ts + (int64_t)head * a.o_hs + 4 * g;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+            *reinterpret_cast<uint2 *>(op + 16 * t) = make_uint2(kv_pack<T>(st.o[t][0] * inv, st.o[t][1] * inv),
+                                                                 kv_pack<T>(st.o[t][2] * inv, st.o[t][3] * inv));
+        return;
+    }
+    float *const pt = a.part + (int64_t)blockIdx.x * (16 * HD + 32);
+    if (row < rq.rows) {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) reinterpret_cast<f32x4 *>(pt)[t * 64 + lane] = st.o[t];
+        if (g == 0) {
+            pt[16 * HD + col] = ref;
+            pt[16 * HD + 16 + col] = sum;
+        }
+    }
+}
+
+// Joins the split items of one row tile of one kv head, in the order of their key ranges.
+template <class T, int HD>
+__global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
+    constexpr int kTiles = HD / 16;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
+    const int h = blockIdx.x % a.n_kv, want = blockIdx.x / a.n_kv;
+    int first = 0;
+    const KvItem it = kv_item<true>(a, want, kv_chunk(a, lane), lane, &first);
+    // (row ranges that overlap can name more items than the grid holds; those have no partial sums)
+    if (it.r < 0 || it.splits == 1 || first + it.splits > a.items) return;
+    const int row = it.tile * kKvRowTile + col;
+    if (row >= it.q.rows) return;
+    const int tok = row / a.group, head = h * a.group + (row - tok * a.group);
+    const int64_t stride = (int64_t)a.n_kv * (16 * HD + 32);
+    const float *const pt = a.part + (int64_t)first * stride + (int64_t)h * (16 * HD + 32);
+    float ref = -INFINITY, sum = 0.f;
+    for (int s = 0; s < it.splits; ++s) ref = fmaxf(ref, pt[s * stride + 16 * HD + col]);
+    f32x4 o[(kTiles + 3) / 4];
+#pragma unroll
+    for (int i = 0; i < (kTiles + 3) / 4; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < it.splits; ++s) {
+        const float r = pt[s * stride + 16 * HD + col];
+        const float f = r == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(r - ref);
+        sum += f * pt[s * stride + 16 * HD + 16 + col];
+#pragma unroll
+        for (int i = 0; i < (kTiles + 3) / 4; ++i) o[i] += f * reinterpret_cast<const f32x4 *>(pt + s * stride)[(wave + 4 * i) * 64 + lane];
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint16_t *op = a.out + (int64_t)(it.q.q0 + tok) * a.o_ts + (int64_t)head * a.o_hs + 4 * g;
+#pragma unroll
+    for (int i = 0; i < (kTiles + 3) / 4; ++i)
+        *reinterpret_cast<uint2 *>(op + 16 * (wave + 4 * i)) =
+            make_uint2(kv_pack<T>(o[i][0] * inv, o[i][1] * inv), kv_pack<T>(o[i][2] * inv, o[i][3] * inv));
+}
+
+}  // namespace pik

@@ -1,0 +1,423 @@
+"""The paged-cache operators on the GPU against plain 64-bit references: block tables, append, attention, and
+the three together in a replayed graph."""
+import math
+import random
+
+import pytest
+import torch
+
+import activation_sparse_ffn_rank_amd as pi
+import kv_util
+from gpu_util import announce
+
+pytestmark = pytest.mark.gpu
+
+
+def dev(x, dtype=torch.int32):
+    return torch.tensor(x, dtype=dtype, device="cuda")
+
+
+# ------------------------------------------------------------------------------ tables
+
+def run_step(cached, fresh, ring, pool, table, page, max_tokens, in_place=False, slack=0):
+    n = len(cached)
+    wide = torch.full((n, len(table[0]) + slack), -7, dtype=torch.int32, device="cuda")
+    st = dict(cached=dev(cached), fresh=dev(fresh), free_ring=dev(ring), pool=dev(pool))
+    st["block_table"] = wide[:, : len(table[0])]
+    st["block_table"].copy_(dev(table))
+    new = lambda m: torch.full((m,), -77, dtype=torch.int32, device="cuda")
+    st.update(q_start=new(n + 1), kv_len=new(n), slots=new(max_tokens), counts=new(4))
+    st["cached_next"] = st["cached"] if in_place else new(n)
+    st["pool_next"] = st["pool"] if in_place else new(2)
+    tables = pi.make_kv_tables(st["cached"], st["fresh"], st["free_ring"], st["pool"], st["block_table"], page, st["q_start"],
+                               st["kv_len"], st["cached_next"], st["slots"], st["pool_next"], st["counts"])
+    pi.pi_kv_step(tables)
+    torch.cuda.synchronize()
+    assert slack == 0 or bool((wide[:, len(table[0]):] == -7).all())
+    return st, tables
+
+
+def check_step(st, want):
+    for name, value in want.items():
+        assert st[name].cpu().tolist() == value, name
+
+
+@pytest.mark.parametrize("in_place", (False, True))
+@pytest.mark.parametrize("n_req,page,max_pages,max_tokens,free", [
+    (1, 16, 1, 1, None), (1, 256, 3, 700, None), (7, 16, 5, 100, None), (64, 32, 9, 300, None), (64, 16, 40, 257, 20),
+    (333, 128, 4, 4000, 100), (1025, 64, 3, 5000, None), (1500, 16, 70, 40000, None), (4096, 16, 6, 70000, 3000), (200, 16, 9, 30, 0)])
+def test_step(n_req, page, max_pages, max_tokens, free, in_place):
+    announce(f"kv step n_req={n_req} page={page} max_pages={max_pages} max_tokens={max_tokens} free={free} in_place={in_place}")
+    for seed in range(2):
+        args = kv_util.step_inputs(seed, n_req, page, max_pages, max_tokens, free=free)
+        want = kv_util.step_reference(*args, page, max_tokens)
+        st, _ = run_step(*args, page, max_tokens, in_place, slack=seed * 3)
+        check_step(st, want)
+
+
+def test_step_no_tokens_and_all_ended():
+    for kinds in ((0,), (-1,), (-9,)):
+        announce(f"kv step kinds={kinds}")
+        args = kv_util.step_inputs(3, 50, 16, 8, 10, kinds=kinds)
+        st, _ = run_step(*args, 16, 10)
+        check_step(st, kv_util.step_reference(*args, 16, 10))
+
+
+def test_step_lengths_out_of_bounds():
+    announce("kv step lengths out of bounds")
+    args = kv_util.step_inputs(4, 300, 32, 6, 2000, in_bounds=False)
+    st, _ = run_step(*args, 32, 2000)
+    check_step(st, kv_util.step_reference(*args, 32, 2000))
+
+
+def test_steps_in_place_follow_the_rules():
+    """Forty steps on their own state (in place, replayed as a graph): every page stays in one place."""
+    page, max_pages, n, max_tokens = 16, 12, 24, 400
+    rng = random.Random(5)
+    n_pages = 150
+    cached, table, ring, pool = [0] * n, [[-1] * max_pages for _ in range(n)], list(range(n_pages)), [0, n_pages]
+    announce("kv step in place, 40 steps")
+    st, tables = run_step(cached, [0] * n, ring, pool, table, page, max_tokens, in_place=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pi.pi_kv_step(tables)
+    for _ in range(40):
+        fresh = [rng.choice((1, 1, 1, 0, rng.randint(1, 40), -1)) for _ in range(n)]
+        st["fresh"].copy_(dev(fresh))
+        want = kv_util.step_reference(st["cached"].tolist(), fresh, st["free_ring"].tolist(), st["pool"].tolist(),
+                                      st["block_table"].tolist(), page, max_tokens)
+        graph.replay()
+        torch.cuda.synchronize()
+        check_step(st, want)
+        head, count = st["pool"].tolist()
+        free = [st["free_ring"].tolist()[(head + j) % n_pages] for j in range(count)]
+        held = [p for row, c in zip(st["block_table"].tolist(), st["cached"].tolist()) for p in row[: kv_util.ceil_div(c, page)]]
+        assert sorted(free + held) == list(range(n_pages))
+
+
+# ------------------------------------------------------------------------------ append
+
+@pytest.mark.parametrize("tokens,n_kv,hd,page,dtype,fused", [
+    (1, 1, 64, 16, "f16", False), (3, 2, 128, 16, "bf16", True), (16, 32, 128, 16, "f16", True), (63, 3, 256, 32, "bf16", False),
+    (64, 2, 64, 256, "f16", True), (65, 8, 64, 64, "bf16", True), (500, 4, 128, 128, "f16", False), (1031, 2, 256, 64, "f16", True),
+    (777, 5, 64, 32, "bf16", False)])
+def test_append(tokens, n_kv, hd, page, dtype, fused):
+    announce(f"kv append tokens={tokens} n_kv={n_kv} hd={hd} page={page} {dtype} fused={fused}")
+    gen = torch.Generator().manual_seed(tokens)
+    rng = random.Random(tokens)
+    n_pages = kv_util.ceil_div(tokens, page) * 2 + 3
+    for scattered in (False, True):
+        # runs of neighbouring slots from odd places on, or slots in any order; some rows without one
+        perm = torch.randperm(n_pages * page, generator=gen)[:tokens] if scattered else torch.arange(tokens) + rng.randrange(page)
+        slots = perm.to(torch.int32)
+        for t in range(0, tokens, 11):
+            if tokens > 1:
+                slots[t] = (-1, n_pages * page, -2 ** 31, 2 ** 31 - 1)[t // 11 % 4]
+        k0 = torch.randn((n_pages, n_kv, page, hd), generator=gen).to(kv_util.DT[dtype])
+        v0 = torch.randn((n_pages, n_kv, hd, page), generator=gen).to(kv_util.DT[dtype])
+        if fused:
+            qkv = torch.randn((tokens, 3 * n_kv + 1, hd), generator=gen).to(kv_util.DT[dtype]).cuda()
+            k, v = qkv[:, 1: 2 * n_kv: 2] if n_kv > 1 else qkv[:, 1:2], qkv[:, 2 * n_kv: 3 * n_kv]
+        else:
+            k, v = (torch.randn((tokens, n_kv, hd), generator=gen).to(kv_util.DT[dtype]).cuda() for _ in range(2))
+        kg, vg = k0.cuda(), v0.cuda()
+        pi.pi_kv_append(pi.make_kv_cache(kg, vg), k[:, :n_kv], v, slots.cuda())
+        torch.cuda.synchronize()
+        kc, vc = k.cpu(), v.cpu()
+        for t, s in enumerate(slots.tolist()):
+            if 0 <= s < n_pages * page:
+                k0[s // page, :, s % page] = kc[t]
+                v0[s // page, :, :, s % page] = vc[t]
+        assert torch.equal(kg.cpu().view(torch.int16), k0.view(torch.int16)), "keys"
+        assert torch.equal(vg.cpu().view(torch.int16), v0.view(torch.int16)), "values"
+
+
+# ------------------------------------------------------------------------------ attention
+
+def run_attn(c, window=0, *, max_q=None, max_kv=None, stream=None, wide=False):
+    """The call on a case's tensors; `wide`: queries, outputs and tables are slices of wider rows."""
+    n = [b - a for a, b in zip(c["starts"], c["starts"][1:])]
+    dt, (rows, n_q, hd) = c["q"].dtype, c["q"].shape
+    table = dev(c["table"])
+    if wide:
+        buf = torch.full((rows, n_q + 3, hd + 8), 7.0, dtype=dt, device="cuda")
+        q, o_all = buf[:, 1: n_q + 1, :hd], torch.full((rows + 2, n_q + 5, hd + 16), 7.0, dtype=dt, device="cuda")
+        q.copy_(c["q"].cuda())
+        out = o_all[1: rows + 1, 2: n_q + 2, 8: hd + 8]
+        t_all = torch.full((table.shape[0], table.shape[1] + 5), 1 << 30, dtype=torch.int32, device="cuda")
+        t_all[:, : table.shape[1]] = table
+        table = t_all[:, : table.shape[1]]
+    else:
+        q, out = c["q"].cuda(), torch.full((rows, n_q, hd), 7.0, dtype=dt, device="cuda")
+    cache = pi.make_kv_cache(c["k"].cuda(), c["v"].cuda())
+    batch = pi.make_kv_batch(table, dev(c["starts"]), dev(c["kv"]), max_q=max_q or max(1, max(n)),
+                             max_kv=max(c["kv"]) if max_kv is None else max_kv)
+    ws = torch.full((pi.pi_kv_attn_workspace_bytes(cache, batch, rows, n_q),), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    pi.pi_kv_attn(cache, batch, q, out, ws, scale=c["scale"], window=window, stream=stream)
+    torch.cuda.synchronize()
+    if wide:
+        got = out.clone()
+        out.fill_(7.0)
+        assert bool((o_all == 7.0).all()), "written outside the output's rows"
+        return got
+    return out
+
+
+def attn(c, window=0, **kw):
+    got = run_attn(c, window, **kw)
+    return got.cpu()
+
+
+def check_attn(c, window=0, got=None, **kw):
+    got = attn(c, window, **kw) if got is None else got
+    want, mag = kv_util.attn_reference(c["q"], c["k"], c["v"], c["table"], c["starts"], c["kv"], c["scale"], window)
+    tol = kv_util.attn_tolerance(want, mag, c["q"].dtype, c["q"].shape[2])
+    err = (got.double() - want).abs()
+    assert torch.isfinite(got).all()
+    assert bool((err <= tol).all()), f"worst {float((err / tol).max()):.3f} of the tolerance"
+    return got
+
+
+HEADS = ((4, 4, 64), (2, 2, 128), (16, 1, 64), (10, 2, 128), (8, 1, 256), (3, 1, 128), (40, 2, 64), (2, 2, 256))
+
+
+@pytest.mark.parametrize("dtype", ("f16", "bf16"))
+@pytest.mark.parametrize("page", (16, 32, 64, 128, 256))
+@pytest.mark.parametrize("n_q,n_kv,hd", HEADS)
+def test_attn_single_tokens(n_q, n_kv, hd, page, dtype):
+    lens = [(1, m) for m in (1, 2, 15, 16, 17, 31, 33, 64, 127, 300, 517)]
+    announce(f"kv attn single tokens heads={n_q}/{n_kv} hd={hd} page={page} {dtype}")
+    c = kv_util.attn_case(page + hd, lens, n_q, n_kv, hd, page, dtype)
+    kv_util.past_end(c, math.nan)
+    check_attn(c)
+
+
+@pytest.mark.parametrize("window", (0, 1, 20, 150))
+@pytest.mark.parametrize("n_q,n_kv,hd,page,dtype", [(4, 4, 64, 16, "f16"), (2, 2, 128, 64, "bf16"), (16, 1, 64, 32, "bf16"),
+                                                    (10, 2, 128, 16, "f16"), (8, 1, 256, 256, "f16"), (2, 2, 256, 16, "bf16")])
+def test_attn_ragged_chunks(n_q, n_kv, hd, page, dtype, window):
+    """Prompts without a past, chunks behind one, drafts and single tokens in one call."""
+    lens = [(1, 70), (5, 5), (0, 40), (33, 90), (2, 259), (130, 130), (1, 1), (47, 300), (0, 0), (64, 64)]
+    announce(f"kv attn ragged heads={n_q}/{n_kv} hd={hd} page={page} {dtype} window={window}")
+    c = kv_util.attn_case(window + hd, lens, n_q, n_kv, hd, page, dtype)
+    kv_util.past_end(c, math.nan)
+    check_attn(c, window, wide=True)
+
+
+@pytest.mark.parametrize("n_q,n_kv,hd,page,dtype", [(4, 4, 64, 64, "bf16"), (2, 2, 128, 128, "f16"), (16, 1, 64, 16, "f16"),
+                                                    (8, 1, 256, 32, "bf16"), (10, 2, 128, 16, "bf16")])
+def test_attn_chunk_of_many_tiles(n_q, n_kv, hd, page, dtype):
+    lens = [(200, 1000), (321, 321), (1, 900), (257, 640)]
+    announce(f"kv attn chunk heads={n_q}/{n_kv} hd={hd} page={page} {dtype}")
+    c = kv_util.attn_case(hd, lens, n_q, n_kv, hd, page, dtype)
+    kv_util.past_end(c, math.inf)
+    check_attn(c)
+    check_attn(c, 100)
+
+
+@pytest.mark.parametrize("n_q,n_kv,hd,page,dtype,window", [
+    (8, 2, 64, 16, "f16", 0), (4, 1, 128, 32, "bf16", 0), (2, 1, 256, 64, "f16", 0), (16, 1, 64, 256, "bf16", 0),
+    (2, 2, 128, 16, "f16", 2500), (5, 1, 128, 16, "bf16", 3000)])
+def test_attn_long_ranges(n_q, n_kv, hd, page, dtype, window):
+    """Key ranges that are cut and joined, for single tokens and for drafts of several."""
+    for lens in ([(1, 4097), (1, 3), (1, 2900)], [(5, 4000), (3, 513), (1, 1)]):
+        announce(f"kv attn long heads={n_q}/{n_kv} hd={hd} page={page} {dtype} window={window} lens={lens}")
+        c = kv_util.attn_case(hd + page, lens, n_q, n_kv, hd, page, dtype)
+        kv_util.past_end(c, math.nan)
+        got = check_attn(c, window)
+        assert torch.equal(got, attn(c, window)), "the result depends on timing"
+        # bounds looser than the lengths change the grid, not the values
+        check_attn(c, window, max_q=70, max_kv=9000)
+
+
+def test_attn_many_requests():
+    lens = [(1, 1 + 37 * r % 200) for r in range(300)]
+    announce("kv attn 300 requests")
+    c = kv_util.attn_case(1, lens, 2, 1, 64, 16, "f16")
+    check_attn(c)
+    c = kv_util.attn_case(2, [(r % 4, max(r % 4, 7 * r % 90)) for r in range(150)], 4, 2, 64, 16, "bf16")
+    check_attn(c)
+
+
+@pytest.mark.parametrize("bad", (math.nan, math.inf, -math.inf))
+@pytest.mark.parametrize("n_q,n_kv,hd,page,dtype", [(4, 4, 64, 16, "f16"), (8, 1, 128, 64, "bf16"), (2, 1, 256, 32, "f16")])
+def test_attn_masked_places_have_no_effect(n_q, n_kv, hd, page, dtype, bad):
+    """Infinite and NaN keys and values: tokens that do not see them come out as if they were zero."""
+    for lens, window in (([(90, 200), (3, 45)], 0), ([(90, 200), (1, 190)], 33), ([(300, 700)], 0), ([(300, 700)], 70)):
+        announce(f"kv attn masked {bad} heads={n_q}/{n_kv} hd={hd} page={page} {dtype} lens={lens} window={window}")
+        c = kv_util.attn_case(7, lens, n_q, n_kv, hd, page, dtype)
+        kv_util.past_end(c, bad)
+        m = c["kv"][0]
+        spots = (m - 40, m - 41, m - 7, m - lens[0][0] // 2, 100)
+        seen_by = torch.zeros(lens[0][0], dtype=torch.bool)
+        for j in spots:
+            pos = torch.arange(m - lens[0][0], m)
+            seen_by |= (pos >= j) & ((pos - j < window) if window else torch.ones_like(pos, dtype=torch.bool))
+            for t in ("k", "v"):
+                x = c[t][c["table"][0][j // page]]
+                (x[:, j % page] if t == "k" else x[:, :, j % page]).zero_()
+        want, mag = kv_util.attn_reference(c["q"], c["k"], c["v"], c["table"], c["starts"], c["kv"], c["scale"], window)
+        tol = kv_util.attn_tolerance(want, mag, c["q"].dtype, hd)
+        for which in ("k", "v"):
+            d = dict(c, k=c["k"].clone(), v=c["v"].clone())
+            for j in spots:
+                x = d[which][c["table"][0][j // page]]
+                if which == "k":
+                    x[:, j % page] = bad
+                else:
+                    x[:, ::3, j % page] = bad
+            got = attn(d, window)
+            for t in range(lens[0][0]):
+                if not seen_by[t]:
+                    assert bool(((got[t].double() - want[t]).abs() <= tol[t]).all()), (which, t)
+            if which == "v":
+                clean = torch.arange(hd) % 3 != 0              # columns of V without the bad values
+                e = (got[: lens[0][0]].double() - want[: lens[0][0]]).abs()
+                assert bool((e[..., clean] <= tol[: lens[0][0]][..., clean]).all())
+                # a token that sees such a value passes it on
+                assert not torch.isfinite(got[lens[0][0] - 1][:, 0]).any() or not bool(seen_by[-1])
+
+
+def test_attn_rows_without_keys():
+    """No keys at all, fewer keys than new tokens, and table entries out of range."""
+    announce("kv attn rows without keys")
+    c = kv_util.attn_case(9, [(3, 0), (6, 2), (1, 40), (20, 100), (1, 600)], 4, 2, 64, 16, "bf16")
+    kv_util.past_end(c, math.nan)
+    c["table"][3][2], c["table"][3][5] = -1, c["k"].shape[0]
+    c["table"][4][0], c["table"][4][7], c["table"][4][8] = 2 ** 31 - 1, -2 ** 31, -1
+    got = check_attn(c)
+    assert got[:7].abs().max() == 0
+    c["table"][2] = [-1] * len(c["table"][2])
+    got = check_attn(c)
+    assert got[9].abs().max() == 0
+
+
+def test_attn_extreme_scores():
+    """Scores far apart: one key carries everything; equal large scores share; the range is not exceeded."""
+    for dtype in ("f16", "bf16"):
+        announce(f"kv attn extreme {dtype}")
+        c = kv_util.attn_case(3, [(1, 300), (40, 300)], 2, 1, 64, 32, dtype)
+        c["q"] *= 40
+        want, mag = kv_util.attn_reference(c["q"], c["k"], c["v"], c["table"], c["starts"], c["kv"], c["scale"], 0)
+        got = attn(c)
+        tol = kv_util.attn_tolerance(want, mag, c["q"].dtype, 64, partial=8.0 * 40)
+        assert bool(((got.double() - want).abs() <= tol).all())
+        c["q"].zero_()
+        check_attn(c)
+
+
+def test_attn_bounds_cut_lengths():
+    """New tokens past max_q are not written; keys past max_kv are not read."""
+    announce("kv attn bounds")
+    c = kv_util.attn_case(4, [(1, 300), (9, 200)], 4, 4, 64, 16, "f16")
+    got = attn(c, max_q=4, max_kv=300)
+    assert bool((got[5:] == 7.0).all())
+    want, mag = kv_util.attn_reference(c["q"], c["k"], c["v"], c["table"], c["starts"], c["kv"], c["scale"], 0)
+    tol = kv_util.attn_tolerance(want, mag, torch.float16, 64)
+    assert bool(((got.double() - want).abs()[:5] <= tol[:5]).all())
+    d = kv_util.attn_case(5, [(1, 300)], 4, 4, 64, 16, "f16")
+    got = attn(d, max_kv=150)
+    want, mag = kv_util.attn_reference(d["q"], d["k"], d["v"], d["table"], [0, 1], [150], d["scale"], 0)
+    assert bool(((got.double() - want).abs() <= kv_util.attn_tolerance(want, mag, torch.float16, 64)).all())
+
+
+def test_attn_row_ranges_out_of_bounds():
+    """A request whose rows lie outside the packed queries is left out; the others are computed."""
+    announce("kv attn row ranges")
+    c = kv_util.attn_case(6, [(2, 30), (3, 50)], 2, 2, 64, 16, "f16")
+    want, mag = kv_util.attn_reference(c["q"], c["k"], c["v"], c["table"], c["starts"], c["kv"], c["scale"], 0)
+    tol = kv_util.attn_tolerance(want, mag, torch.float16, 64)
+    for starts, ok in (([0, 2, 9], slice(0, 2)), ([-4, 2, 5], slice(2, 5)), ([0, 2, 1], slice(0, 2))):
+        d = dict(c, starts=starts)
+        got = attn(d, max_q=3)
+        assert bool(((got.double() - want).abs()[ok] <= tol[ok]).all())
+        rest = torch.ones(5, dtype=torch.bool)
+        rest[ok] = False
+        assert bool((got[rest] == 7.0).all())
+
+
+def test_attn_offsets_past_32_bits():
+    """A pool of more than 2^32 elements: pages at its end are read and written in their place."""
+    page, n_kv, hd = 256, 8, 256
+    n_pages = (1 << 32) // (page * n_kv * hd) + 40
+    announce(f"kv attn pool of {n_pages} pages")
+    c = kv_util.attn_case(8, [(1, 700), (3, 300)], 8, 8, hd, page, "bf16")
+    small = c["k"].shape[0]
+    k = torch.zeros((n_pages, n_kv, page, hd), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros((n_pages, n_kv, hd, page), dtype=torch.bfloat16, device="cuda")
+    at = n_pages - small
+    cache = pi.make_kv_cache(k, v)
+    rows = small * page
+    kt = c["k"].transpose(1, 2).reshape(rows, n_kv, hd).cuda()
+    vt = c["v"].permute(0, 3, 1, 2).reshape(rows, n_kv, hd).cuda()
+    pi.pi_kv_append(cache, kt, vt, torch.arange(rows, dtype=torch.int32, device="cuda") + at * page)
+    table = [[p + at if p >= 0 else p for p in row] for row in c["table"]]
+    batch = pi.make_kv_batch(dev(table), dev(c["starts"]), dev(c["kv"]), max_q=3, max_kv=700)
+    out = torch.empty(c["q"].shape, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(pi.pi_kv_attn_workspace_bytes(cache, batch, 4, 8), dtype=torch.uint8, device="cuda")
+    pi.pi_kv_attn(cache, batch, c["q"].cuda(), out, ws, scale=c["scale"])
+    torch.cuda.synchronize()
+    assert torch.equal(k[at:].cpu(), c["k"]) and torch.equal(v[at:].cpu(), c["v"]) and not bool(k[:at].any())
+    check_attn(c, got=out.cpu())
+
+
+# ------------------------------------------------------------------------------ together
+
+def test_steps_in_a_replayed_graph_on_another_stream():
+    """Tables, append and attention captured once and replayed with new lengths, against eager calls on
+    copies of the same state and against the reference."""
+    n, page, max_pages, n_q, n_kv, hd, max_tokens, n_pages = 6, 16, 20, 4, 2, 64, 64, 90
+    gen = torch.Generator().manual_seed(1)
+    rng = random.Random(1)
+    announce("kv steps in a graph")
+
+    def state():
+        ints = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+        st = dict(cached=ints(n), fresh=ints(n), ring=torch.arange(n_pages, dtype=torch.int32, device="cuda"),
+                  pool=dev([3, n_pages]), table=torch.full((n, max_pages), -1, dtype=torch.int32, device="cuda"),
+                  q_start=ints(n + 1), kv_len=ints(n), slots=ints(max_tokens), counts=ints(4),
+                  k=torch.zeros((n_pages, n_kv, page, hd), dtype=torch.float16, device="cuda"),
+                  v=torch.zeros((n_pages, n_kv, hd, page), dtype=torch.float16, device="cuda"),
+                  qkv=torch.zeros((max_tokens, n_q + 2 * n_kv, hd), dtype=torch.float16, device="cuda"),
+                  out=torch.zeros((max_tokens, n_q, hd), dtype=torch.float16, device="cuda"))
+        st["tables"] = pi.make_kv_tables(st["cached"], st["fresh"], st["ring"], st["pool"], st["table"], page, st["q_start"],
+                                         st["kv_len"], st["cached"], st["slots"], st["pool"], st["counts"])
+        st["cache"] = pi.make_kv_cache(st["k"], st["v"])
+        st["batch"] = pi.make_kv_batch(st["table"], st["q_start"], st["kv_len"], max_q=24, max_kv=max_pages * page)
+        st["ws"] = torch.empty(pi.pi_kv_attn_workspace_bytes(st["cache"], st["batch"], max_tokens, n_q), dtype=torch.uint8,
+                               device="cuda")
+        return st
+
+    def step(st, stream=None):
+        pi.pi_kv_step(st["tables"], stream)
+        pi.pi_kv_append(st["cache"], st["qkv"][:, n_q: n_q + n_kv], st["qkv"][:, n_q + n_kv:], st["slots"], stream)
+        pi.pi_kv_attn(st["cache"], st["batch"], st["qkv"][:, :n_q], st["out"], st["ws"], scale=0.125, stream=stream)
+
+    a, b = state(), state()
+    side = torch.cuda.Stream()
+    step(a)                                   # no tokens: builds nothing, changes nothing
+    step(b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(a)
+    for it in range(12):
+        fresh = [rng.choice((1, 1, 1, 0, rng.randint(1, 24), -1)) for _ in range(n)] if it else [5, 20, 1, 0, 7, 3]
+        while sum(max(f, 0) for f in fresh) > max_tokens:
+            fresh = [min(f, 5) for f in fresh]
+        qkv = torch.randn((max_tokens, n_q + 2 * n_kv, hd), generator=gen).half().cuda()
+        for st in (a, b):
+            st["fresh"].copy_(dev(fresh))
+            st["qkv"].copy_(qkv)
+        torch.cuda.synchronize()
+        graph.replay()
+        step(b, side)
+        torch.cuda.synchronize()
+        for name in ("cached", "ring", "pool", "table", "q_start", "kv_len", "slots", "counts", "k", "v", "out"):
+            assert torch.equal(a[name], b[name]), (it, name)
+        rows = int(a["counts"][0])
+        want, mag = kv_util.attn_reference(a["qkv"][:rows, :n_q].cpu(), a["k"].cpu(), a["v"].cpu(), a["table"].tolist(),
+                                           a["q_start"].tolist(), a["kv_len"].tolist(), 0.125, 0)
+        tol = kv_util.attn_tolerance(want, mag, torch.float16, hd)
+        assert bool(((a["out"][:rows].cpu().double() - want).abs() <= tol).all()), it
