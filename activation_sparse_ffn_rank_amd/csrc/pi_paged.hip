@@ -12,7 +12,8 @@ using namespace pik;
 
 constexpr int kMaxHeads = 1024;
 // Key ranges are cut so that about this many workgroups share the work of all requests.
-constexpr int kSplitTarget = 1024;
+constexpr int kSplitTarget = 1024;        // k_kv_rows
+constexpr int kSplitTargetWide = 512;     // k_kv_tile
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -58,40 +59,78 @@ int check_strides(const void *p, int64_t ts, int64_t hs) {
     return PI_OK;
 }
 
+// One launch over the requests of row_min .. row_max query rows per kv head, TR rows per workgroup.
 struct AttnGeom {
-    int tiles;       // row tiles per kv head, at most
+    int tiles;       // row tiles per kv head, at most; 0: no launch
     int items;       // items per kv head, at most
     int target;      // split target, 0: no key range is cut
     size_t part;     // bytes of the split items' partial sums
 };
 
-AttnGeom attn_geom(const pi_kv_cache *c, const pi_kv_batch *b, int total_q, int n_q) {
+AttnGeom attn_geom(const pi_kv_cache *c, const pi_kv_batch *b, int total_q, int n_q, int TR, int row_min, int row_max,
+                   int split_target) {
     AttnGeom g{};
-    const int64_t group = n_q / c->n_kv;
-    const int64_t by_rows = total_q * group / kKvRowTile + std::min(b->n_req, total_q);
-    const int64_t by_req = b->n_req * ((std::min(b->max_q, total_q) * group + kKvRowTile - 1) / kKvRowTile);
+    const int64_t group = n_q / c->n_kv, rows = std::min(b->max_q, total_q) * group;
+    if (rows < row_min) return g;
+    // requests that can have row_min rows or more, and their tiles
+    const int64_t reqs = std::min<int64_t>(b->n_req, std::max<int64_t>(total_q * group / row_min, 1));
+    const int64_t by_rows = total_q * group / TR + reqs;
+    const int64_t by_req = reqs * ((std::min<int64_t>(rows, row_max) + TR - 1) / TR);
     g.tiles = (int)std::min(by_rows, by_req);
     g.items = g.tiles;
     // enough row tiles to fill the chip, or too few keys for two items: nothing is cut
-    if ((int64_t)g.tiles * c->n_kv < kSplitTarget && b->max_kv > kKvMinChunk) {
-        g.target = kSplitTarget;
-        g.items += kSplitTarget / c->n_kv + 2;      // 2: the device sums the work in fp32
-        g.part = (size_t)g.items * c->n_kv * (16 * c->head_dim + 32) * sizeof(float);
+    if ((int64_t)g.tiles * c->n_kv < split_target && b->max_kv > kKvMinChunk) {
+        g.target = split_target;
+        g.items += split_target / c->n_kv + 2;      // 2: the device sums the work in fp32
+        g.part = (size_t)g.items * c->n_kv * TR * (c->head_dim + 2) * sizeof(float);
     }
     return g;
 }
 
-template <class T, int HD>
-int launch_attn(const KvAttnArgs &a, const AttnGeom &g, hipStream_t st) {
-    hipLaunchKernelGGL((k_kv_rows<T, HD>), dim3((uint32_t)g.items * a.n_kv), dim3(256), 0, st, a);
-    if (hipGetLastError() != hipSuccess) return PI_ERR_HIP;
+struct AttnPlan {
+    AttnGeom rows, tile;
+    size_t bytes;
+};
+AttnPlan attn_plan(const pi_kv_cache *c, const pi_kv_batch *b, int total_q, int n_q) {
+    AttnPlan p{};
+    p.rows = attn_geom(c, b, total_q, n_q, kKvRowTile, 1, kKvRowTile, kSplitTarget);
+    p.tile = attn_geom(c, b, total_q, n_q, kKvWideTile, kKvRowTile + 1, INT32_MAX, kSplitTargetWide);
+    p.bytes = std::max<size_t>(p.rows.part + p.tile.part, 16);
+    return p;
+}
+
+template <class T, int HD, int TR>
+int launch_join(const KvAttnArgs &a, const AttnGeom &g, hipStream_t st) {
     if (!g.target) return PI_OK;
-    hipLaunchKernelGGL((k_kv_join<T, HD>), dim3((uint32_t)g.tiles * a.n_kv), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((k_kv_join<T, HD, TR>), dim3((uint32_t)g.tiles * a.n_kv * (TR / 16)), dim3(256), 0, st, a);
     return hipGetLastError() == hipSuccess ? PI_OK : PI_ERR_HIP;
 }
 
+template <class T, int HD>
+int launch_attn(KvAttnArgs a, const AttnPlan &p, hipStream_t st) {
+    float *const ws = a.part;
+    if (p.tile.tiles) {
+        a.row_min = kKvRowTile + 1, a.row_max = INT32_MAX, a.split_target = p.tile.target, a.items = p.tile.items;
+        const dim3 grid((uint32_t)a.items * a.n_kv);
+        if ((1 << a.page_log) < KvTile<HD>::kKeys)
+            hipLaunchKernelGGL((k_kv_tile<T, HD, true>), grid, dim3(256), 0, st, a);
+        else
+            hipLaunchKernelGGL((k_kv_tile<T, HD, false>), grid, dim3(256), 0, st, a);
+        if (hipGetLastError() != hipSuccess) return PI_ERR_HIP;
+        if (int rc = launch_join<T, HD, kKvWideTile>(a, p.tile, st)) return rc;
+    }
+    if (p.rows.tiles) {
+        a.part = ws + p.tile.part / sizeof(float);
+        a.row_min = 1, a.row_max = kKvRowTile, a.split_target = p.rows.target, a.items = p.rows.items;
+        hipLaunchKernelGGL((k_kv_rows<T, HD>), dim3((uint32_t)a.items * a.n_kv), dim3(256), 0, st, a);
+        if (hipGetLastError() != hipSuccess) return PI_ERR_HIP;
+        if (int rc = launch_join<T, HD, kKvRowTile>(a, p.rows, st)) return rc;
+    }
+    return PI_OK;
+}
+
 template <class T>
-int launch_attn_hd(int hd, const KvAttnArgs &a, const AttnGeom &g, hipStream_t st) {
+int launch_attn_hd(int hd, const KvAttnArgs &a, const AttnPlan &g, hipStream_t st) {
     if (hd == 64) return launch_attn<T, 64>(a, g, st);
     if (hd == 128) return launch_attn<T, 128>(a, g, st);
     return launch_attn<T, 256>(a, g, st);
@@ -138,7 +177,7 @@ extern "C" int pi_kv_append(const pi_kv_cache *cache, const void *k, int64_t k_t
 
 extern "C" size_t pi_kv_attn_workspace_bytes(const pi_kv_cache *cache, const pi_kv_batch *batch, int32_t total_q, int32_t n_q) {
     if (check_cache(cache) || check_batch(batch) || check_rows(cache, total_q, n_q)) return 0;
-    return std::max<size_t>(attn_geom(cache, batch, total_q, n_q).part, 16);
+    return attn_plan(cache, batch, total_q, n_q).bytes;
 }
 
 extern "C" int pi_kv_attn(const pi_kv_cache *cache, const pi_kv_batch *batch, const void *q, int64_t q_token_stride,
@@ -151,15 +190,14 @@ extern "C" int pi_kv_attn(const pi_kv_cache *cache, const pi_kv_batch *batch, co
     if (window < 0 || !(scale > 0.f) || !std::isfinite(scale)) return PI_ERR_SHAPE;
     if ((rc = check_strides(q, q_token_stride, q_head_stride)) || (rc = check_strides(out, out_token_stride, out_head_stride)))
         return rc;
-    const AttnGeom g = attn_geom(cache, batch, total_q, n_q);
-    if (!ws || ws_bytes < std::max<size_t>(g.part, 16)) return PI_ERR_WORKSPACE;
+    const AttnPlan g = attn_plan(cache, batch, total_q, n_q);
+    if (!ws || ws_bytes < g.bytes) return PI_ERR_WORKSPACE;
     if (!aligned16(ws)) return PI_ERR_ALIGN;
     if (total_q == 0) return PI_OK;
     KvAttnArgs a{};
     a.n_pages = cache->n_pages, a.n_kv = cache->n_kv, a.page_log = page_log(cache->page);
     a.n_req = batch->n_req, a.max_pages = batch->max_pages, a.max_q = batch->max_q, a.max_kv = batch->max_kv;
     a.total_q = total_q, a.n_q = n_q, a.group = n_q / cache->n_kv, a.window = window;
-    a.split_target = g.target, a.items = g.items;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.table_stride = batch->table_stride;
     a.q_ts = q_token_stride, a.q_hs = q_head_stride, a.o_ts = out_token_stride, a.o_hs = out_head_stride;

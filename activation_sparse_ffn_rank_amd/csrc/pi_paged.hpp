@@ -21,6 +21,7 @@ namespace pik {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 struct KvF16 {
     typedef f16 e;
@@ -35,6 +36,9 @@ struct KvF16 {
     static __device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
     }
+    static __device__ __forceinline__ f32x16 mfma32(uint4 a, uint4 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+    }
 };
 
 struct KvBf16 {
@@ -46,6 +50,9 @@ struct KvBf16 {
     static constexpr float kLag = 6.f;
     static __device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f32x16 mfma32(uint4 a, uint4 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
     }
 };
 
@@ -263,6 +270,7 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppendArgs a) {
 struct KvAttnArgs {
     int n_pages, n_kv, page_log;
     int n_req, max_pages, max_q, max_kv, total_q, n_q, group, window;
+    int row_min, row_max;             // requests with this many query rows per kv head; the others are left to another launch
     int split_target;                 // 0: key ranges are not cut
     int items;                        // items per kv head that the workspace and the grid hold
     float scale_log2;                 // scale / ln 2, > 0: weights are powers of two
@@ -270,7 +278,7 @@ struct KvAttnArgs {
     const uint16_t *k, *v, *q;
     const int *table, *q_start, *kv_len;
     uint16_t *out;
-    float *part;                      // per split item: O^T [HD/16][64 lanes][4], then max [16], sum [16]
+    float *part;                      // per split item of TR rows: weighted sums [TR][HD], reference [TR], sum of weights [TR]
 };
 
 // Rows and keys of request r: the rows of one kv head are (token, query head of the group), token
@@ -288,15 +296,18 @@ __device__ __forceinline__ KvReq kv_req(const KvAttnArgs &a, int r) {
     x.n = ok ? q1 - q0 : 0;
     x.m = max(a.kv_len[r], 0);
     x.rows = min(x.n, a.max_q) * a.group;
+    if (x.rows < a.row_min || x.rows > a.row_max) x.rows = 0;
     x.hi = (int)min((int64_t)min(x.m, a.max_kv), (int64_t)a.max_pages << a.page_log);
     x.lo = a.window ? min(max(x.m - x.n - a.window + 1, 0), x.hi) & ~63 : 0;
     return x;
 }
 
 constexpr int kKvRowTile = 16;          // query rows of a k_kv_rows workgroup
+constexpr int kKvWideTile = 128;        // ... and of a k_kv_tile workgroup
 constexpr int kKvMinChunk = 256;        // keys of a split item, at least
 
-// Keys of one split item, from the sum over all requests of row tiles x keys.
+// Keys of one split item, from the sum over all requests of row tiles (of TR rows) x keys.
+template <int TR>
 __device__ __forceinline__ int kv_chunk(const KvAttnArgs &a, int lane) {
     if (!a.split_target) return 0x40000000;
     float sum = 0.f;
@@ -304,7 +315,7 @@ __device__ __forceinline__ int kv_chunk(const KvAttnArgs &a, int lane) {
         float x = 0.f;
         if (r0 + lane < a.n_req) {
             const KvReq q = kv_req(a, r0 + lane);
-            x = (float)((q.rows + kKvRowTile - 1) / kKvRowTile) * (float)(q.hi - q.lo);
+            x = (float)((q.rows + TR - 1) / TR) * (float)(q.hi - q.lo);
         }
         sum += wave_sum(x);
     }
@@ -317,7 +328,7 @@ struct KvItem {
     int r, tile, split, splits;     // r < 0: there is no such item
     KvReq q;
 };
-template <bool JOIN>                // JOIN: items are row tiles, `first` receives the first split item
+template <int TR, bool JOIN>        // JOIN: items are row tiles, `first` receives the first split item
 __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, int chunk, int lane, int *first) {
     KvItem it;
     it.r = -1;
@@ -327,7 +338,7 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, int chu
         int tiles = 0, splits = 1;
         if (r0 + lane < a.n_req) {
             q = kv_req(a, r0 + lane);
-            tiles = (q.rows + kKvRowTile - 1) / kKvRowTile;
+            tiles = (q.rows + TR - 1) / TR;
             splits = max((q.hi - q.lo + chunk - 1) / chunk, 1);
         }
         const int items = tiles * splits, mine = JOIN ? tiles : items;
@@ -380,7 +391,7 @@ __global__ __launch_bounds__(256) void k_kv_rows(KvAttnArgs a) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = lane & 15, g = lane >> 4;
     const int h = blockIdx.x % a.n_kv, want = blockIdx.x / a.n_kv;
-    const KvItem it = kv_item<false>(a, want, kv_chunk(a, lane), lane, nullptr);
+    const KvItem it = kv_item<kKvRowTile, false>(a, want, kv_chunk<kKvRowTile>(a, lane), lane, nullptr);
     if (it.r < 0) return;
     const KvReq &rq = it.q;
 
@@ -403,7 +414,7 @@ __global__ __launch_bounds__(256) void k_kv_rows(KvAttnArgs a) {
     const int all_hi = min(pos_a + 1, rq.hi), all_lo = a.window ? max(pos_b - a.window + 1, 0) : 0;
     int lo = max(tile_lo & ~31, rq.lo), hi = tile_hi;
     if (it.splits > 1) {
-        const int chunk = kv_chunk(a, lane), from = rq.lo + it.split * chunk;
+        const int chunk = kv_chunk<kKvRowTile>(a, lane), from = rq.lo + it.split * chunk;
         lo = max(lo, from);
         hi = min(hi, from + chunk);
     }
@@ -575,50 +586,352 @@ __global__ __launch_bounds__(256) void k_kv_rows(KvAttnArgs a) {
                                                                  kv_pack<T>(st.o[t][2] * inv, st.o[t][3] * inv));
         return;
     }
-    float *const pt = a.part + (int64_t)blockIdx.x * (16 * HD + 32);
+    float *const pt = a.part + (int64_t)blockIdx.x * (kKvRowTile * (HD + 2));
     if (row < rq.rows) {
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) reinterpret_cast<f32x4 *>(pt)[t * 64 + lane] = st.o[t];
+        for (int t = 0; t < kTiles; ++t) *reinterpret_cast<f32x4 *>(pt + col * HD + 16 * t + 4 * g) = st.o[t];
         if (g == 0) {
-            pt[16 * HD + col] = ref;
-            pt[16 * HD + 16 + col] = sum;
+            pt[kKvRowTile * HD + col] = ref;
+            pt[kKvRowTile * (HD + 1) + col] = sum;
         }
     }
 }
 
-// Joins the split items of one row tile of one kv head, in the order of their key ranges.
-template <class T, int HD>
-__global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
-    constexpr int kTiles = HD / 16;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
+// One workgroup: one item of TR = 128 query rows of one kv head, 32 of them per wave, over one key
+// range, KT keys at a time.  K and V of a block go from the pages to LDS without passing registers
+// (16 bytes per lane), the next block's while this one is computed; the waves read them from there
+// as MFMA operands.  Inside a row of either tile the 16-byte units are permuted by the row's number, on
+// the way in, so that the 16 lanes that read the same unit of 16 rows find them in 16 bank groups.
+// The products are those of k_kv_rows on 32x32x16 MFMA: tile row 16s + 8u + 4h + v is key 16s + 8h + 4u
+// + v, so that lane half h holds keys 16s + 8h .. +7 of its query row in accumulators 8s .. 8s+7.
+template <int HD>
+struct KvTile {
+    static constexpr int kKeys = HD == 256 ? 32 : 64;      // 64 KB of LDS for both buffers at most
+    static constexpr int kUnitsK = HD / 8, kUnitsV = kKeys / 8;
+    static constexpr int kLoads = kKeys * HD * 2 / 1024 / 4;     // 1 KB loads per wave and operand
+    static constexpr int kBytes = kKeys * HD * 2;                // of one operand's tile
+    static __device__ __forceinline__ int swz_k(int key) { return kUnitsK >= 16 ? key & 15 : (key >> 1) & 7; }
+    static __device__ __forceinline__ int swz_v(int d) { return kUnitsV == 8 ? (d >> 1) & 7 : (d >> 2) & 3; }
+};
+
+// 64 lanes x 16 bytes from base + off (per lane) to 1 KB of LDS at byte address `lds`.  The compiler
+// does not see the load in flight: kv_lds_wait before the barrier after which the bytes are read.
+__device__ __forceinline__ void kv_lds_load(const uint16_t *base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void kv_lds_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+template <class T, int HD, bool SMALL>      // SMALL: pages of fewer positions than a block has keys
+__global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a) {
+    typedef KvTile<HD> L;
+    constexpr int KT = L::kKeys, kSub = KT / 32, kSteps = HD / 16, kTiles = HD / 32;
+    __shared__ __align__(16) uint16_t s_kv[2][2][L::kBytes / 2];       // [buffer][K, V]
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 31, half = lane >> 5;
     const int h = blockIdx.x % a.n_kv, want = blockIdx.x / a.n_kv;
+    const int chunk = kv_chunk<kKvWideTile>(a, lane);
+    const KvItem it = kv_item<kKvWideTile, false>(a, want, chunk, lane, nullptr);
+    if (it.r < 0) return;
+    const KvReq &rq = it.q;
+    // later rows see more keys: they go first
+    const int tile = (rq.rows + kKvWideTile - 1) / kKvWideTile - 1 - it.tile;
+    const int past = rq.m - rq.n;
+
+    // this lane's query row
+    const int row = tile * kKvWideTile + wave * 32 + col, row_c = min(row, rq.rows - 1);
+    const int tok = row_c / a.group, head = h * a.group + (row_c - tok * a.group);
+    const int pos = past + tok;
+    const int see_hi = min(pos + 1, rq.hi), see_lo = a.window ? max(pos - a.window + 1, 0) : 0;
+    uint4 qf[kSteps];
+    {
+        const uint16_t *qp = a.q + (int64_t)(rq.q0 + tok) * a.q_ts + (int64_t)head * a.q_hs + 8 * half;
+#pragma unroll
+        for (int t = 0; t < kSteps; ++t) qf[t] = ld16(qp + 16 * t);
+    }
+    // keys that some row of the workgroup sees, within the item's chunk
+    const int pos_first = past + tile * kKvWideTile / a.group;
+    const int pos_last = past + (min((tile + 1) * kKvWideTile, rq.rows) - 1) / a.group;
+    int lo = a.window ? max(pos_first - a.window + 1, 0) : 0, hi = min(pos_last + 1, rq.hi);
+    lo = max(lo & ~(KT - 1), rq.lo);
+    if (it.splits > 1) {
+        const int from = rq.lo + it.split * chunk;
+        lo = max(lo, from);
+        hi = min(hi, from + chunk);
+    }
+    // keys that some row of this wave sees, and those that all of them see
+    const int wrow = tile * kKvWideTile + wave * 32;
+    const int pos_a = past + min(wrow, rq.rows - 1) / a.group, pos_b = past + (min(wrow + 32, rq.rows) - 1) / a.group;
+    const bool idle = wrow >= rq.rows;
+    const int wave_hi = idle ? 0 : min(pos_b + 1, rq.hi), wave_lo = a.window ? max(pos_a - a.window + 1, 0) : 0;
+    const int all_hi = min(pos_a + 1, rq.hi), all_lo = a.window ? max(pos_b - a.window + 1, 0) : 0;
+
+    // where this lane's 16 bytes of each load come from, inside a page
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t *)&s_kv[0][0][0];
+    uint32_t off_k[L::kLoads], off_v[L::kLoads];
+    int unit_v[L::kLoads];
+#pragma unroll
+    for (int i = 0; i < L::kLoads; ++i) {
+        const int u = (wave * L::kLoads + i) * 64 + lane;
+        const int key = u / L::kUnitsK, d = u / L::kUnitsV;
+        const int first = (wave * L::kLoads + i) * 64 / L::kUnitsK;
+        off_k[i] = (uint32_t)(((key - first) * HD + 8 * ((u % L::kUnitsK) ^ L::swz_k(key))) * 2);
+        unit_v[i] = (u % L::kUnitsV) ^ L::swz_v(d);
+        off_v[i] = (uint32_t)((d << a.page_log) + (SMALL ? 0 : 8 * unit_v[i])) * 2;
+    }
+
+    const int *const tab = a.table + (int64_t)it.r * a.table_stride;
+    const int page = 1 << a.page_log, held = (rq.hi + page - 1) >> a.page_log;
+    const int64_t page_elems = ((int64_t)a.n_kv << a.page_log) * HD, head_elems = (int64_t)h * HD << a.page_log;
+    int tab0 = 0, ids = 0;
+    bool none = true;                    // no table entries at hand yet
+    // The loads of block kb into buffer buf; returns which of its 16-key groups have no page.
+    auto load = [&](int kb, int buf) -> uint32_t {
+        const int p0 = kb >> a.page_log, p1 = (kb + KT - 1) >> a.page_log;
+        if (none || p1 - tab0 >= 64) {
+            tab0 = p0;
+            ids = tab0 + lane < held ? tab[tab0 + lane] : -1;
+            none = false;
+        }
+        uint32_t dead = 0;
+        const bool bad = (uint32_t)ids >= (uint32_t)a.n_pages;
+        const int id_safe = bad ? 0 : ids;               // something in bounds; its keys are masked
+        const uint64_t bads = __ballot(bad);
+        const uint32_t dst = lds0 + buf * 2 * L::kBytes + wave * L::kLoads * 1024;
+        if (SMALL) {
+#pragma unroll
+            for (int j = 0; j < KT / 16; ++j)
+                if (bads >> (((kb + 16 * j) >> a.page_log) - tab0) & 1) dead |= 1u << j;
+#pragma unroll
+            for (int i = 0; i < L::kLoads; ++i) {
+                const int k0 = kb + (wave * L::kLoads + i) * 64 / L::kUnitsK;
+                const int64_t id = bcast(id_safe, (k0 >> a.page_log) - tab0);
+                kv_lds_load(a.k + id * page_elems + head_elems + (int64_t)(k0 & (page - 1)) * HD, off_k[i], dst + i * 1024);
+            }
+#pragma unroll
+            for (int i = 0; i < L::kLoads; ++i) {
+                // the units of a V^T row come from several pages: 64-bit addresses per lane
+                const int k0 = kb + 8 * unit_v[i];
+                const int64_t id = __shfl(id_safe, (k0 >> a.page_log) - tab0);
+                const uint16_t *src = a.v + id * page_elems + head_elems + (k0 & (page - 1));
+                src = reinterpret_cast<const uint16_t *>(reinterpret_cast<const char *>(src) + off_v[i]);
+                asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src),
+                             "s"(dst + L::kBytes + i * 1024) : "memory", "m0");
+            }
+        } else {
+            const int64_t id = bcast(id_safe, p0 - tab0);
+            if (bads >> (p0 - tab0) & 1) dead = 15u;
+            const uint16_t *const kp = a.k + id * page_elems + head_elems + (int64_t)(kb & (page - 1)) * HD;
+            const uint16_t *const vp = a.v + id * page_elems + head_elems + (kb & (page - 1));
+#pragma unroll
+            for (int i = 0; i < L::kLoads; ++i)
+                kv_lds_load(kp + (wave * L::kLoads + i) * 512, off_k[i], dst + i * 1024);
+#pragma unroll
+            for (int i = 0; i < L::kLoads; ++i) kv_lds_load(vp, off_v[i], dst + L::kBytes + i * 1024);
+        }
+        return dead;
+    };
+
+    f32x16 o[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[t][i] = 0.f;
+    float ref = -INFINITY, sum = 0.f;
+    const int krow = (col & ~12) | (col & 8) >> 1 | (col & 4) << 1;
+
+    uint32_t dead_next = 0;
+    int buf = 0;
+    if (lo < hi) dead_next = load(lo, 0);
+    for (int kb = lo; kb < hi; kb += KT, buf ^= 1) {
+        const uint32_t dead = dead_next;
+        kv_lds_wait();
+        __syncthreads();                 // block kb is in LDS, and every wave is done with the buffer before it
+        if (kb + KT < hi) dead_next = load(kb + KT, buf ^ 1);
+        if (kb >= wave_hi || kb + KT <= wave_lo) continue;
+        const uint16_t *const sk = s_kv[buf][0], *const sv = s_kv[buf][1];
+
+        f32x16 s[kSub];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[u][i] = 0.f;
+            const int key = 32 * u + krow;
+#pragma unroll
+            for (int t = 0; t < kSteps; ++t) {
+                const int unit = (2 * t + half) ^ L::swz_k(key);
+                s[u] = T::mfma32(*reinterpret_cast<const uint4 *>(sk + key * HD + unit * 8), qf[t], s[u]);
+            }
+        }
+        const bool edge = kb < all_lo || kb + KT > all_hi || dead != 0;
+        if (edge) {
+            const int from = see_lo - kb - 8 * half, to = see_hi - kb - 8 * half;
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int e = 32 * u + 16 * (i >> 3) + (i & 7);
+                    if (e < from || e >= to || (dead >> (2 * u + (i >> 3)) & 1)) s[u][i] = -INFINITY;
+                }
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
+        top = top * a.scale_log2 - T::kShift;
+        // The reference moves only when some score of the wave passes it by more than the lag.
+        if (__any(top > ref + T::kLag)) {
+            const float to = fmaxf(fmaxf(top, __shfl_xor(top, 32)), ref);
+            const float f = ref == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ref - to);
+            sum *= f;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) o[t] *= f;
+            ref = to;
+        }
+        const float r = ref == -INFINITY ? 0.f : ref;
+        float part = 0.f;
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][i], a.scale_log2, -r));
+                part += s[u][i];
+            }
+        sum += part;
+        // At an edge: values that no row of the wave sees are cleared (0 x infinity would be NaN); those that
+        // some rows see and others do not, and that are not finite, are cleared too and added row by row.
+        uint64_t drop = 0;
+        auto v_frag = [&](int t, int j) -> uint4 {
+            const int d = 32 * t + col, unit = (2 * j + half) ^ L::swz_v(d);
+            return *reinterpret_cast<const uint4 *>(sv + d * KT + unit * 8);
+        };
+        auto clear = [&](uint4 x, int j) -> uint4 {
+            const uint32_t m = (uint32_t)(drop >> (16 * j + 8 * half)) & 0xffu;
+            auto keep = [&](int b) { return (m >> b & 1 ? 0u : 0xffffu) | (m >> b & 2 ? 0u : 0xffff0000u); };
+            x.x &= keep(0), x.y &= keep(2), x.z &= keep(4), x.w &= keep(6);
+            return x;
+        };
+        if (edge) {
+            for (int e = 0; e < KT; ++e)
+                if (kb + e < wave_lo || kb + e >= wave_hi || (dead >> (e >> 4) & 1)) drop |= 1ull << e;
+            uint64_t odd_keys = 0;
+            if (pos_a != pos_b) {
+#pragma unroll 1
+                for (int j = 0; j < 2 * kSub; ++j) {
+                    uint32_t odd = 0;
+#pragma unroll 1
+                    for (int t = 0; t < kTiles; ++t) {
+                        const uint4 x = clear(v_frag(t, j), j);
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            if ((w[b] & T::kExpMask & 0xffffu) == (T::kExpMask & 0xffffu)) odd |= 1u << (2 * b);
+                            if ((w[b] & T::kExpMask & 0xffff0000u) == (T::kExpMask & 0xffff0000u)) odd |= 2u << (2 * b);
+                        }
+                    }
+                    if (__any(odd != 0)) {
+                        for (int x = 1; x < 32; x <<= 1) odd |= __shfl_xor(odd, x);
+                        odd_keys |= ((uint64_t)(uint32_t)bcast((int)odd, 0) | (uint64_t)(uint32_t)bcast((int)odd, 32) << 8) << (16 * j);
+                    }
+                }
+            }
+            drop |= odd_keys;
+            while (odd_keys) {
+                const int j = __builtin_ctzll(odd_keys);
+                odd_keys &= odd_keys - 1;
+                float mine = 0.f;
+#pragma unroll
+                for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) mine = (32 * u + 16 * (i >> 3) + (i & 7)) == (j & ~8) ? s[u][i] : mine;
+                const float w = __shfl(mine, (j & 8 ? 32 : 0) + col);
+                if (kb + j < see_lo || kb + j >= see_hi) continue;
+                int d0 = 4 * half;
+                asm volatile("" : "+v"(d0));        // its addresses are not worth registers outside this loop
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int d = 32 * t + 8 * (i >> 2) + d0 + (i & 3);
+                        o[t][i] += w * (float)__builtin_bit_cast(typename T::e, sv[d * KT + ((j >> 3) ^ L::swz_v(d)) * 8 + (j & 7)]);
+                    }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2 * kSub; ++j) {
+            const f32x16 &x = s[j >> 1];
+            const int b = 8 * (j & 1);
+            const uint4 pf = make_uint4(kv_pack<T>(x[b], x[b + 1]), kv_pack<T>(x[b + 2], x[b + 3]),
+                                        kv_pack<T>(x[b + 4], x[b + 5]), kv_pack<T>(x[b + 6], x[b + 7]));
+            if (edge) {
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) o[t] = T::mfma32(clear(v_frag(t, j), j), pf, o[t]);
+            } else {
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) o[t] = T::mfma32(v_frag(t, j), pf, o[t]);
+            }
+        }
+    }
+
+    if (row >= rq.rows) return;
+    sum += __shfl_xor(sum, 32);
+    if (it.splits == 1) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        uint16_t *op = a.out + (int64_t)(rq.q0 + tok) * a.o_ts + (int64_t)head * a.o_hs + 4 * half;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<uint2 *>(op + 32 * t + 2 * i) = make_uint2(kv_pack<T>(o[t][i] * inv, o[t][i + 1] * inv),
+                                                                             kv_pack<T>(o[t][i + 2] * inv, o[t][i + 3] * inv));
+        return;
+    }
+    const int prow = wave * 32 + col;
+    // (the items of a request are numbered by it.tile, so the join finds them in the same order)
+    float *const pt = a.part + (int64_t)blockIdx.x * (kKvWideTile * (HD + 2));
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<f32x4 *>(pt + prow * HD + 32 * t + 2 * i + 4 * half) = f32x4{o[t][i], o[t][i + 1], o[t][i + 2], o[t][i + 3]};
+    if (half == 0) {
+        pt[kKvWideTile * HD + prow] = ref;
+        pt[kKvWideTile * (HD + 1) + prow] = sum;
+    }
+}
+
+// Joins the split items of 16 rows of a row tile of one kv head, in the order of their key ranges.
+template <class T, int HD, int TR>
+__global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
+    constexpr int kLanes = HD / 4, kRows = 256 / kLanes;          // threads per row, rows at a time
+    const int lane = threadIdx.x & 63;
+    const int sub = blockIdx.x % (TR / 16), at = blockIdx.x / (TR / 16);
+    const int h = at % a.n_kv, want = at / a.n_kv;
     int first = 0;
-    const KvItem it = kv_item<true>(a, want, kv_chunk(a, lane), lane, &first);
+    const KvItem it = kv_item<TR, true>(a, want, kv_chunk<TR>(a, lane), lane, &first);
     // (row ranges that overlap can name more items than the grid holds; those have no partial sums)
     if (it.r < 0 || it.splits == 1 || first + it.splits > a.items) return;
-    const int row = it.tile * kKvRowTile + col;
-    if (row >= it.q.rows) return;
-    const int tok = row / a.group, head = h * a.group + (row - tok * a.group);
-    const int64_t stride = (int64_t)a.n_kv * (16 * HD + 32);
-    const float *const pt = a.part + (int64_t)first * stride + (int64_t)h * (16 * HD + 32);
-    float ref = -INFINITY, sum = 0.f;
-    for (int s = 0; s < it.splits; ++s) ref = fmaxf(ref, pt[s * stride + 16 * HD + col]);
-    f32x4 o[(kTiles + 3) / 4];
-#pragma unroll
-    for (int i = 0; i < (kTiles + 3) / 4; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < it.splits; ++s) {
-        const float r = pt[s * stride + 16 * HD + col];
-        const float f = r == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(r - ref);
-        sum += f * pt[s * stride + 16 * HD + 16 + col];
-#pragma unroll
-        for (int i = 0; i < (kTiles + 3) / 4; ++i) o[i] += f * reinterpret_cast<const f32x4 *>(pt + s * stride)[(wave + 4 * i) * 64 + lane];
+    const int tile = TR == kKvRowTile ? it.tile : (it.q.rows + TR - 1) / TR - 1 - it.tile;
+    const int64_t stride = (int64_t)a.n_kv * (TR * (HD + 2));
+    const float *const pt = a.part + (int64_t)first * stride + (int64_t)h * (TR * (HD + 2));
+    const int d = (threadIdx.x % kLanes) * 4;
+    for (int prow = sub * 16 + threadIdx.x / kLanes; prow < sub * 16 + 16; prow += kRows) {
+        const int row = tile * TR + prow;
+        if (row >= it.q.rows) return;
+        float ref = -INFINITY, sum = 0.f;
+        for (int s = 0; s < it.splits; ++s) ref = fmaxf(ref, pt[s * stride + TR * HD + prow]);
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < it.splits; ++s) {
+            const float r = pt[s * stride + TR * HD + prow];
+            const float f = r == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(r - ref);
+            sum += f * pt[s * stride + TR * (HD + 1) + prow];
+            o += f * *reinterpret_cast<const f32x4 *>(pt + s * stride + prow * HD + d);
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int tok = row / a.group, head = h * a.group + (row - tok * a.group);
+        *reinterpret_cast<uint2 *>(a.out + (int64_t)(it.q.q0 + tok) * a.o_ts + (int64_t)head * a.o_hs + d) =
+            make_uint2(kv_pack<T>(o[0] * inv, o[1] * inv), kv_pack<T>(o[2] * inv, o[3] * inv));
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint16_t *op = a.out + (int64_t)(it.q.q0 + tok) * a.o_ts + (int64_t)head * a.o_hs + 4 * g;
-#pragma unroll
-    for (int i = 0; i < (kTiles + 3) / 4; ++i)
-        *reinterpret_cast<uint2 *>(op + 16 * (wave + 4 * i)) =
-            make_uint2(kv_pack<T>(o[i][0] * inv, o[i][1] * inv), kv_pack<T>(o[i][2] * inv, o[i][3] * inv));
 }
 
 }  // namespace pik
