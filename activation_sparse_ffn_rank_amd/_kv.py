@@ -11,7 +11,9 @@ import ctypes
 
 import torch
 
-from ._abi import PI_ERR_DTYPE, PI_ERR_NULL, PI_ERR_SHAPE, PiError, _check, _nbytes, _stream, lib
+from ._abi import PI_ERR_DTYPE, PI_ERR_NULL, PI_ERR_SHAPE, PI_OK, PiError, _check, lib
+
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 PI_KV_F16, PI_KV_BF16 = 1, 2
 PI_KV_MAX_REQ, PI_KV_MAX_TABLE, PI_KV_MAX_TOKENS = 4096, 1 << 17, 1 << 19
@@ -60,13 +62,13 @@ def kv_lib() -> ctypes.CDLL:
     return _kv_lib
 
 
-def _ints(fn: str, t, *shape) -> int:
-    """Address of a contiguous int32 tensor of this shape (-1: any size)."""
+def _ints(fn: str, t, n: int) -> int:
+    """Address of a contiguous int32 tensor [n] (-1: any size)."""
     if t is None:
         raise PiError(fn, PI_ERR_NULL)
     if t.dtype != torch.int32:
         raise PiError(fn, PI_ERR_DTYPE)
-    if t.dim() != len(shape) or any(w not in (-1, n) for w, n in zip(shape, t.shape)) or not t.is_contiguous():
+    if t.dim() != 1 or (n >= 0 and t.shape[0] != n) or not t.is_contiguous():
         raise PiError(fn, PI_ERR_SHAPE)
     return t.data_ptr()
 
@@ -88,12 +90,21 @@ def _rows(fn: str, t, cache: pi_kv_cache) -> tuple[int, int, int, int, int]:
         raise PiError(fn, PI_ERR_NULL)
     if KV_DTYPES.get(t.dtype) != cache.dtype:
         raise PiError(fn, PI_ERR_DTYPE)
-    n, heads, hd = t.shape if t.dim() == 3 else (0, 0, 0)
-    ts, hs, one = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if t.dim() != 3:
+        raise PiError(fn, PI_ERR_SHAPE)
+    n, heads, hd = t.shape
+    ts, hs, one = t.stride()
     if hd != cache.head_dim or one != 1:
         raise PiError(fn, PI_ERR_SHAPE)
     # the stride along an axis of one element is never used
     return t.data_ptr(), ts if n > 1 else heads * hd, hs if heads > 1 else hd, n, heads
+
+
+def _raw_stream(stream, t) -> int:
+    """As ``_abi._stream``, the current stream taken from the tensor's device (a cheaper query)."""
+    if stream is None:
+        return _current_stream(t.device.index or 0) if t.is_cuda else 0
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def make_kv_cache(k_pages: torch.Tensor, v_pages: torch.Tensor) -> pi_kv_cache:
@@ -146,7 +157,7 @@ def make_kv_tables(cached: torch.Tensor, fresh: torch.Tensor, free_ring: torch.T
 
 def pi_kv_step(tables: pi_kv_tables, stream=None) -> None:
     """One step of the block tables: pages for the new tokens, pages of ended requests back, slot map."""
-    _check("pi_kv_step", kv_lib().pi_kv_step(tables, _stream(stream)))
+    _check("pi_kv_step", kv_lib().pi_kv_step(tables, _raw_stream(stream, tables._keep[0])))
 
 
 def pi_kv_append(cache: pi_kv_cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
@@ -156,7 +167,9 @@ def pi_kv_append(cache: pi_kv_cache, k: torch.Tensor, v: torch.Tensor, slots: to
     vp, vt, vh, n_v, heads_v = _rows(fn, v, cache)
     if heads != cache.n_kv or heads_v != heads or n_v != n:
         raise PiError(fn, PI_ERR_SHAPE)
-    _check(fn, kv_lib().pi_kv_append(cache, kp, kt, kh, vp, vt, vh, _ints(fn, slots, n), n, _stream(stream)))
+    rc = kv_lib().pi_kv_append(cache, kp, kt, kh, vp, vt, vh, _ints(fn, slots, n), n, _raw_stream(stream, k))
+    if rc != PI_OK:
+        raise PiError(fn, rc)
 
 
 def pi_kv_attn_workspace_bytes(cache: pi_kv_cache, batch: pi_kv_batch, total_q: int, n_q: int) -> int:
@@ -172,5 +185,7 @@ def pi_kv_attn(cache: pi_kv_cache, batch: pi_kv_batch, q: torch.Tensor, out: tor
     op, ot, oh, n_o, heads_o = _rows(fn, out, cache)
     if n_o != n or heads_o != heads:
         raise PiError(fn, PI_ERR_SHAPE)
-    _check(fn, kv_lib().pi_kv_attn(cache, batch, qp, qt, qh, op, ot, oh, n, heads, scale, window,
-                                   None if ws is None else ws.data_ptr(), 0 if ws is None else _nbytes(ws), _stream(stream)))
+    wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
+    rc = kv_lib().pi_kv_attn(cache, batch, qp, qt, qh, op, ot, oh, n, heads, scale, window, wp, wn, _raw_stream(stream, q))
+    if rc != PI_OK:
+        raise PiError(fn, rc)

@@ -59,74 +59,54 @@ int check_strides(const void *p, int64_t ts, int64_t hs) {
     return PI_OK;
 }
 
-// One launch over the requests of row_min .. row_max query rows per kv head, TR rows per workgroup.
-struct AttnGeom {
-    int tiles;       // row tiles per kv head, at most; 0: no launch
-    int items;       // items per kv head, at most
-    int target;      // split target, 0: no key range is cut
-    size_t part;     // bytes of the split items' partial sums
-};
-
-AttnGeom attn_geom(const pi_kv_cache *c, const pi_kv_batch *b, int total_q, int n_q, int TR, int row_min, int row_max,
-                   int split_target) {
-    AttnGeom g{};
-    const int64_t group = n_q / c->n_kv, rows = std::min(b->max_q, total_q) * group;
-    if (rows < row_min) return g;
-    // requests that can have row_min rows or more, and their tiles
-    const int64_t reqs = std::min<int64_t>(b->n_req, std::max<int64_t>(total_q * group / row_min, 1));
-    const int64_t by_rows = total_q * group / TR + reqs;
-    const int64_t by_req = reqs * ((std::min<int64_t>(rows, row_max) + TR - 1) / TR);
-    g.tiles = (int)std::min(by_rows, by_req);
-    g.items = g.tiles;
-    // enough row tiles to fill the chip, or too few keys for two items: nothing is cut
-    if ((int64_t)g.tiles * c->n_kv < split_target && b->max_kv > kKvMinChunk) {
-        g.target = split_target;
-        g.items += split_target / c->n_kv + 2;      // 2: the device sums the work in fp32
-        g.part = (size_t)g.items * c->n_kv * TR * (c->head_dim + 2) * sizeof(float);
-    }
-    return g;
-}
-
+// Rows per workgroup by the most query rows that a request can have per kv head: single tokens and
+// drafts of small groups go to k_kv_rows, whose waves share out the keys; the rest, and whatever
+// single tokens run beside it, to k_kv_tile.
 struct AttnPlan {
-    AttnGeom rows, tile;
-    size_t bytes;
+    int TR;
+    int tiles;       // row tiles per kv head, at most
+    int items;       // items per kv head, at most
+    int slots;       // split items per kv head, at most
+    int target;      // split target, 0: no key range is cut
+    size_t bytes;    // of the split items' partial sums
 };
+
 AttnPlan attn_plan(const pi_kv_cache *c, const pi_kv_batch *b, int total_q, int n_q) {
     AttnPlan p{};
-    p.rows = attn_geom(c, b, total_q, n_q, kKvRowTile, 1, kKvRowTile, kSplitTarget);
-    p.tile = attn_geom(c, b, total_q, n_q, kKvWideTile, kKvRowTile + 1, INT32_MAX, kSplitTargetWide);
-    p.bytes = std::max<size_t>(p.rows.part + p.tile.part, 16);
+    const int64_t group = n_q / c->n_kv, rows = std::min(b->max_q, total_q) * group, reqs = std::min(b->n_req, total_q);
+    p.TR = rows <= kKvRowTile ? kKvRowTile : kKvWideTile;
+    p.tiles = (int)std::min(total_q * group / p.TR + reqs, reqs * ((rows + p.TR - 1) / p.TR));
+    p.items = p.tiles;
+    p.bytes = 16;
+    // Nothing is cut where there are too few keys for two items, or row tiles to fill the chip many times.
+    const int target = p.TR == kKvRowTile ? kSplitTarget : kSplitTargetWide;
+    if ((int64_t)p.tiles * c->n_kv < 8 * target && b->max_kv > kKvMinChunk) {
+        p.target = target;
+        p.items += target / c->n_kv + 2;             // 2: the device sums the work in fp32
+        p.slots = std::min(p.items, 2 * target / c->n_kv + 4);
+        p.bytes = (size_t)p.slots * c->n_kv * p.TR * (c->head_dim + 2) * sizeof(float);
+    }
     return p;
 }
 
 template <class T, int HD, int TR>
-int launch_join(const KvAttnArgs &a, const AttnGeom &g, hipStream_t st) {
-    if (!g.target) return PI_OK;
-    hipLaunchKernelGGL((k_kv_join<T, HD, TR>), dim3((uint32_t)g.tiles * a.n_kv * (TR / 16)), dim3(256), 0, st, a);
+int launch_join(const KvAttnArgs &a, const AttnPlan &p, hipStream_t st) {
+    if (!p.target) return PI_OK;
+    hipLaunchKernelGGL((k_kv_join<T, HD, TR>), dim3((uint32_t)p.tiles * a.n_kv * (TR / 16)), dim3(256), 0, st, a);
     return hipGetLastError() == hipSuccess ? PI_OK : PI_ERR_HIP;
 }
 
 template <class T, int HD>
-int launch_attn(KvAttnArgs a, const AttnPlan &p, hipStream_t st) {
-    float *const ws = a.part;
-    if (p.tile.tiles) {
-        a.row_min = kKvRowTile + 1, a.row_max = INT32_MAX, a.split_target = p.tile.target, a.items = p.tile.items;
-        const dim3 grid((uint32_t)a.items * a.n_kv);
-        if ((1 << a.page_log) < KvTile<HD>::kKeys)
-            hipLaunchKernelGGL((k_kv_tile<T, HD, true>), grid, dim3(256), 0, st, a);
-        else
-            hipLaunchKernelGGL((k_kv_tile<T, HD, false>), grid, dim3(256), 0, st, a);
-        if (hipGetLastError() != hipSuccess) return PI_ERR_HIP;
-        if (int rc = launch_join<T, HD, kKvWideTile>(a, p.tile, st)) return rc;
-    }
-    if (p.rows.tiles) {
-        a.part = ws + p.tile.part / sizeof(float);
-        a.row_min = 1, a.row_max = kKvRowTile, a.split_target = p.rows.target, a.items = p.rows.items;
-        hipLaunchKernelGGL((k_kv_rows<T, HD>), dim3((uint32_t)a.items * a.n_kv), dim3(256), 0, st, a);
-        if (hipGetLastError() != hipSuccess) return PI_ERR_HIP;
-        if (int rc = launch_join<T, HD, kKvRowTile>(a, p.rows, st)) return rc;
-    }
-    return PI_OK;
+int launch_attn(const KvAttnArgs &a, const AttnPlan &p, hipStream_t st) {
+    const dim3 grid((uint32_t)p.items * a.n_kv);
+    if (p.TR == kKvRowTile)
+        hipLaunchKernelGGL((k_kv_rows<T, HD>), grid, dim3(256), 0, st, a);
+    else if ((1 << a.page_log) < KvTile<HD>::kKeys)
+        hipLaunchKernelGGL((k_kv_tile<T, HD, true>), grid, dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_kv_tile<T, HD, false>), grid, dim3(256), 0, st, a);
+    if (hipGetLastError() != hipSuccess) return PI_ERR_HIP;
+    return p.TR == kKvRowTile ? launch_join<T, HD, kKvRowTile>(a, p, st) : launch_join<T, HD, kKvWideTile>(a, p, st);
 }
 
 template <class T>
@@ -161,10 +141,10 @@ extern "C" int pi_kv_append(const pi_kv_cache *cache, const void *k, int64_t k_t
                             void *stream) {
     int rc = check_cache(cache);
     if (rc) return rc;
-    if (!k || !v || !slots) return PI_ERR_NULL;
     if (n_tokens < 0 || n_tokens > PI_KV_MAX_TOKENS) return PI_ERR_SHAPE;
+    if (n_tokens == 0) return PI_OK;                 // empty tensors have no address
+    if (!k || !v || !slots) return PI_ERR_NULL;
     if ((rc = check_strides(k, k_token_stride, k_head_stride)) || (rc = check_strides(v, v_token_stride, v_head_stride))) return rc;
-    if (n_tokens == 0) return PI_OK;
     KvAppendArgs a{n_tokens, cache->n_kv, cache->head_dim, page_log(cache->page), cache->n_pages * cache->page,
                    k_token_stride, k_head_stride, v_token_stride, v_head_stride, static_cast<const uint16_t *>(k),
                    static_cast<const uint16_t *>(v), slots, static_cast<uint16_t *>(cache->k_pages),
@@ -185,19 +165,20 @@ extern "C" int pi_kv_attn(const pi_kv_cache *cache, const pi_kv_batch *batch, co
                           int32_t n_q, float scale, int32_t window, void *ws, size_t ws_bytes, void *stream) {
     int rc = check_cache(cache);
     if (rc || (rc = check_batch(batch))) return rc;
-    if (!q || !out) return PI_ERR_NULL;
     if ((rc = check_rows(cache, total_q, n_q))) return rc;
+    if (total_q == 0) return PI_OK;
+    if (!q || !out) return PI_ERR_NULL;
     if (window < 0 || !(scale > 0.f) || !std::isfinite(scale)) return PI_ERR_SHAPE;
     if ((rc = check_strides(q, q_token_stride, q_head_stride)) || (rc = check_strides(out, out_token_stride, out_head_stride)))
         return rc;
     const AttnPlan g = attn_plan(cache, batch, total_q, n_q);
     if (!ws || ws_bytes < g.bytes) return PI_ERR_WORKSPACE;
     if (!aligned16(ws)) return PI_ERR_ALIGN;
-    if (total_q == 0) return PI_OK;
     KvAttnArgs a{};
     a.n_pages = cache->n_pages, a.n_kv = cache->n_kv, a.page_log = page_log(cache->page);
     a.n_req = batch->n_req, a.max_pages = batch->max_pages, a.max_q = batch->max_q, a.max_kv = batch->max_kv;
     a.total_q = total_q, a.n_q = n_q, a.group = n_q / cache->n_kv, a.window = window;
+    a.split_target = g.target, a.slots = g.slots;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.table_stride = batch->table_stride;
     a.q_ts = q_token_stride, a.q_hs = q_head_stride, a.o_ts = out_token_stride, a.o_hs = out_head_stride;

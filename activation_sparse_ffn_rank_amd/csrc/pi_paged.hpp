@@ -270,9 +270,8 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppendArgs a) {
 struct KvAttnArgs {
     int n_pages, n_kv, page_log;
     int n_req, max_pages, max_q, max_kv, total_q, n_q, group, window;
-    int row_min, row_max;             // requests with this many query rows per kv head; the others are left to another launch
     int split_target;                 // 0: key ranges are not cut
-    int items;                        // items per kv head that the workspace and the grid hold
+    int slots;                        // split items per kv head that the workspace holds
     float scale_log2;                 // scale / ln 2, > 0: weights are powers of two
     int64_t table_stride, q_ts, q_hs, o_ts, o_hs;
     const uint16_t *k, *v, *q;
@@ -296,7 +295,6 @@ __device__ __forceinline__ KvReq kv_req(const KvAttnArgs &a, int r) {
     x.n = ok ? q1 - q0 : 0;
     x.m = max(a.kv_len[r], 0);
     x.rows = min(x.n, a.max_q) * a.group;
-    if (x.rows < a.row_min || x.rows > a.row_max) x.rows = 0;
     x.hi = (int)min((int64_t)min(x.m, a.max_kv), (int64_t)a.max_pages << a.page_log);
     x.lo = a.window ? min(max(x.m - x.n - a.window + 1, 0), x.hi) & ~63 : 0;
     return x;
@@ -323,16 +321,19 @@ __device__ __forceinline__ int kv_chunk(const KvAttnArgs &a, int lane) {
     return max((int)fminf(c, 1073741824.f), kKvMinChunk);
 }
 
-// Item `want` of one kv head: requests in order, row tiles, key chunks.
+// Item `want` of one kv head: requests in order, row tiles, key chunks.  Items of requests whose key
+// range is cut are numbered apart (slot): a request of c > 1 chunks has more than (c - 1) * chunk keys, so
+// their count is below twice the split target whatever the number of row tiles.
 struct KvItem {
     int r, tile, split, splits;     // r < 0: there is no such item
+    int slot;                       // of the tile's first chunk, if splits > 1
     KvReq q;
 };
-template <int TR, bool JOIN>        // JOIN: items are row tiles, `first` receives the first split item
-__device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, int chunk, int lane, int *first) {
+template <int TR, bool JOIN>        // JOIN: items are row tiles
+__device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, int chunk, int lane) {
     KvItem it;
     it.r = -1;
-    int base = 0, base_split = 0;
+    int base = 0, base_slot = 0;
     for (int r0 = 0; r0 < a.n_req; r0 += 64) {
         KvReq q{};
         int tiles = 0, splits = 1;
@@ -341,9 +342,9 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, int chu
             tiles = (q.rows + TR - 1) / TR;
             splits = max((q.hi - q.lo + chunk - 1) / chunk, 1);
         }
-        const int items = tiles * splits, mine = JOIN ? tiles : items;
+        const int cut = splits > 1 ? tiles * splits : 0, mine = JOIN ? tiles : tiles * splits;
         const int incl = wave_incl_scan(mine), total = __builtin_amdgcn_readlane(incl, 63);
-        const int incl_split = JOIN ? wave_incl_scan(items) : 0;
+        const int incl_slot = a.split_target ? wave_incl_scan(cut) : 0;
         if (want < base + total) {
             const uint64_t past = __ballot(incl > want - base);
             const int l = __builtin_ctzll(past);
@@ -352,13 +353,15 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, int chu
             it.splits = bcast(splits, l);
             it.tile = JOIN ? at : at / it.splits;
             it.split = JOIN ? 0 : at - it.tile * it.splits;
+            it.slot = base_slot + bcast(incl_slot, l) - bcast(cut, l) + it.tile * it.splits;
             it.q.q0 = bcast(q.q0, l), it.q.n = bcast(q.n, l), it.q.m = bcast(q.m, l);
             it.q.rows = bcast(q.rows, l), it.q.lo = bcast(q.lo, l), it.q.hi = bcast(q.hi, l);
-            if (JOIN) *first = base_split + bcast(incl_split, l) - bcast(items, l) + at * it.splits;
+            // (row ranges that overlap can ask for more than the workspace holds; those are left out)
+            if (it.splits > 1 && it.slot + it.splits > a.slots) it.r = -1;
             return it;
         }
         base += total;
-        if (JOIN) base_split += __builtin_amdgcn_readlane(incl_split, 63);
+        base_slot += __builtin_amdgcn_readlane(incl_slot, 63);
     }
     return it;
 }
@@ -391,7 +394,8 @@ __global__ __launch_bounds__(256) void k_kv_rows(KvAttnArgs a) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = lane & 15, g = lane >> 4;
     const int h = blockIdx.x % a.n_kv, want = blockIdx.x / a.n_kv;
-    const KvItem it = kv_item<kKvRowTile, false>(a, want, kv_chunk<kKvRowTile>(a, lane), lane, nullptr);
+    const int chunk = kv_chunk<kKvRowTile>(a, lane);
+    const KvItem it = kv_item<kKvRowTile, false>(a, want, chunk, lane);
     if (it.r < 0) return;
     const KvReq &rq = it.q;
 
@@ -414,7 +418,7 @@ __global__ __launch_bounds__(256) void k_kv_rows(KvAttnArgs a) {
     const int all_hi = min(pos_a + 1, rq.hi), all_lo = a.window ? max(pos_b - a.window + 1, 0) : 0;
     int lo = max(tile_lo & ~31, rq.lo), hi = tile_hi;
     if (it.splits > 1) {
-        const int chunk = kv_chunk<kKvRowTile>(a, lane), from = rq.lo + it.split * chunk;
+        const int from = rq.lo + it.split * chunk;
         lo = max(lo, from);
         hi = min(hi, from + chunk);
     }
@@ -430,37 +434,57 @@ __global__ __launch_bounds__(256) void k_kv_rows(KvAttnArgs a) {
 
     const int *const tab = a.table + (int64_t)it.r * a.table_stride;
     const int page = 1 << a.page_log, held = (rq.hi + page - 1) >> a.page_log;
-    int tab0 = 0, ids = -1;
-    for (int kb = k_lo; kb < k_hi; kb += 32) {
-        const int pg = kb >> a.page_log;
-        if (kb == k_lo || pg - tab0 + 1 >= 64) {       // the next 64 table entries, one per lane
-            tab0 = pg;
+    const int64_t page_elems = ((int64_t)a.n_kv << a.page_log) * HD;
+    const uint16_t *const k_head = a.k + ((int64_t)h * HD << a.page_log), *const v_head = a.v + ((int64_t)h * HD << a.page_log);
+    int tab0 = 0, ids = 0;
+    bool none = true;                    // no table entries at hand yet
+    // Where the 32 keys of a block lie: elements of the pages of keys kb..+15 and kb+16..+31 (the same one unless
+    // pages hold 16 positions), and whether there are such pages.
+    struct Block {
+        int64_t b0, b1;
+        int in0, in1;
+        bool dead0, dead1;
+    };
+    auto find = [&](int kb) -> Block {
+        Block x;
+        const int p0 = kb >> a.page_log, p1 = (kb + 16) >> a.page_log;
+        if (none || p1 - tab0 >= 64) {                  // the next 64 table entries, one per lane
+            tab0 = p0;
             ids = tab0 + lane < held ? tab[tab0 + lane] : -1;
+            none = false;
         }
-        // pages of keys kb..+15 and kb+16..+31 (the same one unless pages hold 16 positions)
-        int id0 = bcast(ids, pg - tab0), id1 = bcast(ids, ((kb + 16) >> a.page_log) - tab0);
-        const bool dead0 = (uint32_t)id0 >= (uint32_t)a.n_pages, dead1 = (uint32_t)id1 >= (uint32_t)a.n_pages;
-        if (dead0 && dead1) continue;
-        if (dead0) id0 = id1;                            // read something in bounds; its keys are masked below
-        if (dead1) id1 = id0;
-        const int in_page = kb & (page - 1), in_page1 = (kb + 16) & (page - 1);
-        const int64_t b0 = (((int64_t)id0 * a.n_kv + h) << a.page_log) * HD;
-        const int64_t b1 = (((int64_t)id1 * a.n_kv + h) << a.page_log) * HD;
-
-        // scores of 32 keys: tile u, row 4a + b is key 8a + 4u + b
-        const int krow = 8 * ((col >> 2) & 1) + (col & 3);
-        const uint16_t *kp = a.k + (col & 8 ? b1 + (int64_t)(in_page1 + krow) * HD : b0 + (int64_t)(in_page + krow) * HD) + 8 * g;
-        uint4 kf[2][kSteps];
+        const int id0 = bcast(ids, p0 - tab0), id1 = bcast(ids, p1 - tab0);
+        x.dead0 = (uint32_t)id0 >= (uint32_t)a.n_pages, x.dead1 = (uint32_t)id1 >= (uint32_t)a.n_pages;
+        // without a page something in bounds is read; its keys are masked
+        x.b0 = (x.dead0 ? 0 : id0) * page_elems, x.b1 = (x.dead1 ? 0 : id1) * page_elems;
+        x.in0 = kb & (page - 1), x.in1 = (kb + 16) & (page - 1);
+        return x;
+    };
+    uint4 kf[2][kSteps], vf[kTiles];
+    // keys: tile u, row 4a + b is key 8a + 4u + b
+    const int krow = 8 * ((col >> 2) & 1) + (col & 3);
+    auto load_k = [&](const Block &x) {
+        const uint16_t *kp = k_head + (col & 8 ? x.b1 + (int64_t)x.in1 * HD : x.b0 + (int64_t)x.in0 * HD) + krow * HD + 8 * g;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int t = 0; t < kSteps; ++t)
 #pragma unroll
-            for (int t = 0; t < kSteps; ++t) kf[u][t] = ld16(kp + 4 * u * HD + 32 * t);
-        const int64_t vrow = (g & 2 ? b1 + in_page1 : b0 + in_page) + 8 * (g & 1);
-        const uint16_t *vp = a.v + vrow + ((int64_t)col << a.page_log);
-        uint4 vf[kTiles];
+            for (int u = 0; u < 2; ++u) kf[u][t] = ld16(kp + 4 * u * HD + 32 * t);
+    };
+    auto load_v = [&](const Block &x) {
+        const uint16_t *vp = v_head + (g & 2 ? x.b1 + x.in1 : x.b0 + x.in0) + 8 * (g & 1) + (col << a.page_log);
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) vf[t] = ld16(vp + ((int64_t)(16 * t) << a.page_log));
-
+        for (int t = 0; t < kTiles; ++t) vf[t] = ld16(vp + ((16 * t) << a.page_log));
+    };
+    Block at{}, next{};
+    if (k_lo < k_hi) {
+        next = find(k_lo);
+        load_k(next);
+        load_v(next);
+    }
+    for (int kb = k_lo; kb < k_hi; kb += 32) {
+        at = next;
+        const bool dead0 = at.dead0, dead1 = at.dead1, more = kb + 32 < k_hi;
+        if (more) next = find(kb + 32);
         float s[8];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -470,6 +494,8 @@ __global__ __launch_bounds__(256) void k_kv_rows(KvAttnArgs a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[4 * u + i] = acc[i] * a.scale_log2;
         }
+
+        if (more) load_k(next);          // in flight during the softmax and the second product
 
         uint32_t odd_keys = 0;                           // keys of the block with an infinite or NaN value somewhere
         if (kb < all_lo || kb + 32 > all_hi || dead0 || dead1) {
@@ -532,6 +558,8 @@ __global__ __launch_bounds__(256) void k_kv_rows(KvAttnArgs a) {
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) st.o[t] = T::mfma16(vf[t], pf, st.o[t]);
 
+        if (more) load_v(next);
+
         while (odd_keys) {
             const int j = __builtin_ctz(odd_keys);
             odd_keys &= odd_keys - 1;
@@ -540,12 +568,14 @@ __global__ __launch_bounds__(256) void k_kv_rows(KvAttnArgs a) {
             for (int e = 1; e < 8; ++e) mine = (j & 7) == e ? p[e] : mine;
             const float w = __shfl(mine, (j >> 3) * 16 + col);
             if (kb + j < see_lo || kb + j >= see_hi) continue;
-            const uint16_t *x = a.v + (j & 16 ? b1 + in_page1 + (j & 15) : b0 + in_page + j) + ((int64_t)(4 * g) << a.page_log);
+            int d0 = 4 * g;
+            asm volatile("" : "+v"(d0));                // its addresses are not worth registers outside this loop
+            const uint16_t *x = v_head + (j & 16 ? at.b1 + at.in1 + (j & 15) : at.b0 + at.in0 + j);
 #pragma unroll
             for (int t = 0; t < kTiles; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    st.o[t][i] += w * (float)__builtin_bit_cast(typename T::e, x[(int64_t)(16 * t + i) << a.page_log]);
+                    st.o[t][i] += w * (float)__builtin_bit_cast(typename T::e, x[(d0 + 16 * t + i) << a.page_log]);
         }
     }
 
@@ -586,7 +616,7 @@ __global__ __launch_bounds__(256) void k_kv_rows(KvAttnArgs a) {
                                                                  kv_pack<T>(st.o[t][2] * inv, st.o[t][3] * inv));
         return;
     }
-    float *const pt = a.part + (int64_t)blockIdx.x * (kKvRowTile * (HD + 2));
+    float *const pt = a.part + ((int64_t)(it.slot + it.split) * a.n_kv + h) * (kKvRowTile * (HD + 2));
     if (row < rq.rows) {
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) *reinterpret_cast<f32x4 *>(pt + col * HD + 16 * t + 4 * g) = st.o[t];
@@ -630,7 +660,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
     const int col = lane & 31, half = lane >> 5;
     const int h = blockIdx.x % a.n_kv, want = blockIdx.x / a.n_kv;
     const int chunk = kv_chunk<kKvWideTile>(a, lane);
-    const KvItem it = kv_item<kKvWideTile, false>(a, want, chunk, lane, nullptr);
+    const KvItem it = kv_item<kKvWideTile, false>(a, want, chunk, lane);
     if (it.r < 0) return;
     const KvReq &rq = it.q;
     // later rows see more keys: they go first
@@ -732,13 +762,17 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
     };
 
     f32x16 o[kTiles];
+    float ref, sum;
+    const int krow = (col & ~12) | (col & 8) >> 1 | (col & 4) << 1;
+    // An infinity or NaN among the values of keys that some rows of a wave see and others do not reaches
+    // the others too (0 x infinity).  Such values are looked for only if a result is not finite: the
+    // workgroup then computes its item once more and handles them apart (careful).
+    for (bool careful = false;; careful = true) {
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[t][i] = 0.f;
-    float ref = -INFINITY, sum = 0.f;
-    const int krow = (col & ~12) | (col & 8) >> 1 | (col & 4) << 1;
-
+    ref = -INFINITY, sum = 0.f;
     uint32_t dead_next = 0;
     int buf = 0;
     if (lo < hi) dead_next = load(lo, 0);
@@ -815,7 +849,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
             for (int e = 0; e < KT; ++e)
                 if (kb + e < wave_lo || kb + e >= wave_hi || (dead >> (e >> 4) & 1)) drop |= 1ull << e;
             uint64_t odd_keys = 0;
-            if (pos_a != pos_b) {
+            if (careful) {
 #pragma unroll 1
                 for (int j = 0; j < 2 * kSub; ++j) {
                     uint32_t odd = 0;
@@ -872,6 +906,23 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
             }
         }
     }
+    if (careful) break;
+    float probe = 0.f;                   // 0 if every sum is finite, NaN otherwise
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) probe += 0.f * o[t][i];
+    // (the buffers are free: a word of them carries the waves' vote, so that LDS stays at 64 KB)
+    volatile int *const again = reinterpret_cast<volatile int *>(&s_kv[0][0][0]);
+    __syncthreads();
+    if (threadIdx.x == 0) *again = 0;
+    __syncthreads();
+    if (pos_a != pos_b && probe != 0.f) *again = 1;
+    __syncthreads();
+    const int vote = *again;
+    __syncthreads();
+    if (!vote) break;
+    }
 
     if (row >= rq.rows) return;
     sum += __shfl_xor(sum, 32);
@@ -887,8 +938,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
         return;
     }
     const int prow = wave * 32 + col;
-    // (the items of a request are numbered by it.tile, so the join finds them in the same order)
-    float *const pt = a.part + (int64_t)blockIdx.x * (kKvWideTile * (HD + 2));
+    float *const pt = a.part + ((int64_t)(it.slot + it.split) * a.n_kv + h) * (kKvWideTile * (HD + 2));
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
 #pragma unroll
@@ -904,28 +954,45 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
 template <class T, int HD, int TR>
 __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
     constexpr int kLanes = HD / 4, kRows = 256 / kLanes;          // threads per row, rows at a time
+    constexpr int kDeep = 8;                                       // chunks whose loads are in flight together
     const int lane = threadIdx.x & 63;
     const int sub = blockIdx.x % (TR / 16), at = blockIdx.x / (TR / 16);
     const int h = at % a.n_kv, want = at / a.n_kv;
-    int first = 0;
-    const KvItem it = kv_item<TR, true>(a, want, kv_chunk<TR>(a, lane), lane, &first);
-    // (row ranges that overlap can name more items than the grid holds; those have no partial sums)
-    if (it.r < 0 || it.splits == 1 || first + it.splits > a.items) return;
+    const KvItem it = kv_item<TR, true>(a, want, kv_chunk<TR>(a, lane), lane);
+    if (it.r < 0 || it.splits == 1) return;
     const int tile = TR == kKvRowTile ? it.tile : (it.q.rows + TR - 1) / TR - 1 - it.tile;
     const int64_t stride = (int64_t)a.n_kv * (TR * (HD + 2));
-    const float *const pt = a.part + (int64_t)first * stride + (int64_t)h * (TR * (HD + 2));
+    const float *const pt = a.part + ((int64_t)it.slot * a.n_kv + h) * (TR * (HD + 2));
     const int d = (threadIdx.x % kLanes) * 4;
     for (int prow = sub * 16 + threadIdx.x / kLanes; prow < sub * 16 + 16; prow += kRows) {
         const int row = tile * TR + prow;
         if (row >= it.q.rows) return;
         float ref = -INFINITY, sum = 0.f;
-        for (int s = 0; s < it.splits; ++s) ref = fmaxf(ref, pt[s * stride + TR * HD + prow]);
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < it.splits; ++s) {
-            const float r = pt[s * stride + TR * HD + prow];
-            const float f = r == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(r - ref);
-            sum += f * pt[s * stride + TR * (HD + 1) + prow];
-            o += f * *reinterpret_cast<const f32x4 *>(pt + s * stride + prow * HD + d);
+        for (int s0 = 0; s0 < it.splits; s0 += kDeep) {
+            float r[kDeep], w[kDeep];
+            f32x4 x[kDeep];
+#pragma unroll
+            for (int i = 0; i < kDeep; ++i) {
+                const float *const ps = pt + min(s0 + i, it.splits - 1) * stride;
+                r[i] = ps[TR * HD + prow];
+                w[i] = ps[TR * (HD + 1) + prow];
+                x[i] = *reinterpret_cast<const f32x4 *>(ps + prow * HD + d);
+            }
+            float to = ref;
+#pragma unroll
+            for (int i = 0; i < kDeep; ++i) to = fmaxf(to, r[i]);
+            const float f0 = ref == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ref - to);
+            sum *= f0;
+            o *= f0;
+            ref = to;
+#pragma unroll
+            for (int i = 0; i < kDeep; ++i) {
+                if (s0 + i >= it.splits) break;
+                const float f = r[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(r[i] - ref);
+                sum += f * w[i];
+                o += f * x[i];
+            }
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int tok = row / a.group, head = h * a.group + (row - tok * a.group);

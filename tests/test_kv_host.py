@@ -60,7 +60,7 @@ def test_cache_rejects(L):
 def test_append_rejects(L):
     c = cache()
     call = lambda k=A, kt=1024, kh=128, v=A, vt=1024, vh=128, slots=A, n=4: L.pi_kv_append(c, k, kt, kh, v, vt, vh, slots, n, None)
-    assert call(n=0) == _abi.PI_OK
+    assert call(n=0) == _abi.PI_OK and call(n=0, k=0, v=0, slots=0) == _abi.PI_OK
     for kw in (dict(k=0), dict(v=0), dict(slots=0)):
         assert call(**kw) == _abi.PI_ERR_NULL
     for kw in (dict(n=-1), dict(n=(1 << 19) + 1), dict(kt=-1024), dict(vh=-128)):
@@ -85,7 +85,7 @@ def test_attn_rejects(L):
 
     def call(c=None, b=None, q=A, qt=4096, qh=128, out=A, ot=4096, oh=128, total=4, n_q=32, scale=0.1, window=0, ws=A, n=need):
         return L.pi_kv_attn(c or cache(), b or batch(), q, qt, qh, out, ot, oh, total, n_q, scale, window, ws, n, None)
-    assert call(total=0) == _abi.PI_OK
+    assert call(total=0) == _abi.PI_OK and call(total=0, q=0, out=0, ws=0) == _abi.PI_OK
     assert L.pi_kv_attn(None, batch(), A, 4096, 128, A, 4096, 128, 4, 32, 0.1, 0, A, need, None) == _abi.PI_ERR_NULL
     assert L.pi_kv_attn(cache(), None, A, 4096, 128, A, 4096, 128, 4, 32, 0.1, 0, A, need, None) == _abi.PI_ERR_NULL
     for kw in (dict(q=0), dict(out=0), dict(b=batch(table=0)), dict(b=batch(starts=0)), dict(b=batch(kv=0))):
