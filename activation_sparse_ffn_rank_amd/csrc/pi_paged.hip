@@ -14,6 +14,7 @@ constexpr int kMaxHeads = 1024;
 // Key ranges are cut so that about this many workgroups share the work of all requests.
 constexpr int kSplitTarget = 1024;        // k_kv_rows
 constexpr int kSplitTargetWide = 512;     // k_kv_tile
+constexpr int kJoinGroups = 1024;         // workgroups of k_kv_join, at most
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -92,7 +93,10 @@ AttnPlan attn_plan(const pi_kv_cache *c, const pi_kv_batch *b, int total_q, int 
 template <class T, int HD, int TR>
 int launch_join(const KvAttnArgs &a, const AttnPlan &p, hipStream_t st) {
     if (!p.target) return PI_OK;
-    hipLaunchKernelGGL((k_kv_join<T, HD, TR>), dim3((uint32_t)p.tiles * a.n_kv * (TR / 16)), dim3(256), 0, st, a);
+    // at most every row of every tile, a few rows per workgroup; long lists are walked by a bounded grid
+    const int64_t rows = std::min<int64_t>((int64_t)p.tiles * TR, (int64_t)a.total_q * a.group);
+    const int64_t groups = (rows * (HD / 4) + 63) / 64 * a.n_kv;
+    hipLaunchKernelGGL((k_kv_join<T, HD, TR>), dim3((uint32_t)std::min<int64_t>(groups, kJoinGroups)), dim3(256), 0, st, a);
     return hipGetLastError() == hipSuccess ? PI_OK : PI_ERR_HIP;
 }
 

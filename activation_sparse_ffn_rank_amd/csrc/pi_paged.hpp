@@ -329,7 +329,8 @@ struct KvItem {
     int slot;                       // of the tile's first chunk, if splits > 1
     KvReq q;
 };
-template <int TR, bool JOIN>        // JOIN: items are row tiles
+// ROWS > 0 counts groups of ROWS rows of the cut requests instead (for the join; split is then the group).
+template <int TR, int ROWS>
 __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, int chunk, int lane) {
     KvItem it;
     it.r = -1;
@@ -342,7 +343,8 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, int chu
             tiles = (q.rows + TR - 1) / TR;
             splits = max((q.hi - q.lo + chunk - 1) / chunk, 1);
         }
-        const int cut = splits > 1 ? tiles * splits : 0, mine = JOIN ? tiles : tiles * splits;
+        const int cut = splits > 1 ? tiles * splits : 0;
+        const int mine = ROWS == 0 ? tiles * splits : splits > 1 ? (q.rows + ROWS - 1) / (ROWS == 0 ? 1 : ROWS) : 0;
         const int incl = wave_incl_scan(mine), total = __builtin_amdgcn_readlane(incl, 63);
         const int incl_slot = a.split_target ? wave_incl_scan(cut) : 0;
         if (want < base + total) {
@@ -351,13 +353,20 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, int chu
             const int at = want - base - (bcast(incl, l) - bcast(mine, l));
             it.r = r0 + l;
             it.splits = bcast(splits, l);
-            it.tile = JOIN ? at : at / it.splits;
-            it.split = JOIN ? 0 : at - it.tile * it.splits;
-            it.slot = base_slot + bcast(incl_slot, l) - bcast(cut, l) + it.tile * it.splits;
             it.q.q0 = bcast(q.q0, l), it.q.n = bcast(q.n, l), it.q.m = bcast(q.m, l);
             it.q.rows = bcast(q.rows, l), it.q.lo = bcast(q.lo, l), it.q.hi = bcast(q.hi, l);
+            if (ROWS == 0) {
+                it.tile = at / it.splits;
+                it.split = at - it.tile * it.splits;
+                // wide tiles: later rows see more keys and go first
+                if (TR != kKvRowTile) it.tile = bcast(tiles, l) - 1 - it.tile;
+            } else {
+                it.tile = at * ROWS / TR;
+                it.split = at;
+            }
+            it.slot = base_slot + bcast(incl_slot, l) - bcast(cut, l) + it.tile * it.splits;
             // (row ranges that overlap can ask for more than the workspace holds; those are left out)
-            if (it.splits > 1 && it.slot + it.splits > a.slots) it.r = -1;
+            if (it.splits > 1 && it.slot + it.splits > a.slots) it.r = -2;
             return it;
         }
         base += total;
@@ -395,7 +404,7 @@ __global__ __launch_bounds__(256) void k_kv_rows(KvAttnArgs a) {
     const int col = lane & 15, g = lane >> 4;
     const int h = blockIdx.x % a.n_kv, want = blockIdx.x / a.n_kv;
     const int chunk = kv_chunk<kKvRowTile>(a, lane);
-    const KvItem it = kv_item<kKvRowTile, false>(a, want, chunk, lane);
+    const KvItem it = kv_item<kKvRowTile, 0>(a, want, chunk, lane);
     if (it.r < 0) return;
     const KvReq &rq = it.q;
 
@@ -660,12 +669,10 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
     const int col = lane & 31, half = lane >> 5;
     const int h = blockIdx.x % a.n_kv, want = blockIdx.x / a.n_kv;
     const int chunk = kv_chunk<kKvWideTile>(a, lane);
-    const KvItem it = kv_item<kKvWideTile, false>(a, want, chunk, lane);
+    const KvItem it = kv_item<kKvWideTile, 0>(a, want, chunk, lane);
     if (it.r < 0) return;
     const KvReq &rq = it.q;
-    // later rows see more keys: they go first
-    const int tile = (rq.rows + kKvWideTile - 1) / kKvWideTile - 1 - it.tile;
-    const int past = rq.m - rq.n;
+    const int tile = it.tile, past = rq.m - rq.n;
 
     // this lane's query row
     const int row = tile * kKvWideTile + wave * 32 + col, row_c = min(row, rq.rows - 1);
@@ -950,54 +957,77 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
     }
 }
 
-// Joins the split items of 16 rows of a row tile of one kv head, in the order of their key ranges.
+// Joins the split items: a workgroup takes a few rows of one kv head at a time (a row per HD / 4 lanes, 16
+// bytes each), its four waves a quarter of the chunks each, kDeep of them in flight; the quarters are added in
+// order.  The grid does not depend on how many requests are cut: with none it ends at once.
 template <class T, int HD, int TR>
 __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
-    constexpr int kLanes = HD / 4, kRows = 256 / kLanes;          // threads per row, rows at a time
-    constexpr int kDeep = 8;                                       // chunks whose loads are in flight together
-    const int lane = threadIdx.x & 63;
-    const int sub = blockIdx.x % (TR / 16), at = blockIdx.x / (TR / 16);
-    const int h = at % a.n_kv, want = at / a.n_kv;
-    const KvItem it = kv_item<TR, true>(a, want, kv_chunk<TR>(a, lane), lane);
-    if (it.r < 0 || it.splits == 1) return;
-    const int tile = TR == kKvRowTile ? it.tile : (it.q.rows + TR - 1) / TR - 1 - it.tile;
+    constexpr int kLanes = HD / 4, kRows = 64 / kLanes, kDeep = 8, kWaves = 4;
+    __shared__ f32x4 s_o[kWaves][64];
+    __shared__ float s_ref[kWaves][64], s_sum[kWaves][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int chunk = kv_chunk<TR>(a, lane);
     const int64_t stride = (int64_t)a.n_kv * (TR * (HD + 2));
-    const float *const pt = a.part + ((int64_t)it.slot * a.n_kv + h) * (TR * (HD + 2));
-    const int d = (threadIdx.x % kLanes) * 4;
-    for (int prow = sub * 16 + threadIdx.x / kLanes; prow < sub * 16 + 16; prow += kRows) {
-        const int row = tile * TR + prow;
-        if (row >= it.q.rows) return;
+    const int d = (lane % kLanes) * 4;
+    for (int u = blockIdx.x;; u += gridDim.x) {
+        const int h = u % a.n_kv, want = u / a.n_kv;
+        const KvItem it = kv_item<TR, kRows>(a, want, chunk, lane);
+        if (it.r == -1) return;
+        if (it.r < 0) continue;
+        const int row = it.split * kRows + lane / kLanes, row_c = min(row, it.q.rows - 1), prow = row_c - it.tile * TR;
+        const float *const pt = a.part + ((int64_t)it.slot * a.n_kv + h) * (TR * (HD + 2));
+        const int quarter = (it.splits + kWaves - 1) / kWaves, from = wave * quarter, to = min(from + quarter, it.splits);
         float ref = -INFINITY, sum = 0.f;
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
-        for (int s0 = 0; s0 < it.splits; s0 += kDeep) {
+        for (int s0 = from; s0 < to; s0 += kDeep) {
             float r[kDeep], w[kDeep];
             f32x4 x[kDeep];
 #pragma unroll
             for (int i = 0; i < kDeep; ++i) {
-                const float *const ps = pt + min(s0 + i, it.splits - 1) * stride;
+                const float *const ps = pt + min(s0 + i, to - 1) * stride;
                 r[i] = ps[TR * HD + prow];
                 w[i] = ps[TR * (HD + 1) + prow];
                 x[i] = *reinterpret_cast<const f32x4 *>(ps + prow * HD + d);
             }
-            float to = ref;
+            float top = ref;
 #pragma unroll
-            for (int i = 0; i < kDeep; ++i) to = fmaxf(to, r[i]);
-            const float f0 = ref == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ref - to);
+            for (int i = 0; i < kDeep; ++i) top = fmaxf(top, r[i]);
+            const float f0 = ref == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ref - top);
             sum *= f0;
             o *= f0;
-            ref = to;
+            ref = top;
 #pragma unroll
             for (int i = 0; i < kDeep; ++i) {
-                if (s0 + i >= it.splits) break;
+                if (s0 + i >= to) break;
                 const float f = r[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(r[i] - ref);
                 sum += f * w[i];
                 o += f * x[i];
             }
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int tok = row / a.group, head = h * a.group + (row - tok * a.group);
-        *reinterpret_cast<uint2 *>(a.out + (int64_t)(it.q.q0 + tok) * a.o_ts + (int64_t)head * a.o_hs + d) =
-            make_uint2(kv_pack<T>(o[0] * inv, o[1] * inv), kv_pack<T>(o[2] * inv, o[3] * inv));
+        s_o[wave][lane] = o;
+        s_ref[wave][lane] = ref;
+        s_sum[wave][lane] = sum;
+        __syncthreads();
+        if (wave == 0) {
+            float top = s_ref[0][lane];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) top = fmaxf(top, s_ref[w][lane]);
+            sum = 0.f;
+            o = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const float r = s_ref[w][lane], f = r == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(r - top);
+                sum += f * s_sum[w][lane];
+                o += f * s_o[w][lane];
+            }
+            if (row < it.q.rows) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const int tok = row / a.group, head = h * a.group + (row - tok * a.group);
+                *reinterpret_cast<uint2 *>(a.out + (int64_t)(it.q.q0 + tok) * a.o_ts + (int64_t)head * a.o_hs + d) =
+                    make_uint2(kv_pack<T>(o[0] * inv, o[1] * inv), kv_pack<T>(o[2] * inv, o[3] * inv));
+            }
+        }
+        __syncthreads();
     }
 }
 
