@@ -11,9 +11,9 @@ namespace {
 using namespace pik;
 
 constexpr int kMaxHeads = 1024;
-// Key ranges are cut so that about this many workgroups share the work of all requests.
-constexpr int kSplitTarget = 1024;        // k_kv_rows
-constexpr int kSplitTargetWide = 512;     // k_kv_tile
+// Key ranges are cut so that about as many workgroups share the work of all requests as the 256 CUs hold
+// at once: 3, 2 or 1 each, by the registers of either kernel.
+constexpr int split_target(int hd) { return hd == 64 ? 768 : hd == 128 ? 512 : 256; }
 constexpr int kJoinGroups = 1024;         // workgroups of k_kv_join, at most
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -65,6 +65,7 @@ int check_strides(const void *p, int64_t ts, int64_t hs) {
 // single tokens run beside it, to k_kv_tile.
 struct AttnPlan {
     int TR;
+    bool mixed;      // k_kv_tile with a path of its own for requests of few rows
     int tiles;       // row tiles per kv head, at most
     int items;       // items per kv head, at most
     int slots;       // split items per kv head, at most
@@ -76,12 +77,18 @@ AttnPlan attn_plan(const pi_kv_cache *c, const pi_kv_batch *b, int total_q, int 
     AttnPlan p{};
     const int64_t group = n_q / c->n_kv, rows = std::min(b->max_q, total_q) * group, reqs = std::min(b->n_req, total_q);
     p.TR = rows <= kKvRowTile ? kKvRowTile : kKvWideTile;
+    // on average, requests of fewer than half of max_q tokens: some of them have few rows
+    p.mixed = (int64_t)2 * total_q < (int64_t)b->max_q * b->n_req;
     p.tiles = (int)std::min(total_q * group / p.TR + reqs, reqs * ((rows + p.TR - 1) / p.TR));
     p.items = p.tiles;
     p.bytes = 16;
     // Nothing is cut where there are too few keys for two items, or row tiles to fill the chip many times.
-    const int target = p.TR == kKvRowTile ? kSplitTarget : kSplitTargetWide;
-    if ((int64_t)p.tiles * c->n_kv < 8 * target && b->max_kv > kKvMinChunk) {
+    // With few tiles the pieces fill the chip just once (4 x 60k grouped: 84.8 us, and 88.6 with twice as many); with
+    // about as many as it holds, finer ones even out their lengths (16 x 2k: 62.6 us, and 66.3 with half as many).
+    int target = split_target(c->head_dim);
+    const int64_t all = (int64_t)p.tiles * c->n_kv;
+    if (all < 8 * target && b->max_kv >= 2 * kKvMinChunk) {
+        if (2 * all > target) target *= 2;
         p.target = target;
         p.items += target / c->n_kv + 2;             // 2: the device sums the work in fp32
         p.slots = std::min(p.items, 2 * target / c->n_kv + 4);
@@ -100,15 +107,23 @@ int launch_join(const KvAttnArgs &a, const AttnPlan &p, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? PI_OK : PI_ERR_HIP;
 }
 
+template <class T, int HD, bool MIXED>
+void launch_tile(const KvAttnArgs &a, dim3 grid, hipStream_t st) {
+    if ((1 << a.page_log) < KvTile<HD>::kKeys)
+        hipLaunchKernelGGL((k_kv_tile<T, HD, true, MIXED>), grid, dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_kv_tile<T, HD, false, MIXED>), grid, dim3(256), 0, st, a);
+}
+
 template <class T, int HD>
 int launch_attn(const KvAttnArgs &a, const AttnPlan &p, hipStream_t st) {
     const dim3 grid((uint32_t)p.items * a.n_kv);
     if (p.TR == kKvRowTile)
-        hipLaunchKernelGGL((k_kv_rows<T, HD>), grid, dim3(256), 0, st, a);
-    else if ((1 << a.page_log) < KvTile<HD>::kKeys)
-        hipLaunchKernelGGL((k_kv_tile<T, HD, true>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((k_kv_rows<T, HD>), grid, dim3(64 * kKvRowWaves), 0, st, a);
+    else if (p.mixed)
+        launch_tile<T, HD, true>(a, grid, st);
     else
-        hipLaunchKernelGGL((k_kv_tile<T, HD, false>), grid, dim3(256), 0, st, a);
+        launch_tile<T, HD, false>(a, grid, st);
     if (hipGetLastError() != hipSuccess) return PI_ERR_HIP;
     return p.TR == kKvRowTile ? launch_join<T, HD, kKvRowTile>(a, p, st) : launch_join<T, HD, kKvWideTile>(a, p, st);
 }
@@ -181,7 +196,8 @@ extern "C" int pi_kv_attn(const pi_kv_cache *cache, const pi_kv_batch *batch, co
     KvAttnArgs a{};
     a.n_pages = cache->n_pages, a.n_kv = cache->n_kv, a.page_log = page_log(cache->page);
     a.n_req = batch->n_req, a.max_pages = batch->max_pages, a.max_q = batch->max_q, a.max_kv = batch->max_kv;
-    a.total_q = total_q, a.n_q = n_q, a.group = n_q / cache->n_kv, a.window = window;
+    // positions stay below 2^31 - 2^19 - window: the lower ends of windows are computed in 32 bits
+    a.total_q = total_q, a.n_q = n_q, a.group = n_q / cache->n_kv, a.window = std::min(window, INT32_MAX - PI_KV_MAX_TOKENS);
     a.split_target = g.target, a.slots = g.slots;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.table_stride = batch->table_stride;

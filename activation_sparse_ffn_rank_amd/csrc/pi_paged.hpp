@@ -303,11 +303,13 @@ __device__ __forceinline__ KvReq kv_req(const KvAttnArgs &a, int r) {
 constexpr int kKvRowTile = 16;          // query rows of a k_kv_rows workgroup
 constexpr int kKvWideTile = 128;        // ... and of a k_kv_tile workgroup
 constexpr int kKvMinChunk = 256;        // keys of a split item, at least
+constexpr int kKvRowWaves = 4;          // waves that share the keys of 16 query rows
 
-// Keys of one split item, from the sum over all requests of row tiles (of TR rows) x keys.
+// How key ranges are cut: into pieces of about sum / split_target keys, the sum taken over all requests of row
+// tiles (of TR rows) x keys, so that the pieces fill the chip once.  Returns pieces per key; 0: none is cut.
 template <int TR>
-__device__ __forceinline__ int kv_chunk(const KvAttnArgs &a, int lane) {
-    if (!a.split_target) return 0x40000000;
+__device__ __forceinline__ float kv_cut(const KvAttnArgs &a, int lane) {
+    if (!a.split_target) return 0.f;
     float sum = 0.f;
     for (int r0 = 0; r0 < a.n_req; r0 += 64) {
         float x = 0.f;
@@ -317,31 +319,39 @@ __device__ __forceinline__ int kv_chunk(const KvAttnArgs &a, int lane) {
         }
         sum += wave_sum(x);
     }
-    const float c = ceilf(sum * (float)a.n_kv / (float)a.split_target / 64.f) * 64.f;
-    return max((int)fminf(c, 1073741824.f), kKvMinChunk);
+    return sum > 0.f ? (float)a.split_target / (sum * (float)a.n_kv) : 0.f;
 }
 
-// Item `want` of one kv head: requests in order, row tiles, key chunks.  Items of requests whose key
-// range is cut are numbered apart (slot): a request of c > 1 chunks has more than (c - 1) * chunk keys, so
-// their count is below twice the split target whatever the number of row tiles.
+// Keys per piece of a request of `keys` keys.  A range is cut in c only from c - 1/4 times the aim on: a little
+// more than the chip holds at once costs a second round, and partial sums are written and read.  Hence the
+// pieces of all cut ranges number at most (2 / 1.75) * split_target.
+__device__ __forceinline__ int kv_piece(int keys, float cut) {
+    const int n = min((int)fminf((float)keys * cut + 0.25f, 65536.f), keys / kKvMinChunk);
+    return n > 1 ? ((keys + n - 1) / n + 63) & ~63 : max(keys, 1);
+}
+
+// Item `want` of one kv head: requests in order, row tiles, pieces.  Items of requests whose key range is
+// cut are numbered apart (slot), so that the workspace does not grow with the row tiles.
 struct KvItem {
     int r, tile, split, splits;     // r < 0: there is no such item
-    int slot;                       // of the tile's first chunk, if splits > 1
+    int slot;                       // of the tile's first piece, if splits > 1
+    int piece;                      // keys of a piece
     KvReq q;
 };
 // ROWS > 0 counts groups of ROWS rows of the cut requests instead (for the join; split is then the group).
 template <int TR, int ROWS>
-__device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, int chunk, int lane) {
+__device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, float cut_rate, int lane) {
     KvItem it;
     it.r = -1;
     int base = 0, base_slot = 0;
     for (int r0 = 0; r0 < a.n_req; r0 += 64) {
         KvReq q{};
-        int tiles = 0, splits = 1;
+        int tiles = 0, splits = 1, piece = 1;
         if (r0 + lane < a.n_req) {
             q = kv_req(a, r0 + lane);
             tiles = (q.rows + TR - 1) / TR;
-            splits = max((q.hi - q.lo + chunk - 1) / chunk, 1);
+            piece = kv_piece(q.hi - q.lo, cut_rate);
+            splits = max((q.hi - q.lo + piece - 1) / piece, 1);
         }
         const int cut = splits > 1 ? tiles * splits : 0;
         const int mine = ROWS == 0 ? tiles * splits : splits > 1 ? (q.rows + ROWS - 1) / (ROWS == 0 ? 1 : ROWS) : 0;
@@ -353,6 +363,7 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, int chu
             const int at = want - base - (bcast(incl, l) - bcast(mine, l));
             it.r = r0 + l;
             it.splits = bcast(splits, l);
+            it.piece = bcast(piece, l);
             it.q.q0 = bcast(q.q0, l), it.q.n = bcast(q.n, l), it.q.m = bcast(q.m, l);
             it.q.rows = bcast(q.rows, l), it.q.lo = bcast(q.lo, l), it.q.hi = bcast(q.hi, l);
             if (ROWS == 0) {
@@ -393,19 +404,21 @@ __device__ __forceinline__ float kv_row_sum(float x) {
     return x + __shfl_xor(x, 32);
 }
 
+// What the waves of a workgroup hand over to each other at the end of an item of 16 rows.
+template <int HD>
+struct KvRowsLds {
+    f32x4 o[kKvRowWaves / 2][HD / 16][64];
+    float ref[kKvRowWaves][16], sum[kKvRowWaves / 2][64];
+};
+
 // One workgroup: one item (16 query rows of one kv head, one key range) of one request; its waves
-// take a part of the range each, 32 keys at a time, straight from the pages into registers.
-template <class T, int HD>
-__global__ __launch_bounds__(256) void k_kv_rows(KvAttnArgs a) {
-    constexpr int kSteps = HD / 32, kTiles = HD / 16, kWaves = 4;
-    __shared__ f32x4 s_o[kWaves / 2][kTiles][64];
-    __shared__ float s_ref[kWaves][16], s_sum[kWaves / 2][64];
+// take a part of the range each, 32 keys at a time, straight from the pages into registers.  TR: rows of
+// a split item in the workspace.
+template <class T, int HD, int TR>
+__device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &it, int h, KvRowsLds<HD> &sh) {
+    constexpr int kSteps = HD / 32, kTiles = HD / 16, kWaves = kKvRowWaves;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = lane & 15, g = lane >> 4;
-    const int h = blockIdx.x % a.n_kv, want = blockIdx.x / a.n_kv;
-    const int chunk = kv_chunk<kKvRowTile>(a, lane);
-    const KvItem it = kv_item<kKvRowTile, 0>(a, want, chunk, lane);
-    if (it.r < 0) return;
     const KvReq &rq = it.q;
 
     // this lane's query row
@@ -427,9 +440,9 @@ __global__ __launch_bounds__(256) void k_kv_rows(KvAttnArgs a) {
     const int all_hi = min(pos_a + 1, rq.hi), all_lo = a.window ? max(pos_b - a.window + 1, 0) : 0;
     int lo = max(tile_lo & ~31, rq.lo), hi = tile_hi;
     if (it.splits > 1) {
-        const int from = rq.lo + it.split * chunk;
+        const int from = rq.lo + it.split * it.piece;
         lo = max(lo, from);
-        hi = min(hi, from + chunk);
+        hi = min(hi, from + it.piece);
     }
     // this wave's part
     const int part = max((((hi - lo + kWaves - 1) / kWaves) + 31) & ~31, 32);
@@ -589,11 +602,11 @@ __global__ __launch_bounds__(256) void k_kv_rows(KvAttnArgs a) {
     }
 
     // the waves' parts: a common reference per row, then sums in a fixed order
-    if (lane < 16) s_ref[wave][lane] = st.ref;
+    if (lane < 16) sh.ref[wave][lane] = st.ref;
     __syncthreads();
-    float ref = s_ref[0][col];
+    float ref = sh.ref[0][col];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) ref = fmaxf(ref, s_ref[w][col]);
+    for (int w = 1; w < kWaves; ++w) ref = fmaxf(ref, sh.ref[w][col]);
     const float f = st.ref == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(st.ref - ref);
     st.sum *= f;
 #pragma unroll
@@ -602,14 +615,14 @@ __global__ __launch_bounds__(256) void k_kv_rows(KvAttnArgs a) {
     for (int half = kWaves / 2; half >= 1; half >>= 1) {
         if (wave >= half && wave < 2 * half) {
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) s_o[wave - half][t][lane] = st.o[t];
-            s_sum[wave - half][lane] = st.sum;
+            for (int t = 0; t < kTiles; ++t) sh.o[wave - half][t][lane] = st.o[t];
+            sh.sum[wave - half][lane] = st.sum;
         }
         __syncthreads();
         if (wave < half) {
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) st.o[t] += s_o[wave][t][lane];
-            st.sum += s_sum[wave][lane];
+            for (int t = 0; t < kTiles; ++t) st.o[t] += sh.o[wave][t][lane];
+            st.sum += sh.sum[wave][lane];
         }
         __syncthreads();
     }
@@ -625,15 +638,26 @@ __global__ __launch_bounds__(256) void k_kv_rows(KvAttnArgs a) {
                                                                  kv_pack<T>(st.o[t][2] * inv, st.o[t][3] * inv));
         return;
     }
-    float *const pt = a.part + ((int64_t)(it.slot + it.split) * a.n_kv + h) * (kKvRowTile * (HD + 2));
+    float *const pt = a.part + ((int64_t)(it.slot + it.split) * a.n_kv + h) * (TR * (HD + 2));
     if (row < rq.rows) {
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) *reinterpret_cast<f32x4 *>(pt + col * HD + 16 * t + 4 * g) = st.o[t];
         if (g == 0) {
-            pt[kKvRowTile * HD + col] = ref;
-            pt[kKvRowTile * (HD + 1) + col] = sum;
+            pt[TR * HD + col] = ref;
+            pt[TR * (HD + 1) + col] = sum;
         }
     }
+}
+
+// Calls in which no request has more than 16 query rows per kv head.
+template <class T, int HD>
+__global__ __launch_bounds__(64 * kKvRowWaves) void k_kv_rows(KvAttnArgs a) {
+    __shared__ KvRowsLds<HD> sh;
+    const int lane = threadIdx.x & 63;
+    const int h = blockIdx.x % a.n_kv, want = blockIdx.x / a.n_kv;
+    const KvItem it = kv_item<kKvRowTile, 0>(a, want, kv_cut<kKvRowTile>(a, lane), lane);
+    if (it.r < 0) return;
+    kv_rows_item<T, HD, kKvRowTile>(a, it, h, sh);
 }
 
 // One workgroup: one item of TR = 128 query rows of one kv head, 32 of them per wave, over one key
@@ -660,18 +684,40 @@ __device__ __forceinline__ void kv_lds_load(const uint16_t *base, uint32_t off, 
 }
 __device__ __forceinline__ void kv_lds_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-template <class T, int HD, bool SMALL>      // SMALL: pages of fewer positions than a block has keys
+// Bits 0 .. n-1 (n <= 64), and the bits of the 16-key groups named by a mask of at most 4 bits.
+__device__ __forceinline__ uint64_t kv_bits(uint32_t n) { return n >= 64 ? ~0ull : (1ull << n) - 1; }
+__device__ __forceinline__ uint64_t kv_dead_bits(uint32_t m) {
+    // each bit to the foot of its group, then over the group
+    const uint64_t f = (uint64_t)(m & 1) | (uint64_t)(m & 2) << 15 | (uint64_t)(m & 4) << 30 | (uint64_t)(m & 8) << 45;
+    return f * 0xffffull;
+}
+
+// SMALL: pages of fewer positions than a block has keys.  MIXED: requests of few rows, single tokens beside
+// prompt chunks among them, are taken too, by kv_rows_item: they wait for memory, not for MFMA.  (14 single tokens
+// beside two chunks of 777, 56 heads of 128: 165 -> 156 us.  Without them the other path stays out of the
+// kernel, whose registers then serve the one loop: a 4096-token chunk 1009 -> 953.)
+template <class T, int HD, bool SMALL, bool MIXED>
 __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a) {
     typedef KvTile<HD> L;
     constexpr int KT = L::kKeys, kSub = KT / 32, kSteps = HD / 16, kTiles = HD / 32;
-    __shared__ __align__(16) uint16_t s_kv[2][2][L::kBytes / 2];       // [buffer][K, V]
+    // [buffer][K, V]
+    __shared__ __align__(16) union {
+        uint16_t kv[2][2][L::kBytes / 2];
+        KvRowsLds<HD> rows;              // of kv_rows_item
+    } s_mem;
+    uint16_t (&s_kv)[2][2][L::kBytes / 2] = s_mem.kv;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 31, half = lane >> 5;
     const int h = blockIdx.x % a.n_kv, want = blockIdx.x / a.n_kv;
-    const int chunk = kv_chunk<kKvWideTile>(a, lane);
-    const KvItem it = kv_item<kKvWideTile, 0>(a, want, chunk, lane);
+    const KvItem it = kv_item<kKvWideTile, 0>(a, want, kv_cut<kKvWideTile>(a, lane), lane);
     if (it.r < 0) return;
     const KvReq &rq = it.q;
+    if constexpr (MIXED) {
+        if (rq.rows <= kKvRowTile) {
+            kv_rows_item<T, HD, kKvWideTile>(a, it, h, s_mem.rows);
+            return;
+        }
+    }
     const int tile = it.tile, past = rq.m - rq.n;
 
     // this lane's query row
@@ -691,9 +737,9 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
     int lo = a.window ? max(pos_first - a.window + 1, 0) : 0, hi = min(pos_last + 1, rq.hi);
     lo = max(lo & ~(KT - 1), rq.lo);
     if (it.splits > 1) {
-        const int from = rq.lo + it.split * chunk;
+        const int from = rq.lo + it.split * it.piece;
         lo = max(lo, from);
-        hi = min(hi, from + chunk);
+        hi = min(hi, from + it.piece);
     }
     // keys that some row of this wave sees, and those that all of them see
     const int wrow = tile * kKvWideTile + wave * 32;
@@ -771,7 +817,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
     f32x16 o[kTiles];
     float ref, sum;
     const int krow = (col & ~12) | (col & 8) >> 1 | (col & 4) << 1;
-    // An infinity or NaN among the values of keys that some rows of a wave see and others do not reaches
+    // An infinity or NaN among the values of keys that some rows of a tile see and others do not reaches
     // the others too (0 x infinity).  Such values are looked for only if a result is not finite: the
     // workgroup then computes its item once more and handles them apart (careful).
     for (bool careful = false;; careful = true) {
@@ -805,13 +851,17 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
         }
         const bool edge = kb < all_lo || kb + KT > all_hi || dead != 0;
         if (edge) {
-            const int from = see_lo - kb - 8 * half, to = see_hi - kb - 8 * half;
+            // the keys that this lane's row sees, a bit each; its half holds every other 8 of them
+            const uint32_t n_all = KT == 64 ? 64 : 32;
+            const uint32_t from = (uint32_t)min(max(see_lo - kb, 0), (int)n_all), to = (uint32_t)min(max(see_hi - kb, 0), (int)n_all);
+            uint64_t see = kv_bits(to) & ~kv_bits(from) & ~kv_dead_bits(dead);
+            see >>= 8 * half;
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int e = 32 * u + 16 * (i >> 3) + (i & 7);
-                    if (e < from || e >= to || (dead >> (2 * u + (i >> 3)) & 1)) s[u][i] = -INFINITY;
+                    if (!((e < 32 ? (uint32_t)see : (uint32_t)(see >> 32)) >> (e & 31) & 1)) s[u][i] = -INFINITY;
                 }
         }
         float top = s[0][0];
@@ -839,8 +889,9 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
                 part += s[u][i];
             }
         sum += part;
-        // At an edge: values that no row of the wave sees are cleared (0 x infinity would be NaN); those that
-        // some rows see and others do not, and that are not finite, are cleared too and added row by row.
+        // Values past the request's keys and of missing pages may hold anything and are cleared (0 x infinity would be
+        // NaN).  With `careful`, so are those of keys that no row of the wave sees, and those that some rows
+        // see and others do not, and that are not finite, are cleared and added row by row.
         uint64_t drop = 0;
         auto v_frag = [&](int t, int j) -> uint4 {
             const int d = 32 * t + col, unit = (2 * j + half) ^ L::swz_v(d);
@@ -853,10 +904,10 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
             return x;
         };
         if (edge) {
-            for (int e = 0; e < KT; ++e)
-                if (kb + e < wave_lo || kb + e >= wave_hi || (dead >> (e >> 4) & 1)) drop |= 1ull << e;
+            drop = ~kv_bits((uint32_t)min(rq.hi - kb, KT)) | kv_dead_bits(dead);
             uint64_t odd_keys = 0;
             if (careful) {
+                drop |= ~kv_bits((uint32_t)min(wave_hi - kb, KT)) | kv_bits((uint32_t)min(max(wave_lo - kb, 0), KT));
 #pragma unroll 1
                 for (int j = 0; j < 2 * kSub; ++j) {
                     uint32_t odd = 0;
@@ -904,7 +955,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
             const int b = 8 * (j & 1);
             const uint4 pf = make_uint4(kv_pack<T>(x[b], x[b + 1]), kv_pack<T>(x[b + 2], x[b + 3]),
                                         kv_pack<T>(x[b + 4], x[b + 5]), kv_pack<T>(x[b + 6], x[b + 7]));
-            if (edge) {
+            if (drop >> (16 * j) & 0xffffu) {
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) o[t] = T::mfma32(clear(v_frag(t, j), j), pf, o[t]);
             } else {
@@ -924,7 +975,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
     __syncthreads();
     if (threadIdx.x == 0) *again = 0;
     __syncthreads();
-    if (pos_a != pos_b && probe != 0.f) *again = 1;
+    if (probe != 0.f) *again = 1;
     __syncthreads();
     const int vote = *again;
     __syncthreads();
@@ -966,12 +1017,12 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
     __shared__ f32x4 s_o[kWaves][64];
     __shared__ float s_ref[kWaves][64], s_sum[kWaves][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int chunk = kv_chunk<TR>(a, lane);
+    const float cut = kv_cut<TR>(a, lane);
     const int64_t stride = (int64_t)a.n_kv * (TR * (HD + 2));
     const int d = (lane % kLanes) * 4;
     for (int u = blockIdx.x;; u += gridDim.x) {
         const int h = u % a.n_kv, want = u / a.n_kv;
-        const KvItem it = kv_item<TR, kRows>(a, want, chunk, lane);
+        const KvItem it = kv_item<TR, kRows>(a, want, cut, lane);
         if (it.r == -1) return;
         if (it.r < 0) continue;
         const int row = it.split * kRows + lane / kLanes, row_c = min(row, it.q.rows - 1), prow = row_c - it.tile * TR;
