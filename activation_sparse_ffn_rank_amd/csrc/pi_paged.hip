@@ -14,6 +14,7 @@ constexpr int kMaxHeads = 1024;
 // Key ranges are cut so that about as many workgroups share the work of all requests as the 256 CUs hold
 // at once: 3, 2 or 1 each, by the registers of either kernel.
 constexpr int split_target(int hd) { return hd == 64 ? 768 : hd == 128 ? 512 : 256; }
+constexpr int kCus = 256;
 constexpr int kJoinGroups = 1024;         // workgroups of k_kv_join, at most
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -65,6 +66,7 @@ int check_strides(const void *p, int64_t ts, int64_t hs) {
 // single tokens run beside it, to k_kv_tile.
 struct AttnPlan {
     int TR;
+    bool shorts;     // k_kv_rows with more waves per workgroup
     bool mixed;      // k_kv_tile with a path of its own for requests of few rows
     int tiles;       // row tiles per kv head, at most
     int items;       // items per kv head, at most
@@ -87,7 +89,13 @@ AttnPlan attn_plan(const pi_kv_cache *c, const pi_kv_batch *b, int total_q, int 
     // about as many as it holds, finer ones even out their lengths (16 x 2k: 62.6 us, and 66.3 with half as many).
     int target = split_target(c->head_dim);
     const int64_t all = (int64_t)p.tiles * c->n_kv;
-    if (all < 8 * target && b->max_kv >= 2 * kKvMinChunk) {
+    // With a CU for each range, more waves in one workgroup read a short one sooner than its pieces are joined (1 x 513,
+    // 16 heads of 64: 7.5 us, and 9.7 cut; 8 x 1000, 32 heads of 128: 27.8, and 34.4).  A CU alone reads at about 50
+    // GB/s, so the longer ones of these are worth it only if most CUs have one.
+    const int64_t range = (int64_t)b->max_kv * c->head_dim * 4;
+    p.shorts = p.TR == kKvRowTile && c->head_dim != 256 && b->max_kv > kKvMinPiece && all <= kCus &&
+               range <= (2 * all >= kCus ? 512 : 256) << 10;
+    if (!p.shorts && all < 8 * target && b->max_kv >= kv_min_cut(c->head_dim)) {
         if (2 * all > target) target *= 2;
         p.target = target;
         p.items += target / c->n_kv + 2;             // 2: the device sums the work in fp32
@@ -118,8 +126,11 @@ void launch_tile(const KvAttnArgs &a, dim3 grid, hipStream_t st) {
 template <class T, int HD>
 int launch_attn(const KvAttnArgs &a, const AttnPlan &p, hipStream_t st) {
     const dim3 grid((uint32_t)p.items * a.n_kv);
-    if (p.TR == kKvRowTile)
-        hipLaunchKernelGGL((k_kv_rows<T, HD>), grid, dim3(64 * kKvRowWaves), 0, st, a);
+    constexpr int kShort = HD == 256 ? kKvRowWaves : kv_short_waves(HD);
+    if (HD != 256 && p.shorts)
+        hipLaunchKernelGGL((k_kv_rows<T, HD, kShort>), grid, dim3(64 * kShort), 0, st, a);
+    else if (p.TR == kKvRowTile)
+        hipLaunchKernelGGL((k_kv_rows<T, HD, kKvRowWaves>), grid, dim3(64 * kKvRowWaves), 0, st, a);
     else if (p.mixed)
         launch_tile<T, HD, true>(a, grid, st);
     else

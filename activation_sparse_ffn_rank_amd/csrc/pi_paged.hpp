@@ -302,8 +302,12 @@ __device__ __forceinline__ KvReq kv_req(const KvAttnArgs &a, int r) {
 
 constexpr int kKvRowTile = 16;          // query rows of a k_kv_rows workgroup
 constexpr int kKvWideTile = 128;        // ... and of a k_kv_tile workgroup
-constexpr int kKvMinChunk = 256;        // keys of a split item, at least
+constexpr int kKvMinPiece = 256;        // keys of a piece, about, at least
+// Ranges of fewer keys (256 KB of keys and values) are not cut: one workgroup reads them at about 50 GB/s, and a
+// join costs 5 to 7 us (16 x 100..500 keys, 32 heads of 128: 29.3 us cut from 512 on in pieces of 256, 20.5 uncut).
+constexpr int kv_min_cut(int hd) { return (1 << 16) / hd; }
 constexpr int kKvRowWaves = 4;          // waves that share the keys of 16 query rows
+constexpr int kv_short_waves(int hd) { return hd == 64 ? 16 : 8; }      // ... of a short range
 
 // How key ranges are cut: into pieces of about sum / split_target keys, the sum taken over all requests of row
 // tiles (of TR rows) x keys, so that the pieces fill the chip once.  Returns pieces per key; 0: none is cut.
@@ -325,8 +329,10 @@ __device__ __forceinline__ float kv_cut(const KvAttnArgs &a, int lane) {
 // Keys per piece of a request of `keys` keys.  A range is cut in c only from c - 1/4 times the aim on: a little
 // more than the chip holds at once costs a second round, and partial sums are written and read.  Hence the
 // pieces of all cut ranges number at most (2 / 1.75) * split_target.
+template <int HD>
 __device__ __forceinline__ int kv_piece(int keys, float cut) {
-    const int n = min((int)fminf((float)keys * cut + 0.25f, 65536.f), keys / kKvMinChunk);
+    if (keys < kv_min_cut(HD)) return max(keys, 1);
+    const int n = min((int)fminf((float)keys * cut + 0.25f, 65536.f), (keys + kKvMinPiece / 2) / kKvMinPiece);
     return n > 1 ? ((keys + n - 1) / n + 63) & ~63 : max(keys, 1);
 }
 
@@ -339,7 +345,7 @@ struct KvItem {
     KvReq q;
 };
 // ROWS > 0 counts groups of ROWS rows of the cut requests instead (for the join; split is then the group).
-template <int TR, int ROWS>
+template <int HD, int TR, int ROWS>
 __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, float cut_rate, int lane) {
     KvItem it;
     it.r = -1;
@@ -350,7 +356,7 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, float c
         if (r0 + lane < a.n_req) {
             q = kv_req(a, r0 + lane);
             tiles = (q.rows + TR - 1) / TR;
-            piece = kv_piece(q.hi - q.lo, cut_rate);
+            piece = kv_piece<HD>(q.hi - q.lo, cut_rate);
             splits = max((q.hi - q.lo + piece - 1) / piece, 1);
         }
         const int cut = splits > 1 ? tiles * splits : 0;
@@ -405,18 +411,18 @@ __device__ __forceinline__ float kv_row_sum(float x) {
 }
 
 // What the waves of a workgroup hand over to each other at the end of an item of 16 rows.
-template <int HD>
+template <int HD, int WAVES>
 struct KvRowsLds {
-    f32x4 o[kKvRowWaves / 2][HD / 16][64];
-    float ref[kKvRowWaves][16], sum[kKvRowWaves / 2][64];
+    f32x4 o[WAVES / 2][HD / 16][64];
+    float ref[WAVES][16], sum[WAVES / 2][64];
 };
 
 // One workgroup: one item (16 query rows of one kv head, one key range) of one request; its waves
 // take a part of the range each, 32 keys at a time, straight from the pages into registers.  TR: rows of
 // a split item in the workspace.
-template <class T, int HD, int TR>
-__device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &it, int h, KvRowsLds<HD> &sh) {
-    constexpr int kSteps = HD / 32, kTiles = HD / 16, kWaves = kKvRowWaves;
+template <class T, int HD, int TR, int WAVES>
+__device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &it, int h, KvRowsLds<HD, WAVES> &sh) {
+    constexpr int kSteps = HD / 32, kTiles = HD / 16, kWaves = WAVES;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = lane & 15, g = lane >> 4;
     const KvReq &rq = it.q;
@@ -649,15 +655,16 @@ __device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &
     }
 }
 
-// Calls in which no request has more than 16 query rows per kv head.
-template <class T, int HD>
-__global__ __launch_bounds__(64 * kKvRowWaves) void k_kv_rows(KvAttnArgs a) {
-    __shared__ KvRowsLds<HD> sh;
+// Calls in which no request has more than 16 query rows per kv head.  WAVES: 4, or more for few short ranges,
+// which are then not cut, and no join follows.
+template <class T, int HD, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_kv_rows(KvAttnArgs a) {
+    __shared__ KvRowsLds<HD, WAVES> sh;
     const int lane = threadIdx.x & 63;
     const int h = blockIdx.x % a.n_kv, want = blockIdx.x / a.n_kv;
-    const KvItem it = kv_item<kKvRowTile, 0>(a, want, kv_cut<kKvRowTile>(a, lane), lane);
+    const KvItem it = kv_item<HD, kKvRowTile, 0>(a, want, kv_cut<kKvRowTile>(a, lane), lane);
     if (it.r < 0) return;
-    kv_rows_item<T, HD, kKvRowTile>(a, it, h, sh);
+    kv_rows_item<T, HD, kKvRowTile, WAVES>(a, it, h, sh);
 }
 
 // One workgroup: one item of TR = 128 query rows of one kv head, 32 of them per wave, over one key
@@ -703,18 +710,18 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
     // [buffer][K, V]
     __shared__ __align__(16) union {
         uint16_t kv[2][2][L::kBytes / 2];
-        KvRowsLds<HD> rows;              // of kv_rows_item
+        KvRowsLds<HD, kKvRowWaves> rows;     // of kv_rows_item
     } s_mem;
     uint16_t (&s_kv)[2][2][L::kBytes / 2] = s_mem.kv;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 31, half = lane >> 5;
     const int h = blockIdx.x % a.n_kv, want = blockIdx.x / a.n_kv;
-    const KvItem it = kv_item<kKvWideTile, 0>(a, want, kv_cut<kKvWideTile>(a, lane), lane);
+    const KvItem it = kv_item<HD, kKvWideTile, 0>(a, want, kv_cut<kKvWideTile>(a, lane), lane);
     if (it.r < 0) return;
     const KvReq &rq = it.q;
     if constexpr (MIXED) {
         if (rq.rows <= kKvRowTile) {
-            kv_rows_item<T, HD, kKvWideTile>(a, it, h, s_mem.rows);
+            kv_rows_item<T, HD, kKvWideTile, kKvRowWaves>(a, it, h, s_mem.rows);
             return;
         }
     }
@@ -1022,7 +1029,7 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
     const int d = (lane % kLanes) * 4;
     for (int u = blockIdx.x;; u += gridDim.x) {
         const int h = u % a.n_kv, want = u / a.n_kv;
-        const KvItem it = kv_item<TR, kRows>(a, want, cut, lane);
+        const KvItem it = kv_item<HD, TR, kRows>(a, want, cut, lane);
         if (it.r == -1) return;
         if (it.r < 0) continue;
         const int row = it.split * kRows + lane / kLanes, row_c = min(row, it.q.rows - 1), prow = row_c - it.tile * TR;
