@@ -413,8 +413,8 @@ __device__ __forceinline__ float kv_row_sum(float x) {
 // What the waves of a workgroup hand over to each other at the end of an item of 16 rows.
 template <int HD, int WAVES>
 struct KvRowsLds {
-    f32x4 o[WAVES / 2][HD / 16][64];
-    float ref[WAVES][16], sum[WAVES / 2][64];
+    f32x4 o[WAVES > 1 ? WAVES / 2 : 1][HD / 16][64];
+    float ref[WAVES][16], sum[WAVES > 1 ? WAVES / 2 : 1][64];
 };
 
 // One workgroup: one item (16 query rows of one kv head, one key range) of one request; its waves
@@ -608,29 +608,32 @@ __device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &
     }
 
     // the waves' parts: a common reference per row, then sums in a fixed order
-    if (lane < 16) sh.ref[wave][lane] = st.ref;
-    __syncthreads();
-    float ref = sh.ref[0][col];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) ref = fmaxf(ref, sh.ref[w][col]);
-    const float f = st.ref == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(st.ref - ref);
-    st.sum *= f;
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) st.o[t] *= f;
-#pragma unroll
-    for (int half = kWaves / 2; half >= 1; half >>= 1) {
-        if (wave >= half && wave < 2 * half) {
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) sh.o[wave - half][t][lane] = st.o[t];
-            sh.sum[wave - half][lane] = st.sum;
-        }
+    float ref = st.ref;
+    if constexpr (kWaves > 1) {
+        if (lane < 16) sh.ref[wave][lane] = st.ref;
         __syncthreads();
-        if (wave < half) {
+        ref = sh.ref[0][col];
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) st.o[t] += sh.o[wave][t][lane];
-            st.sum += sh.sum[wave][lane];
+        for (int w = 1; w < kWaves; ++w) ref = fmaxf(ref, sh.ref[w][col]);
+        const float f = st.ref == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(st.ref - ref);
+        st.sum *= f;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) st.o[t] *= f;
+#pragma unroll
+        for (int half = kWaves / 2; half >= 1; half >>= 1) {
+            if (wave >= half && wave < 2 * half) {
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) sh.o[wave - half][t][lane] = st.o[t];
+                sh.sum[wave - half][lane] = st.sum;
+            }
+            __syncthreads();
+            if (wave < half) {
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) st.o[t] += sh.o[wave][t][lane];
+                st.sum += sh.sum[wave][lane];
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
     if (wave != 0) return;
     const float sum = kv_row_sum(st.sum);
@@ -655,8 +658,8 @@ __device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &
     }
 }
 
-// Calls in which no request has more than 16 query rows per kv head.  WAVES: 4, or more for few short ranges,
-// which are then not cut, and no join follows.
+// Calls in which no request has more than 16 query rows per kv head.  WAVES: 4; more for few short ranges, 1 for
+// many short ones, neither of which are cut, so that no join follows.
 template <class T, int HD, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_kv_rows(KvAttnArgs a) {
     __shared__ KvRowsLds<HD, WAVES> sh;
