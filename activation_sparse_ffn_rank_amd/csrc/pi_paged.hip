@@ -152,6 +152,13 @@ int launch_attn_hd(int hd, const KvAttnArgs &a, const AttnPlan &g, hipStream_t s
     return launch_attn<T, 256>(a, g, st);
 }
 
+template <int TT>
+int launch_append(const KvAppendArgs &a, hipStream_t st) {
+    const size_t lds = (size_t)TT * (a.hd / 2 + 1) * sizeof(uint32_t);
+    hipLaunchKernelGGL((k_kv_append<TT>), dim3(a.n_kv, (a.n_tokens + TT - 1) / TT), dim3(256), lds, st, a);
+    return hipGetLastError() == hipSuccess ? PI_OK : PI_ERR_HIP;
+}
+
 }  // namespace
 
 extern "C" int pi_kv_step(const pi_kv_tables *t, void *stream) {
@@ -185,10 +192,10 @@ extern "C" int pi_kv_append(const pi_kv_cache *cache, const void *k, int64_t k_t
                    k_token_stride, k_head_stride, v_token_stride, v_head_stride, static_cast<const uint16_t *>(k),
                    static_cast<const uint16_t *>(v), slots, static_cast<uint16_t *>(cache->k_pages),
                    static_cast<uint16_t *>(cache->v_pages)};
-    const size_t lds = (size_t)kKvAppendTokens * (cache->head_dim / 2 + 1) * 4;
-    hipLaunchKernelGGL(k_kv_append, dim3((n_tokens + kKvAppendTokens - 1) / kKvAppendTokens, cache->n_kv), dim3(256), lds,
-                       static_cast<hipStream_t>(stream), a);
-    return hipGetLastError() == hipSuccess ? PI_OK : PI_ERR_HIP;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    // Tiles of 64 tokens, or of 16 where those are fewer workgroups than two per CU (3000 tokens of 2 heads of 256:
+    // 10.6 -> 7.0 us; 64 tokens of 32 heads of 128: 9.3 -> 5.5).
+    return (int64_t)((n_tokens + 63) / 64) * cache->n_kv >= 2 * kCus ? launch_append<64>(a, st) : launch_append<16>(a, st);
 }
 
 extern "C" size_t pi_kv_attn_workspace_bytes(const pi_kv_cache *cache, const pi_kv_batch *batch, int32_t total_q, int32_t n_q) {
