@@ -421,3 +421,81 @@ def test_steps_in_a_replayed_graph_on_another_stream():
                                            a["q_start"].tolist(), a["kv_len"].tolist(), 0.125, 0)
         tol = kv_util.attn_tolerance(want, mag, torch.float16, hd)
         assert bool(((a["out"][:rows].cpu().double() - want).abs() <= tol).all()), it
+
+
+# ------------------------------------------------------------------------------ the kernels' variants by size
+
+@pytest.mark.parametrize("n_q,n_kv,hd,page,dtype,n_req,most", [
+    (13, 13, 64, 16, "f16", 70, 250), (56, 56, 128, 64, "bf16", 20, 18), (24, 12, 128, 16, "f16", 60, 256),
+    (8, 4, 256, 32, "bf16", 140, 90)])
+def test_attn_many_short_ranges(n_q, n_kv, hd, page, dtype, n_req, most):
+    """More workgroups than the chip holds, of at most 256 keys each."""
+    announce(f"kv attn many short heads={n_q}/{n_kv} hd={hd} page={page} {dtype} n_req={n_req} most={most}")
+    rng = random.Random(most)
+    c = kv_util.attn_case(3, [(1, rng.choice((0, 1, most, rng.randint(1, most)))) for _ in range(n_req - 1)] + [(1, most)], n_q, n_kv,
+                          hd, page, dtype)
+    kv_util.past_end(c, math.nan)
+    check_attn(c)
+    check_attn(c, 17, max_kv=256)
+
+
+@pytest.mark.parametrize("n_q,n_kv,hd,page,dtype,lens", [
+    (16, 16, 64, 16, "f16", [(1, 513)]), (4, 2, 64, 256, "bf16", [(1, 1024), (1, 0), (1, 31), (1, 700)]),
+    (32, 32, 128, 16, "bf16", [(1, 512), (1, 1)]), (35, 7, 128, 32, "f16", [(2, 300), (3, 257), (1, 64), (0, 9)]),
+    (64, 64, 128, 64, "f16", [(1, 1000), (1, 5), (1, 999)]), (40, 40, 64, 16, "bf16", [(1, 2000), (1, 1500), (1, 100), (1, 33)])])
+def test_attn_few_short_ranges(n_q, n_kv, hd, page, dtype, lens):
+    """Short ranges with a compute unit for each: read by one workgroup of more waves."""
+    announce(f"kv attn few short heads={n_q}/{n_kv} hd={hd} page={page} {dtype} lens={lens}")
+    c = kv_util.attn_case(hd, lens, n_q, n_kv, hd, page, dtype)
+    kv_util.past_end(c, math.inf)
+    check_attn(c)
+    check_attn(c, 40)
+
+
+@pytest.mark.parametrize("n_q,n_kv,hd,page,dtype,window", [
+    (4, 2, 64, 16, "f16", 0), (2, 2, 128, 32, "bf16", 0), (8, 1, 128, 64, "f16", 3000), (4, 1, 256, 16, "bf16", 0),
+    (6, 2, 256, 256, "f16", 900)])
+def test_attn_long_single_tokens_beside_chunks(n_q, n_kv, hd, page, dtype, window):
+    """Prompt chunks, single tokens whose key ranges are cut, and requests without either, in one call."""
+    lens = [(1, 4500), (180, 400), (1, 2900), (0, 50), (1, 1), (3, 1700), (1, 0), (1, 3000)]
+    announce(f"kv attn long single tokens beside chunks heads={n_q}/{n_kv} hd={hd} page={page} {dtype} window={window}")
+    c = kv_util.attn_case(page, lens, n_q, n_kv, hd, page, dtype)
+    kv_util.past_end(c, math.nan)
+    got = check_attn(c, window, wide=True)
+    assert torch.equal(got, attn(c, window, wide=True)), "the result depends on timing"
+
+
+@pytest.mark.parametrize("bad", (math.nan, math.inf))
+def test_attn_masked_values_beside_chunks(bad):
+    """A value that is not finite reaches exactly the tokens that see its key, chunks and single tokens alike."""
+    lens, window = [(1, 300), (150, 400), (1, 90), (1, 120), (1, 40)], 60
+    for hd, page, dtype in ((64, 16, "bf16"), (128, 64, "f16")):
+        announce(f"kv attn masked values beside chunks hd={hd} page={page} {dtype} {bad}")
+        c = kv_util.attn_case(5, lens, 2, 1, hd, page, dtype)
+        kv_util.past_end(c, bad)
+        spots = {0: (239, 240, 100), 1: (251, 300, 5, 399), 2: (10,), 3: (119,)}
+        for r, js in spots.items():
+            for j in js:
+                c["v"][c["table"][r][j // page]][:, 7, j % page] = bad
+        got = attn(c, window).double()
+        clean = dict(c, v=torch.nan_to_num(c["v"], nan=0.0, posinf=0.0))
+        want, mag = kv_util.attn_reference(c["q"], c["k"], clean["v"], c["table"], c["starts"], c["kv"], c["scale"], window)
+        tol = kv_util.attn_tolerance(want, mag, c["q"].dtype, hd)
+        for r, (n, m) in enumerate(lens):
+            for i in range(n):
+                t, pos = c["starts"][r] + i, m - n + i
+                hit = any(pos - window < j <= pos for j in spots.get(r, ()))
+                rest = torch.arange(hd) != 7
+                assert bool(((got[t] - want[t]).abs() <= tol[t])[:, rest].all()), (r, i)
+                assert bool(torch.isfinite(got[t][:, 7]).all()) == (not hit), (r, i)
+                assert hit or bool(((got[t] - want[t]).abs() <= tol[t])[:, 7].all()), (r, i)
+
+
+def test_attn_windows_past_all_positions():
+    """The largest window is no window, for tokens before position 0 too."""
+    announce("kv attn window 2^31 - 1")
+    for lens in ([(6, 2), (1, 40), (9, 0)], [(40, 30), (1, 5)]):
+        c = kv_util.attn_case(2, lens, 4, 2, 64, 16, "f16")
+        kv_util.past_end(c, math.nan)
+        got = check_attn(c, 2 ** 31 - 1)
+        assert torch.equal(got, attn(c, 0))
