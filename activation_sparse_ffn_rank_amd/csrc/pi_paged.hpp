@@ -688,6 +688,13 @@ struct KvTile {
     static __device__ __forceinline__ int swz_v(int d) { return kUnitsV == 8 ? (d >> 1) & 7 : (d >> 2) & 3; }
 };
 
+// Eight values with those cleared whose bits are set in m.
+__device__ __forceinline__ uint4 kv_clear(uint4 x, uint32_t m) {
+    auto keep = [&](int b) { return (m >> b & 1 ? 0u : 0xffffu) | (m >> b & 2 ? 0u : 0xffff0000u); };
+    x.x &= keep(0), x.y &= keep(2), x.z &= keep(4), x.w &= keep(6);
+    return x;
+}
+
 // 64 lanes x 16 bytes from base + off (per lane) to 1 KB of LDS at byte address `lds`.  The compiler
 // does not see the load in flight: kv_lds_wait before the barrier after which the bytes are read.
 __device__ __forceinline__ void kv_lds_load(const uint16_t *base, uint32_t off, uint32_t lds) {
@@ -708,7 +715,7 @@ __device__ __forceinline__ uint64_t kv_dead_bits(uint32_t m) {
 // beside two chunks of 777, 56 heads of 128: 165 -> 156 us.  Without them the other path stays out of the
 // kernel, whose registers then serve the one loop: a 4096-token chunk 1009 -> 953.)
 template <class T, int HD, bool SMALL, bool MIXED>
-__global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a) {
+__global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_tile(KvAttnArgs a) {
     typedef KvTile<HD> L;
     constexpr int KT = L::kKeys, kSub = KT / 32, kSteps = HD / 16, kTiles = HD / 32;
     // [buffer][K, V]
@@ -845,8 +852,19 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
         kv_lds_wait();
         __syncthreads();                 // block kb is in LDS, and every wave is done with the buffer before it
         if (kb + KT < hi) dead_next = load(kb + KT, buf ^ 1);
+        uint16_t *const sk = s_kv[buf][0], *const sv = s_kv[buf][1];
+        // Values past the request's keys and of missing pages may hold anything and are cleared (0 x infinity would be
+        // NaN), in LDS, by all waves.
+        if (kb + KT > rq.hi || dead != 0) {
+            const uint64_t none = ~kv_bits((uint32_t)min(rq.hi - kb, KT)) | kv_dead_bits(dead);
+            for (int i = threadIdx.x; i < HD * L::kUnitsV; i += 256) {
+                const int d = i / L::kUnitsV, unit = i % L::kUnitsV;
+                uint4 &x = *reinterpret_cast<uint4 *>(sv + d * KT + (unit ^ L::swz_v(d)) * 8);
+                x = kv_clear(x, (uint32_t)(none >> (8 * unit)));
+            }
+            __syncthreads();
+        }
         if (kb >= wave_hi || kb + KT <= wave_lo) continue;
-        const uint16_t *const sk = s_kv[buf][0], *const sv = s_kv[buf][1];
 
         f32x16 s[kSub];
 #pragma unroll
@@ -900,42 +918,33 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
                 part += s[u][i];
             }
         sum += part;
-        // Values past the request's keys and of missing pages may hold anything and are cleared (0 x infinity would be
-        // NaN).  With `careful`, so are those of keys that no row of the wave sees, and those that some rows
-        // see and others do not, and that are not finite, are cleared and added row by row.
+        // With `careful`, values of keys that no row of the wave sees are taken as zero, and so are those that some
+        // rows see and others do not, and that are not finite: those are added row by row.
         uint64_t drop = 0;
         auto v_frag = [&](int t, int j) -> uint4 {
             const int d = 32 * t + col, unit = (2 * j + half) ^ L::swz_v(d);
             return *reinterpret_cast<const uint4 *>(sv + d * KT + unit * 8);
         };
-        auto clear = [&](uint4 x, int j) -> uint4 {
-            const uint32_t m = (uint32_t)(drop >> (16 * j + 8 * half)) & 0xffu;
-            auto keep = [&](int b) { return (m >> b & 1 ? 0u : 0xffffu) | (m >> b & 2 ? 0u : 0xffff0000u); };
-            x.x &= keep(0), x.y &= keep(2), x.z &= keep(4), x.w &= keep(6);
-            return x;
-        };
-        if (edge) {
-            drop = ~kv_bits((uint32_t)min(rq.hi - kb, KT)) | kv_dead_bits(dead);
+        auto clear = [&](uint4 x, int j) -> uint4 { return kv_clear(x, (uint32_t)(drop >> (16 * j + 8 * half))); };
+        if (careful && edge) {
+            drop = ~kv_bits((uint32_t)min(wave_hi - kb, KT)) | kv_bits((uint32_t)min(max(wave_lo - kb, 0), KT));
             uint64_t odd_keys = 0;
-            if (careful) {
-                drop |= ~kv_bits((uint32_t)min(wave_hi - kb, KT)) | kv_bits((uint32_t)min(max(wave_lo - kb, 0), KT));
 #pragma unroll 1
-                for (int j = 0; j < 2 * kSub; ++j) {
-                    uint32_t odd = 0;
+            for (int j = 0; j < 2 * kSub; ++j) {
+                uint32_t odd = 0;
 #pragma unroll 1
-                    for (int t = 0; t < kTiles; ++t) {
-                        const uint4 x = clear(v_frag(t, j), j);
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                for (int t = 0; t < kTiles; ++t) {
+                    const uint4 x = clear(v_frag(t, j), j);
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            if ((w[b] & T::kExpMask & 0xffffu) == (T::kExpMask & 0xffffu)) odd |= 1u << (2 * b);
-                            if ((w[b] & T::kExpMask & 0xffff0000u) == (T::kExpMask & 0xffff0000u)) odd |= 2u << (2 * b);
-                        }
+                    for (int b = 0; b < 4; ++b) {
+                        if ((w[b] & T::kExpMask & 0xffffu) == (T::kExpMask & 0xffffu)) odd |= 1u << (2 * b);
+                        if ((w[b] & T::kExpMask & 0xffff0000u) == (T::kExpMask & 0xffff0000u)) odd |= 2u << (2 * b);
                     }
-                    if (__any(odd != 0)) {
-                        for (int x = 1; x < 32; x <<= 1) odd |= __shfl_xor(odd, x);
-                        odd_keys |= ((uint64_t)(uint32_t)bcast((int)odd, 0) | (uint64_t)(uint32_t)bcast((int)odd, 32) << 8) << (16 * j);
-                    }
+                }
+                if (__any(odd != 0)) {
+                    for (int x = 1; x < 32; x <<= 1) odd |= __shfl_xor(odd, x);
+                    odd_keys |= ((uint64_t)(uint32_t)bcast((int)odd, 0) | (uint64_t)(uint32_t)bcast((int)odd, 32) << 8) << (16 * j);
                 }
             }
             drop |= odd_keys;
@@ -960,16 +969,27 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void k_kv_tile(KvAttnArgs a
                     }
             }
         }
-#pragma unroll
-        for (int j = 0; j < 2 * kSub; ++j) {
+        auto weights = [&](int j) -> uint4 {
             const f32x16 &x = s[j >> 1];
             const int b = 8 * (j & 1);
-            const uint4 pf = make_uint4(kv_pack<T>(x[b], x[b + 1]), kv_pack<T>(x[b + 2], x[b + 3]),
-                                        kv_pack<T>(x[b + 4], x[b + 5]), kv_pack<T>(x[b + 6], x[b + 7]));
-            if (drop >> (16 * j) & 0xffffu) {
+            return make_uint4(kv_pack<T>(x[b], x[b + 1]), kv_pack<T>(x[b + 2], x[b + 3]), kv_pack<T>(x[b + 4], x[b + 5]),
+                              kv_pack<T>(x[b + 6], x[b + 7]));
+        };
+        // (one branch around all of the product, so that its loads run ahead of its MFMAs)
+        if (careful && edge) {
 #pragma unroll
-                for (int t = 0; t < kTiles; ++t) o[t] = T::mfma32(clear(v_frag(t, j), j), pf, o[t]);
-            } else {
+            for (int j = 0; j < 2 * kSub; ++j) {
+                const uint4 pf = weights(j);
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) {
+                    o[t] = T::mfma32(clear(v_frag(t, j), j), pf, o[t]);
+                    __builtin_amdgcn_sched_barrier(0);       // (registers)
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2 * kSub; ++j) {
+                const uint4 pf = weights(j);
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) o[t] = T::mfma32(v_frag(t, j), pf, o[t]);
             }
