@@ -85,7 +85,7 @@ AttnPlan attn_plan(const pi_kv_cache *c, const pi_kv_batch *b, int total_q, int 
     p.tiles = (int)std::min(total_q * group / p.TR + reqs, reqs * ((rows + p.TR - 1) / p.TR));
     p.items = p.tiles;
     p.bytes = 16;
-    // Nothing is cut where there are too few keys for two items, or row tiles to fill the chip many times.
+    // Nothing is cut where there are too few keys for two pieces, or row tiles to fill the chip many times.
     // With few tiles the pieces fill the chip just once (4 x 60k grouped: 84.8 us, and 88.6 with twice as many); with
     // about as many as it holds, finer ones even out their lengths (16 x 2k: 62.6 us, and 66.3 with half as many).
     int target = split_target(c->head_dim);
@@ -99,8 +99,10 @@ AttnPlan attn_plan(const pi_kv_cache *c, const pi_kv_batch *b, int total_q, int 
     // More workgroups than the chip holds, of short ranges each: one wave each, so that it holds four times as many (49
     // requests of up to 18 keys, 56 heads of 128: 32.2 -> 18.5 us).
     p.single = p.TR == kKvRowTile && all > target && b->max_kv <= kKvMinPiece;
-    if (!p.shorts && !p.single && all < 8 * target && b->max_kv >= kv_min_cut(c->head_dim)) {
-        if (2 * all > target) target *= 2;
+    if (2 * all > target && all < 8 * target) target *= 2;
+    // (the tiles of one request alone are all cut in target / all + 1/4: with less than 2 no join is launched)
+    const bool whole = reqs == 1 && 4 * target < 7 * all;
+    if (!p.shorts && !p.single && !whole && all < 8 * target && b->max_kv >= kv_min_cut(c->head_dim)) {
         p.target = target;
         p.items += target / c->n_kv + 2;             // 2: the device sums the work in fp32
         p.slots = std::min(p.items, 2 * target / c->n_kv + 4);

@@ -1,5 +1,6 @@
 // pi_paged.hpp -- gfx950 kernels of the paged key/value cache: block tables (k_kv_tables), cache
-// append (k_kv_append) and attention over the pages (k_kv_rows, k_kv_join).
+// append (k_kv_append) and attention over the pages (k_kv_rows for few query rows, k_kv_tile for many,
+// k_kv_join).
 //
 // Both products of attention run on MFMA with the keys along the rows of the first one,
 //   S^T = K Q^T   (A = K: 16 keys x 32 head dims, B = Q^T: 32 head dims x 16 query rows)
@@ -98,7 +99,8 @@ __device__ __forceinline__ uint32_t kv_block_scan(uint32_t v, uint32_t *part, ui
 // back) that every workgroup makes for itself from the lengths (at most 32 KB from L2), after which
 // the workgroups share out the pages and the rows: nothing waits on another workgroup.  With one
 // workgroup all inputs are read before the first output is written, so a step may run in place.
-// The row sums stay below 2^32: at most 4096 requests of at most 2^19 + 1 counted rows.
+// The row sums stay below 2^32: at most 4096 requests of at most 2^19 + 1 counted rows.  Bound by the
+// latency of its few dependent loads: 64 requests 6.4 us, 1500 with 66 thousand new tokens 9.1 us.
 __global__ __launch_bounds__(kKvTableThreads) void k_kv_tables(KvTablesArgs a) {
     __shared__ uint32_t s_row[PI_KV_MAX_REQ + 1];   // first row
     __shared__ uint32_t s_need[PI_KV_MAX_REQ];      // pages asked for (ended: given back) by the requests before | flags
@@ -419,8 +421,13 @@ struct KvRowsLds {
 };
 
 // One workgroup: one item (16 query rows of one kv head, one key range) of one request; its waves
-// take a part of the range each, 32 keys at a time, straight from the pages into registers.  TR: rows of
-// a split item in the workspace.
+// take a part of the range each, 32 keys at a time, straight from the pages into registers: nothing of K or V
+// is read twice, so LDS would only add a step.  The next block's keys are loaded during the softmax and its values after
+// the second product, 16 KB in flight per wave for heads of 128.  A score more than `lag` powers of two
+// above the running reference moves it; smaller ones do not, so most blocks rescale nothing.  Weights are rounded to
+// the element type for the second product; sums, references and outputs stay in fp32.  Bound by HBM: 16 requests of 2k
+// keys, 32 heads of 128, 275 MB in 58.7 us; 96 heads of 3k, 1.8 GB in 315 us (5.7 TB/s).  TR: rows of a split
+// item in the workspace.
 template <class T, int HD, int TR, int WAVES>
 __device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &it, int h, KvRowsLds<HD, WAVES> &sh) {
     constexpr int kSteps = HD / 32, kTiles = HD / 16, kWaves = WAVES;
@@ -671,13 +678,17 @@ __global__ __launch_bounds__(64 * WAVES) void k_kv_rows(KvAttnArgs a) {
     kv_rows_item<T, HD, kKvRowTile, WAVES>(a, it, h, sh);
 }
 
-// One workgroup: one item of TR = 128 query rows of one kv head, 32 of them per wave, over one key
+// One workgroup: one item of 128 query rows of one kv head, 32 of them per wave, over one key
 // range, KT keys at a time.  K and V of a block go from the pages to LDS without passing registers
 // (16 bytes per lane), the next block's while this one is computed; the waves read them from there
 // as MFMA operands.  Inside a row of either tile the 16-byte units are permuted by the row's number, on
 // the way in, so that the 16 lanes that read the same unit of 16 rows find them in 16 bank groups.
 // The products are those of k_kv_rows on 32x32x16 MFMA: tile row 16s + 8u + 4h + v is key 16s + 8h + 4u
 // + v, so that lane half h holds keys 16s + 8h .. +7 of its query row in accumulators 8s .. 8s+7.
+// Bound by MFMA and softmax together at the clock that the card holds: a 4096-token chunk on 12204 cached
+// keys, 32 heads of 128, 940 to 965 us = 990 TFLOP/s (a library product of 8192^3 reaches 1270); MFMA is busy half of
+// the time, the vector units most of the other half, LDS a quarter, without bank conflicts.  More buffers in
+// flight, other orders of the first product, wave priorities, and sums of the weights by dot products measured no faster.
 template <int HD>
 struct KvTile {
     static constexpr int kKeys = HD == 256 ? 32 : 64;      // 64 KB of LDS for both buffers at most
@@ -1039,9 +1050,10 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
     }
 }
 
-// Joins the split items: a workgroup takes a few rows of one kv head at a time (a row per HD / 4 lanes, 16
+// Joins the split items (1 / l times the sum of the pieces, each scaled to the largest reference): a workgroup takes a few rows of one kv head at a time (a row per HD / 4 lanes, 16
 // bytes each), its four waves a quarter of the chunks each, kDeep of them in flight; the quarters are added in
-// order.  The grid does not depend on how many requests are cut: with none it ends at once.
+// order.  The grid does not depend on how many requests are cut: with none it ends at once.  Bound by latency, 5 to 8
+// us, of which 4 to find that there is nothing to do.
 template <class T, int HD, int TR>
 __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
     constexpr int kLanes = HD / 4, kRows = 64 / kLanes, kDeep = 8, kWaves = 4;

@@ -54,7 +54,7 @@ typedef struct pi_kv_cache {
  * new tokens.  max_q and max_kv bound the lengths on the host (they choose kernels and grids): a
  * request's new tokens past max_q and keys past max_kv are not read, nor keys past max_pages*page.
  * A table entry outside [0, n_pages) is a page without keys.  A request whose q_start range is
- * negative, decreasing or past the packed rows is left out. */
+ * negative, decreasing or past the packed rows is left out, and of ranges that overlap some may be. */
 typedef struct pi_kv_batch {
     int32_t n_req, max_pages, max_q, max_kv;
     int64_t table_stride;          /* entries from one request's table row to the next, >= max_pages */
