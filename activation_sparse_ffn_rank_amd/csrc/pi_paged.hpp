@@ -313,29 +313,43 @@ constexpr int kKvRowWaves = 4;          // waves that share the keys of 16 query
 constexpr int kv_short_waves(int hd) { return hd == 64 ? 16 : 8; }      // ... of a short range
 
 // How key ranges are cut: into pieces of about sum / split_target keys, the sum taken over all requests of row
-// tiles (of TR rows) x keys, so that the pieces fill the chip once.  Returns pieces per key; 0: none is cut.
-template <int TR>
-__device__ __forceinline__ float kv_cut(const KvAttnArgs &a, int lane) {
-    if (!a.split_target) return 0.f;
-    float sum = 0.f;
+// tiles (of TR rows) x keys, so that the pieces fill the chip once; but each piece more writes and reads the
+// partial sums of all their rows once more, so no further than that costs what it saves: a range of m keys in n pieces
+// takes a m / n + b n, least at n = sqrt(m a / b), with a = 20 ns a key (heads of 256: 60) and b = 8 bytes an
+// element at 5 TB/s (300 new tokens on 1000 keys, 96 heads of 128: 85 us cut in four, 41 uncut by this rule).  Tiles of 16
+// rows never reach that.
+struct KvCut {
+    float rate;          // pieces per key; 0: none is cut
+    float most2;         // square of pieces, at most, per key
+};
+template <int HD, int TR>
+__device__ __forceinline__ KvCut kv_cut(const KvAttnArgs &a, int lane) {
+    if (!a.split_target) return {0.f, 0.f};
+    float sum = 0.f, rows = 0.f;
     for (int r0 = 0; r0 < a.n_req; r0 += 64) {
-        float x = 0.f;
+        float x = 0.f, y = 0.f;
         if (r0 + lane < a.n_req) {
             const KvReq q = kv_req(a, r0 + lane);
             x = (float)((q.rows + TR - 1) / TR) * (float)(q.hi - q.lo);
+            y = q.hi - q.lo >= kv_min_cut(HD) ? (float)q.rows : 0.f;
         }
         sum += wave_sum(x);
+        if (TR != kKvRowTile) rows += wave_sum(y);
     }
-    return sum > 0.f ? (float)a.split_target / (sum * (float)a.n_kv) : 0.f;
+    if (!(sum > 0.f)) return {0.f, 0.f};
+    return {(float)a.split_target / (sum * (float)a.n_kv),
+            (HD == 256 ? 0.06f : 0.02f) * 5e6f / (8.f * (HD + 2) * fmaxf(rows, 1.f) * (float)a.n_kv)};
 }
 
 // Keys per piece of a request of `keys` keys.  A range is cut in c only from c - 1/4 times the aim on: a little
-// more than the chip holds at once costs a second round, and partial sums are written and read.  Hence the
-// pieces of all cut ranges number at most (2 / 1.75) * split_target.
-template <int HD>
-__device__ __forceinline__ int kv_piece(int keys, float cut) {
+// more than the chip holds at once costs a second round.  Hence the pieces of all cut ranges number at most
+// (2 / 1.75) * split_target.
+template <int HD, int TR>
+__device__ __forceinline__ int kv_piece(int keys, KvCut cut) {
     if (keys < kv_min_cut(HD)) return max(keys, 1);
-    const int n = min((int)fminf((float)keys * cut + 0.25f, 65536.f), (keys + kKvMinPiece / 2) / kKvMinPiece);
+    float aim = (float)keys * cut.rate + 0.25f;
+    if (TR != kKvRowTile) aim = fminf(aim, __builtin_amdgcn_sqrtf((float)keys * cut.most2));
+    const int n = min((int)fminf(aim, 65536.f), (keys + kKvMinPiece / 2) / kKvMinPiece);
     return n > 1 ? ((keys + n - 1) / n + 63) & ~63 : max(keys, 1);
 }
 
@@ -349,7 +363,7 @@ struct KvItem {
 };
 // ROWS > 0 counts groups of ROWS rows of the cut requests instead (for the join; split is then the group).
 template <int HD, int TR, int ROWS>
-__device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, float cut_rate, int lane) {
+__device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, KvCut aim, int lane) {
     KvItem it;
     it.r = -1;
     int base = 0, base_slot = 0;
@@ -359,7 +373,7 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, float c
         if (r0 + lane < a.n_req) {
             q = kv_req(a, r0 + lane);
             tiles = (q.rows + TR - 1) / TR;
-            piece = kv_piece<HD>(q.hi - q.lo, cut_rate);
+            piece = kv_piece<HD, TR>(q.hi - q.lo, aim);
             splits = max((q.hi - q.lo + piece - 1) / piece, 1);
         }
         const int cut = splits > 1 ? tiles * splits : 0;
@@ -673,7 +687,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_kv_rows(KvAttnArgs a) {
     __shared__ KvRowsLds<HD, WAVES> sh;
     const int lane = threadIdx.x & 63;
     const int h = blockIdx.x % a.n_kv, want = blockIdx.x / a.n_kv;
-    const KvItem it = kv_item<HD, kKvRowTile, 0>(a, want, kv_cut<kKvRowTile>(a, lane), lane);
+    const KvItem it = kv_item<HD, kKvRowTile, 0>(a, want, kv_cut<HD, kKvRowTile>(a, lane), lane);
     if (it.r < 0) return;
     kv_rows_item<T, HD, kKvRowTile, WAVES>(a, it, h, sh);
 }
@@ -738,7 +752,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 31, half = lane >> 5;
     const int h = blockIdx.x % a.n_kv, want = blockIdx.x / a.n_kv;
-    const KvItem it = kv_item<HD, kKvWideTile, 0>(a, want, kv_cut<kKvWideTile>(a, lane), lane);
+    const KvItem it = kv_item<HD, kKvWideTile, 0>(a, want, kv_cut<HD, kKvWideTile>(a, lane), lane);
     if (it.r < 0) return;
     const KvReq &rq = it.q;
     if constexpr (MIXED) {
@@ -1060,7 +1074,7 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
     __shared__ f32x4 s_o[kWaves][64];
     __shared__ float s_ref[kWaves][64], s_sum[kWaves][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const float cut = kv_cut<TR>(a, lane);
+    const KvCut cut = kv_cut<HD, TR>(a, lane);
     const int64_t stride = (int64_t)a.n_kv * (TR * (HD + 2));
     const int d = (lane % kLanes) * 4;
     for (int u = blockIdx.x;; u += gridDim.x) {
