@@ -48,12 +48,13 @@ NUM_XCC = 8                    # ... in 8 XCDs
 
 
 def kernel_sources_sha256() -> str:
-    """Digest of the HIP sources; hardware byte counts taken on other sources are stale."""
+    """Digest of the HIP sources of the measured kernels (the paged cache's files build into units of their own);
+    hardware byte counts taken on other sources are stale."""
     import hashlib
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "activation_sparse_ffn_rank_amd", "csrc")
     for name in sorted(os.listdir(csrc)):
-        if name.endswith((".hip", ".hpp")):
+        if name.endswith((".hip", ".hpp")) and not name.startswith("pi_paged"):
             h.update(name.encode())
             with open(os.path.join(csrc, name), "rb") as fh:
                 h.update(fh.read())

@@ -71,3 +71,18 @@ def test_kernel_prefixes_name_the_profiled_kernels():
                     + bench.ffn_kernel_names(h_kind, B, cfg, synth)[1])
         for pre in prefixes:
             assert any(k.startswith(pre) for k in rec["kernels"]), (rec["workload"], pre)
+
+
+def test_traffic_records_match_the_sources():
+    """Every committed byte count was taken on the sources of the sparse-FFN kernels as they stand."""
+    import glob
+    import json
+
+    sys.path.insert(0, ROOT)
+    import bench
+    for path in glob.glob(os.path.join(ROOT, "profiles", "traffic_*.json")):
+        with open(path) as fh:
+            rec = json.load(fh)
+        assert rec["sources_sha256"] == bench.kernel_sources_sha256(), path
+        for name in rec["kernels"]:
+            assert bench.measured_traffic(rec["workload"], [name]) is not None
