@@ -2,8 +2,9 @@
 the attention that reads it (argument marshalling only, as in ``_abi``).
 
 What only a tensor knows -- element type, shape, strides -- is checked here and refused with the same
-codes that the library uses (``PiError``); the library checks the rest.  The descriptors keep the
-tensors that they name alive.
+codes that the library uses (``PiError``); the library checks the rest.  A tensor that is not on the
+pages' device has no address there (``PI_ERR_NULL``).  The descriptors keep the tensors that they name
+alive.
 """
 from __future__ import annotations
 
@@ -11,7 +12,7 @@ import ctypes
 
 import torch
 
-from ._abi import PI_ERR_DTYPE, PI_ERR_NULL, PI_ERR_SHAPE, PI_OK, PiError, _check, lib
+from ._abi import PI_ERR_DTYPE, PI_ERR_NULL, PI_ERR_SHAPE, PI_ERR_WORKSPACE, PI_OK, PiError, _check, lib
 
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: torch.cuda.current_stream(device).cuda_stream)
 
@@ -100,10 +101,21 @@ def _rows(fn: str, t, cache: pi_kv_cache) -> tuple[int, int, int, int, int]:
     return t.data_ptr(), ts if n > 1 else heads * hd, hs if heads > 1 else hd, n, heads
 
 
-def _raw_stream(stream, t) -> int:
-    """As ``_abi._stream``, the current stream taken from the tensor's device (a cheaper query)."""
+def _device(fn: str, *tensors) -> int:
+    """Index of the one device that holds all of them (-1: host memory)."""
+    d = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != d:
+            raise PiError(fn, PI_ERR_NULL)
+    return d
+
+
+def _raw_stream(fn: str, stream, device: int) -> int:
+    """As ``_abi._stream``, the current stream of the device that holds the tensors."""
+    if device < 0:
+        raise PiError(fn, PI_ERR_NULL)
     if stream is None:
-        return _current_stream(t.device.index or 0) if t.is_cuda else 0
+        return _current_stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -120,6 +132,7 @@ def make_kv_cache(k_pages: torch.Tensor, v_pages: torch.Tensor) -> pi_kv_cache:
     if tuple(v_pages.shape) != (n_pages, n_kv, hd, page):
         raise PiError("make_kv_cache", PI_ERR_SHAPE)
     c = pi_kv_cache(n_pages, n_kv, page, hd, KV_DTYPES[k_pages.dtype], k_pages.data_ptr(), v_pages.data_ptr())
+    c._device = _device("make_kv_cache", k_pages, v_pages)
     c._keep = (k_pages, v_pages)
     return c
 
@@ -133,6 +146,7 @@ def make_kv_batch(block_table: torch.Tensor, q_start: torch.Tensor, kv_len: torc
     n = kv_len.shape[0]
     table, cols, stride = _table(fn, block_table, n)
     b = pi_kv_batch(n, cols, max_q, max_kv, stride, table, _ints(fn, q_start, n + 1), length)
+    b._device = _device(fn, block_table, q_start, kv_len)
     b._keep = (block_table, q_start, kv_len)
     return b
 
@@ -152,12 +166,13 @@ def make_kv_tables(cached: torch.Tensor, fresh: torch.Tensor, free_ring: torch.T
                      _ints(fn, pool, 2), table, _ints(fn, q_start, n + 1), _ints(fn, kv_len, n), _ints(fn, cached_next, n),
                      rows, _ints(fn, pool_next, 2), _ints(fn, counts, 4))
     t._keep = (cached, fresh, free_ring, pool, block_table, q_start, kv_len, cached_next, slots, pool_next, counts)
+    t._device = _device(fn, *t._keep)
     return t
 
 
 def pi_kv_step(tables: pi_kv_tables, stream=None) -> None:
     """One step of the block tables: pages for the new tokens, pages of ended requests back, slot map."""
-    _check("pi_kv_step", kv_lib().pi_kv_step(tables, _raw_stream(stream, tables._keep[0])))
+    _check("pi_kv_step", kv_lib().pi_kv_step(tables, _raw_stream("pi_kv_step", stream, tables._device)))
 
 
 def pi_kv_append(cache: pi_kv_cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
@@ -167,7 +182,10 @@ def pi_kv_append(cache: pi_kv_cache, k: torch.Tensor, v: torch.Tensor, slots: to
     vp, vt, vh, n_v, heads_v = _rows(fn, v, cache)
     if heads != cache.n_kv or heads_v != heads or n_v != n:
         raise PiError(fn, PI_ERR_SHAPE)
-    rc = kv_lib().pi_kv_append(cache, kp, kt, kh, vp, vt, vh, _ints(fn, slots, n), n, _raw_stream(stream, k))
+    at, device = _ints(fn, slots, n), cache._device
+    if k.get_device() != device or v.get_device() != device or slots.get_device() != device:
+        raise PiError(fn, PI_ERR_NULL)
+    rc = kv_lib().pi_kv_append(cache, kp, kt, kh, vp, vt, vh, at, n, _raw_stream(fn, stream, device))
     if rc != PI_OK:
         raise PiError(fn, rc)
 
@@ -185,7 +203,15 @@ def pi_kv_attn(cache: pi_kv_cache, batch: pi_kv_batch, q: torch.Tensor, out: tor
     op, ot, oh, n_o, heads_o = _rows(fn, out, cache)
     if n_o != n or heads_o != heads:
         raise PiError(fn, PI_ERR_SHAPE)
-    wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
-    rc = kv_lib().pi_kv_attn(cache, batch, qp, qt, qh, op, ot, oh, n, heads, scale, window, wp, wn, _raw_stream(stream, q))
+    device, wp, wn = cache._device, None, 0                  # (the library refuses a missing workspace if it needs one)
+    if ws is not None:
+        if not ws.is_contiguous():
+            raise PiError(fn, PI_ERR_WORKSPACE)
+        if ws.get_device() != device:
+            raise PiError(fn, PI_ERR_NULL)
+        wp, wn = ws.data_ptr(), ws.nbytes
+    if q.get_device() != device or out.get_device() != device or batch._device != device:
+        raise PiError(fn, PI_ERR_NULL)
+    rc = kv_lib().pi_kv_attn(cache, batch, qp, qt, qh, op, ot, oh, n, heads, scale, window, wp, wn, _raw_stream(fn, stream, device))
     if rc != PI_OK:
         raise PiError(fn, rc)

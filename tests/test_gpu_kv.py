@@ -499,3 +499,32 @@ def test_attn_windows_past_all_positions():
         kv_util.past_end(c, math.nan)
         got = check_attn(c, 2 ** 31 - 1)
         assert torch.equal(got, attn(c, 0))
+
+
+def test_tensors_of_other_devices_are_refused():
+    """Host tensors in a call on device pages; and calls without rows, which need no workspace."""
+    announce("kv refusals of host tensors")
+    c = kv_util.attn_case(1, [(1, 20), (2, 30)], 4, 2, 64, 16, "f16")
+    k, v, q = c["k"].cuda(), c["v"].cuda(), c["q"].cuda()
+    cache = pi.make_kv_cache(k, v)
+    batch = pi.make_kv_batch(dev(c["table"]), dev(c["starts"]), dev(c["kv"]), max_q=2, max_kv=30)
+    ws = torch.empty(pi.pi_kv_attn_workspace_bytes(cache, batch, 3, 4), dtype=torch.uint8, device="cuda")
+    out, new, slots = torch.empty_like(q), torch.zeros((3, 2, 64), dtype=torch.float16, device="cuda"), dev([0, 1, 2])
+
+    def refused(fn):
+        with pytest.raises(pi.PiError) as e:
+            fn()
+        return e.value.code
+    assert refused(lambda: pi.make_kv_cache(k, c["v"])) == -1
+    assert refused(lambda: pi.make_kv_batch(dev(c["table"]), dev(c["starts"]), torch.tensor(c["kv"], dtype=torch.int32), max_q=2,
+                                            max_kv=30)) == -1
+    assert refused(lambda: pi.pi_kv_append(cache, new, new, slots.cpu())) == -1
+    assert refused(lambda: pi.pi_kv_append(cache, new.cpu(), new, slots)) == -1
+    assert refused(lambda: pi.pi_kv_attn(cache, batch, c["q"], out, ws, scale=0.1)) == -1
+    assert refused(lambda: pi.pi_kv_attn(cache, batch, q, out.cpu(), ws, scale=0.1)) == -1
+    assert refused(lambda: pi.pi_kv_attn(cache, batch, q, out, ws.cpu(), scale=0.1)) == -1
+    assert refused(lambda: pi.pi_kv_attn(cache, batch, q, out, None, scale=0.1)) == -5
+    pi.pi_kv_attn(cache, batch, q[:0], out[:0], None, scale=0.1)
+    pi.pi_kv_append(cache, new[:0], new[:0], slots[:0])
+    torch.cuda.synchronize()
+    assert torch.equal(k.cpu(), c["k"]) and torch.equal(v.cpu(), c["v"])

@@ -152,6 +152,22 @@ def test_descriptors_reject():
         assert code(lambda: _kv.make_kv_tables(*bad)) == _abi.PI_ERR_DTYPE
 
 
+def test_host_tensors_are_refused():
+    """Tensors in host memory, and workspaces whose bytes do not lie together."""
+    k, v = torch.zeros(4, 2, 16, 64, dtype=torch.float16), torch.zeros(4, 2, 64, 16, dtype=torch.float16)
+    ints = lambda n: torch.zeros(n, dtype=torch.int32)
+    c = _kv.make_kv_cache(k, v)
+    b = _kv.make_kv_batch(torch.zeros(3, 5, dtype=torch.int32), ints(4), ints(3), max_q=1, max_kv=80)
+    t = _kv.make_kv_tables(ints(3), ints(3), ints(7), ints(2), torch.zeros(3, 5, dtype=torch.int32), 16, ints(4), ints(3), ints(3),
+                           ints(20), ints(2), ints(4))
+    x, ws = torch.zeros(3, 2, 64, dtype=torch.float16), torch.zeros(1 << 16, dtype=torch.uint8)
+    for stream in (None, 0):
+        assert code(lambda: _kv.pi_kv_step(t, stream)) == _abi.PI_ERR_NULL
+        assert code(lambda: _kv.pi_kv_append(c, x, x, ints(3), stream)) == _abi.PI_ERR_NULL
+        assert code(lambda: _kv.pi_kv_attn(c, b, x, x, ws, scale=1.0, stream=stream)) == _abi.PI_ERR_NULL
+    assert code(lambda: _kv.pi_kv_attn(c, b, x, x, ws[:1].expand(1 << 20), scale=1.0, stream=0)) == _abi.PI_ERR_WORKSPACE
+
+
 def test_step_reference_by_hand():
     # page 4; request 0 grows into a second page, 1 ends, 2 is a prompt of 6, 3 finds no page left
     got = kv_util.step_reference([4, 5, 0, 8], [1, -1, 6, 1], [9, 8, 7, -1, -1, -1, -1, -1, -1, -1], [0, 3],
