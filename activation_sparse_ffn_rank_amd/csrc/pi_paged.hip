@@ -62,8 +62,8 @@ int check_strides(const void *p, int64_t ts, int64_t hs) {
 }
 
 // Rows per workgroup by the most query rows that a request can have per kv head: single tokens and
-// drafts of small groups go to k_kv_rows, whose waves share out the keys; the rest, and whatever
-// single tokens run beside it, to k_kv_tile.
+// drafts go to k_kv_rows, whose waves share out the keys; the rest, and whatever single tokens run
+// beside it, to k_kv_tile.
 struct AttnPlan {
     int TR;
     bool shorts;     // k_kv_rows with more waves per workgroup
@@ -79,7 +79,13 @@ struct AttnPlan {
 AttnPlan attn_plan(const pi_kv_cache *c, const pi_kv_batch *b, int total_q, int n_q) {
     AttnPlan p{};
     const int64_t group = n_q / c->n_kv, rows = std::min(b->max_q, total_q) * group, reqs = std::min(b->n_req, total_q);
-    p.TR = rows <= kKvRowTile ? kKvRowTile : kKvWideTile;
+    // Up to 128 rows fit one wide tile, but tiles of 16, whose waves share out the keys, are done sooner where the latency
+    // of the blocks counts and reading the keys again, from L2, does not: up to 64 MB of that (2 x 3 tokens on 600 keys, 8
+    // kv heads of 64 for 128: 17.0 us wide, 8.3 so; 1 x 8 on 8000: 20.0 wide, 26.1 so), and up to 512 MB for heads of 256,
+    // whose wide tiles run one wave per SIMD (16 x 4 on 8000 keys: 69.6 wide, 59.5 so).
+    const double again = 4.0 * reqs * ((rows + kKvRowTile - 1) / kKvRowTile) * c->n_kv * b->max_kv * c->head_dim;
+    const bool narrow = rows <= kKvRowTile || (rows <= kKvWideTile && again <= (c->head_dim == 256 ? 512 << 20 : 64 << 20));
+    p.TR = narrow ? kKvRowTile : kKvWideTile;
     // on average, requests of fewer than half of max_q tokens: some of them have few rows
     p.mixed = (int64_t)2 * total_q < (int64_t)b->max_q * b->n_req;
     p.tiles = (int)std::min(total_q * group / p.TR + reqs, reqs * ((rows + p.TR - 1) / p.TR));

@@ -680,7 +680,7 @@ __device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &
     }
 }
 
-// Calls in which no request has more than 16 query rows per kv head.  WAVES: 4; more for few short ranges, 1 for
+// Calls in which no request has many query rows per kv head.  WAVES: 4; more for few short ranges, 1 for
 // many short ones, neither of which are cut, so that no join follows.
 template <class T, int HD, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_kv_rows(KvAttnArgs a) {
