@@ -93,7 +93,8 @@ AttnPlan attn_plan(const pi_kv_cache *c, const pi_kv_batch *b, int total_q, int 
     p.bytes = 16;
     // Nothing is cut where there are too few keys for two pieces, or row tiles to fill the chip many times.
     // With few tiles the pieces fill the chip just once (4 x 60k grouped: 84.8 us, and 88.6 with twice as many); with
-    // about as many as it holds, finer ones even out their lengths (16 x 2k: 62.6 us, and 66.3 with half as many).
+    // about as many as it holds, finer ones even out their lengths (16 x 2k: 62.6 us, and 66.3 with half as many), unless
+    // the tiles are wide: their partial sums cost more (2048 tokens on 8000 keys, 32 heads of 128: 349 us cut in two, 259 not).
     int target = split_target(c->head_dim);
     const int64_t all = (int64_t)p.tiles * c->n_kv;
     // With a CU for each range, more waves in one workgroup read a short one sooner than its pieces are joined (1 x 513,
@@ -105,7 +106,7 @@ AttnPlan attn_plan(const pi_kv_cache *c, const pi_kv_batch *b, int total_q, int 
     // More workgroups than the chip holds, of short ranges each: one wave each, so that it holds four times as many (49
     // requests of up to 18 keys, 56 heads of 128: 32.2 -> 18.5 us).
     p.single = p.TR == kKvRowTile && all > target && b->max_kv <= kKvMinPiece;
-    if (2 * all > target && all < 8 * target) target *= 2;
+    if (narrow && 2 * all > target && all < 8 * target) target *= 2;
     // (the tiles of one request alone are all cut in target / all + 1/4: with less than 2 no join is launched)
     const bool whole = reqs == 1 && 4 * target < 7 * all;
     if (!p.shorts && !p.single && !whole && all < 8 * target && b->max_kv >= kv_min_cut(c->head_dim)) {
@@ -129,10 +130,13 @@ int launch_join(const KvAttnArgs &a, const AttnPlan &p, hipStream_t st) {
 
 template <class T, int HD, bool MIXED>
 void launch_tile(const KvAttnArgs &a, dim3 grid, hipStream_t st) {
-    if ((1 << a.page_log) < KvTile<HD>::kKeys)
-        hipLaunchKernelGGL((k_kv_tile<T, HD, true, MIXED>), grid, dim3(256), 0, st, a);
+    constexpr int kKeys = KvTile<HD, 16>::kKeys;
+    if (a.page_log == 4)
+        hipLaunchKernelGGL((k_kv_tile<T, HD, 16, MIXED>), grid, dim3(256), 0, st, a);
+    else if (a.page_log == 5 || kKeys == 32)
+        hipLaunchKernelGGL((k_kv_tile<T, HD, 32, MIXED>), grid, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((k_kv_tile<T, HD, false, MIXED>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((k_kv_tile<T, HD, kKeys, MIXED>), grid, dim3(256), 0, st, a);
 }
 
 template <class T, int HD>

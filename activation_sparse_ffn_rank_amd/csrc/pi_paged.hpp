@@ -703,14 +703,21 @@ __global__ __launch_bounds__(64 * WAVES) void k_kv_rows(KvAttnArgs a) {
 // keys, 32 heads of 128, 940 to 965 us = 990 TFLOP/s (a library product of 8192^3 reaches 1270); MFMA is busy half of
 // the time, the vector units most of the other half, LDS a quarter, without bank conflicts.  More buffers in
 // flight, other orders of the first product, wave priorities, and sums of the weights by dot products measured no faster.
-template <int HD>
+// P: positions that a page gives to a block, the page's or all of the block's.  K lies in LDS as [key][HD], V as in the
+// pages, [page][HD][P], so that every load reads 1 KB of one page from a scalar address (with V gathered as [HD][key],
+// pages of 16 took 16% longer than pages of 64: 2048 tokens on 8000 keys, 32 heads of 128; now 263 and 259 us).
+template <int HD, int P>
 struct KvTile {
     static constexpr int kKeys = HD == 256 ? 32 : 64;      // 64 KB of LDS for both buffers at most
-    static constexpr int kUnitsK = HD / 8, kUnitsV = kKeys / 8;
+    static constexpr int kUnitsK = HD / 8, kUnitsV = P / 8;      // 16-byte units of a row
     static constexpr int kLoads = kKeys * HD * 2 / 1024 / 4;     // 1 KB loads per wave and operand
     static constexpr int kBytes = kKeys * HD * 2;                // of one operand's tile
     static __device__ __forceinline__ int swz_k(int key) { return kUnitsK >= 16 ? key & 15 : (key >> 1) & 7; }
-    static __device__ __forceinline__ int swz_v(int d) { return kUnitsV == 8 ? (d >> 1) & 7 : (d >> 2) & 3; }
+    static __device__ __forceinline__ int swz_v(int d) { return kUnitsV == 8 ? (d >> 1) & 7 : kUnitsV == 4 ? (d >> 2) & 3 : (d >> 3) & 1; }
+    // Where values 8u .. 8u+7 of row d of V^T lie.
+    static __device__ __forceinline__ int at_v(int d, int u) {
+        return (u / kUnitsV) * (HD * P) + d * P + ((u % kUnitsV) ^ swz_v(d)) * 8;
+    }
 };
 
 // Eight values with those cleared whose bits are set in m.
@@ -735,13 +742,13 @@ __device__ __forceinline__ uint64_t kv_dead_bits(uint32_t m) {
     return f * 0xffffull;
 }
 
-// SMALL: pages of fewer positions than a block has keys.  MIXED: requests of few rows, single tokens beside
+// P: as in KvTile.  MIXED: requests of few rows, single tokens beside
 // prompt chunks among them, are taken too, by kv_rows_item: they wait for memory, not for MFMA.  (14 single tokens
 // beside two chunks of 777, 56 heads of 128: 165 -> 156 us.  Without them the other path stays out of the
 // kernel, whose registers then serve the one loop: a 4096-token chunk 1009 -> 953.)
-template <class T, int HD, bool SMALL, bool MIXED>
+template <class T, int HD, int P, bool MIXED>
 __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_tile(KvAttnArgs a) {
-    typedef KvTile<HD> L;
+    typedef KvTile<HD, P> L;
     constexpr int KT = L::kKeys, kSub = KT / 32, kSteps = HD / 16, kTiles = HD / 32;
     // [buffer][K, V]
     __shared__ __align__(16) union {
@@ -794,15 +801,13 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
     // where this lane's 16 bytes of each load come from, inside a page
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t *)&s_kv[0][0][0];
     uint32_t off_k[L::kLoads], off_v[L::kLoads];
-    int unit_v[L::kLoads];
 #pragma unroll
     for (int i = 0; i < L::kLoads; ++i) {
         const int u = (wave * L::kLoads + i) * 64 + lane;
-        const int key = u / L::kUnitsK, d = u / L::kUnitsV;
+        const int key = u / L::kUnitsK, d = u / L::kUnitsV % HD;
         const int first = (wave * L::kLoads + i) * 64 / L::kUnitsK;
         off_k[i] = (uint32_t)(((key - first) * HD + 8 * ((u % L::kUnitsK) ^ L::swz_k(key))) * 2);
-        unit_v[i] = (u % L::kUnitsV) ^ L::swz_v(d);
-        off_v[i] = (uint32_t)((d << a.page_log) + (SMALL ? 0 : 8 * unit_v[i])) * 2;
+        off_v[i] = (uint32_t)((d << a.page_log) + 8 * ((u % L::kUnitsV) ^ L::swz_v(d))) * 2;
     }
 
     const int *const tab = a.table + (int64_t)it.r * a.table_stride;
@@ -823,27 +828,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
         const int id_safe = bad ? 0 : ids;               // something in bounds; its keys are masked
         const uint64_t bads = __ballot(bad);
         const uint32_t dst = lds0 + buf * 2 * L::kBytes + wave * L::kLoads * 1024;
-        if (SMALL) {
-#pragma unroll
-            for (int j = 0; j < KT / 16; ++j)
-                if (bads >> (((kb + 16 * j) >> a.page_log) - tab0) & 1) dead |= 1u << j;
-#pragma unroll
-            for (int i = 0; i < L::kLoads; ++i) {
-                const int k0 = kb + (wave * L::kLoads + i) * 64 / L::kUnitsK;
-                const int64_t id = bcast(id_safe, (k0 >> a.page_log) - tab0);
-                kv_lds_load(a.k + id * page_elems + head_elems + (int64_t)(k0 & (page - 1)) * HD, off_k[i], dst + i * 1024);
-            }
-#pragma unroll
-            for (int i = 0; i < L::kLoads; ++i) {
-                // the units of a V^T row come from several pages: 64-bit addresses per lane
-                const int k0 = kb + 8 * unit_v[i];
-                const int64_t id = __shfl(id_safe, (k0 >> a.page_log) - tab0);
-                const uint16_t *src = a.v + id * page_elems + head_elems + (k0 & (page - 1));
-                src = reinterpret_cast<const uint16_t *>(reinterpret_cast<const char *>(src) + off_v[i]);
-                asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src),
-                             "s"(dst + L::kBytes + i * 1024) : "memory", "m0");
-            }
-        } else {
+        if constexpr (P == KT) {                         // one page
             const int64_t id = bcast(id_safe, p0 - tab0);
             if (bads >> (p0 - tab0) & 1) dead = 15u;
             const uint16_t *const kp = a.k + id * page_elems + head_elems + (int64_t)(kb & (page - 1)) * HD;
@@ -853,6 +838,21 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
                 kv_lds_load(kp + (wave * L::kLoads + i) * 512, off_k[i], dst + i * 1024);
 #pragma unroll
             for (int i = 0; i < L::kLoads; ++i) kv_lds_load(vp, off_v[i], dst + L::kBytes + i * 1024);
+        } else {
+#pragma unroll
+            for (int j = 0; j < KT / P; ++j)
+                if (bads >> (p0 - tab0 + j) & 1) dead |= ((1u << (P / 16)) - 1) << (j * (P / 16));
+#pragma unroll
+            for (int i = 0; i < L::kLoads; ++i) {
+                const int k0 = (wave * L::kLoads + i) * 64 / L::kUnitsK;
+                const int64_t id = bcast(id_safe, p0 - tab0 + k0 / P);
+                kv_lds_load(a.k + id * page_elems + head_elems + (k0 % P) * HD, off_k[i], dst + i * 1024);
+            }
+#pragma unroll
+            for (int i = 0; i < L::kLoads; ++i) {
+                const int64_t id = bcast(id_safe, p0 - tab0 + (wave * L::kLoads + i) * 64 / (HD * L::kUnitsV));
+                kv_lds_load(a.v + id * page_elems + head_elems, off_v[i], dst + L::kBytes + i * 1024);
+            }
         }
         return dead;
     };
@@ -882,9 +882,9 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
         // NaN), in LDS, by all waves.
         if (kb + KT > rq.hi || dead != 0) {
             const uint64_t none = ~kv_bits((uint32_t)min(rq.hi - kb, KT)) | kv_dead_bits(dead);
-            for (int i = threadIdx.x; i < HD * L::kUnitsV; i += 256) {
-                const int d = i / L::kUnitsV, unit = i % L::kUnitsV;
-                uint4 &x = *reinterpret_cast<uint4 *>(sv + d * KT + (unit ^ L::swz_v(d)) * 8);
+            for (int i = threadIdx.x; i < HD * (KT / 8); i += 256) {
+                const int d = i / (KT / 8), unit = i % (KT / 8);
+                uint4 &x = *reinterpret_cast<uint4 *>(sv + L::at_v(d, unit));
                 x = kv_clear(x, (uint32_t)(none >> (8 * unit)));
             }
             __syncthreads();
@@ -947,8 +947,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
         // rows see and others do not, and that are not finite: those are added row by row.
         uint64_t drop = 0;
         auto v_frag = [&](int t, int j) -> uint4 {
-            const int d = 32 * t + col, unit = (2 * j + half) ^ L::swz_v(d);
-            return *reinterpret_cast<const uint4 *>(sv + d * KT + unit * 8);
+            return *reinterpret_cast<const uint4 *>(sv + L::at_v(32 * t + col, 2 * j + half));
         };
         auto clear = [&](uint4 x, int j) -> uint4 { return kv_clear(x, (uint32_t)(drop >> (16 * j + 8 * half))); };
         if (careful && edge) {
@@ -990,7 +989,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int d = 32 * t + 8 * (i >> 2) + d0 + (i & 3);
-                        o[t][i] += w * (float)__builtin_bit_cast(typename T::e, sv[d * KT + ((j >> 3) ^ L::swz_v(d)) * 8 + (j & 7)]);
+                        o[t][i] += w * (float)__builtin_bit_cast(typename T::e, sv[L::at_v(d, j >> 3) + (j & 7)]);
                     }
             }
         }
