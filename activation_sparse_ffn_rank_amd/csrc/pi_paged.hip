@@ -94,7 +94,8 @@ AttnPlan attn_plan(const pi_kv_cache *c, const pi_kv_batch *b, int total_q, int 
     // Nothing is cut where there are too few keys for two pieces, or row tiles to fill the chip many times.
     // With few tiles the pieces fill the chip just once (4 x 60k grouped: 84.8 us, and 88.6 with twice as many); with
     // about as many as it holds, finer ones even out their lengths (16 x 2k: 62.6 us, and 66.3 with half as many), unless
-    // the tiles are wide: their partial sums cost more (2048 tokens on 8000 keys, 32 heads of 128: 349 us cut in two, 259 not).
+    // the tiles are wide: their partial sums cost more (2048 tokens on 8000 keys, 32 heads of 128: 349 us cut in two,
+    // 259 not).
     int target = split_target(c->head_dim);
     const int64_t all = (int64_t)p.tiles * c->n_kv;
     // With a CU for each range, more waves in one workgroup read a short one sooner than its pieces are joined (1 x 513,

@@ -436,7 +436,7 @@ struct KvRowsLds {
 
 // One workgroup: one item (16 query rows of one kv head, one key range) of one request; its waves
 // take a part of the range each, 32 keys at a time, straight from the pages into registers: nothing of K or V
-// is read twice, so LDS would only add a step.  The next block's keys are loaded during the softmax and its values after
+// is read twice by one tile, so LDS would only add a step.  The next block's keys are loaded during the softmax and its values after
 // the second product, 16 KB in flight per wave for heads of 128.  A score more than `lag` powers of two
 // above the running reference moves it; smaller ones do not, so most blocks rescale nothing.  Weights are rounded to
 // the element type for the second product; sums, references and outputs stay in fp32.  Bound by HBM: 16 requests of 2k
@@ -700,9 +700,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_kv_rows(KvAttnArgs a) {
 // The products are those of k_kv_rows on 32x32x16 MFMA: tile row 16s + 8u + 4h + v is key 16s + 8h + 4u
 // + v, so that lane half h holds keys 16s + 8h .. +7 of its query row in accumulators 8s .. 8s+7.
 // Bound by MFMA and softmax together at the clock that the card holds: a 4096-token chunk on 12204 cached
-// keys, 32 heads of 128, 940 to 965 us = 990 TFLOP/s (a library product of 8192^3 reaches 1270); MFMA is busy half of
-// the time, the vector units most of the other half, LDS a quarter, without bank conflicts.  More buffers in
-// flight, other orders of the first product, wave priorities, and sums of the weights by dot products measured no faster.
+// keys, 32 heads of 128, 910 to 960 us = 1000 to 1050 TFLOP/s (a library product of 8192^3 reaches 1270); MFMA is
+// busy half of the time, the vector units most of the other half, LDS a quarter.  More buffers in flight, other
+// orders of the first product, wave priorities, and sums of the weights by dot products measured no faster.
 // P: positions that a page gives to a block, the page's or all of the block's.  K lies in LDS as [key][HD], V as in the
 // pages, [page][HD][P], so that every load reads 1 KB of one page from a scalar address (with V gathered as [HD][key],
 // pages of 16 took 16% longer than pages of 64: 2048 tokens on 8000 keys, 32 heads of 128; now 263 and 259 us).
@@ -744,8 +744,8 @@ __device__ __forceinline__ uint64_t kv_dead_bits(uint32_t m) {
 
 // P: as in KvTile.  MIXED: requests of few rows, single tokens beside
 // prompt chunks among them, are taken too, by kv_rows_item: they wait for memory, not for MFMA.  (14 single tokens
-// beside two chunks of 777, 56 heads of 128: 165 -> 156 us.  Without them the other path stays out of the
-// kernel, whose registers then serve the one loop: a 4096-token chunk 1009 -> 953.)
+// beside two chunks of 777, 56 heads of 128: 165 us without this path, 156 with it, 147 now.  Without such
+// requests it stays out of the kernel, whose registers then serve the one loop: a 4096-token chunk 1009 -> 953.)
 template <class T, int HD, int P, bool MIXED>
 __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_tile(KvAttnArgs a) {
     typedef KvTile<HD, P> L;
@@ -1063,10 +1063,10 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
     }
 }
 
-// Joins the split items (1 / l times the sum of the pieces, each scaled to the largest reference): a workgroup takes a few rows of one kv head at a time (a row per HD / 4 lanes, 16
-// bytes each), its four waves a quarter of the chunks each, kDeep of them in flight; the quarters are added in
-// order.  The grid does not depend on how many requests are cut: with none it ends at once.  Bound by latency, 5 to 8
-// us, of which 4 to find that there is nothing to do.
+// Joins the split items, each scaled to the largest reference, and divides by the row's sum: a workgroup takes a
+// few rows of one kv head at a time (a row per HD / 4 lanes, 16 bytes each), its four waves a quarter of the pieces
+// each, kDeep of them in flight; the quarters are added in order.  The grid does not depend on how many requests are
+// cut: with none it ends at once.  Bound by latency, 5 to 8 us, of which 4 to find that there is nothing to do.
 template <class T, int HD, int TR>
 __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
     constexpr int kLanes = HD / 4, kRows = 64 / kLanes, kDeep = 8, kWaves = 4;
