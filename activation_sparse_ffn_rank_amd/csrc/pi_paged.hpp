@@ -869,6 +869,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[t][i] = 0.f;
     ref = -INFINITY, sum = 0.f;
+    none = true;                         // (a second pass starts over in the table too)
     uint32_t dead_next = 0;
     int buf = 0;
     if (lo < hi) dead_next = load(lo, 0);

@@ -528,3 +528,24 @@ def test_tensors_of_other_devices_are_refused():
     pi.pi_kv_append(cache, new[:0], new[:0], slots[:0])
     torch.cuda.synchronize()
     assert torch.equal(k.cpu(), c["k"]) and torch.equal(v.cpu(), c["v"])
+
+
+@pytest.mark.parametrize("n_q,n_kv,hd,page,dtype", [(4, 4, 64, 16, "f16"), (2, 1, 128, 16, "bf16"), (2, 2, 256, 16, "bf16"),
+                                                    (2, 2, 128, 32, "f16")])
+def test_attn_masked_values_far_into_the_table(n_q, n_kv, hd, page, dtype):
+    """Values that are not finite at the end of more pages than one read of the table holds: tokens before them are as if
+    they were not there."""
+    n, m = 300, 5000
+    announce(f"kv attn masked values far into the table heads={n_q}/{n_kv} hd={hd} page={page} {dtype}")
+    c = kv_util.attn_case(11, [(n, m)], n_q, n_kv, hd, page, dtype)
+    kv_util.past_end(c, math.nan)
+    want, mag = kv_util.attn_reference(c["q"], c["k"], c["v"], c["table"], c["starts"], c["kv"], c["scale"], 0)
+    tol = kv_util.attn_tolerance(want, mag, c["q"].dtype, hd, keys=m)
+    spot = m - 100
+    c["v"][c["table"][0][spot // page]][:, ::5, spot % page] = math.inf
+    got = attn(c)
+    before = n - 100
+    assert bool(((got[:before].double() - want[:before]).abs() <= tol[:before]).all())
+    clean = torch.arange(hd) % 5 != 0
+    assert bool(((got.double() - want).abs() <= tol)[..., clean].all())
+    assert not torch.isfinite(got[before:][..., ~clean]).any()
