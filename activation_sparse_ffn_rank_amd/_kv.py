@@ -2,7 +2,8 @@
 the attention that reads it (argument marshalling only, as in ``_abi``).
 
 What only a tensor knows -- element type, shape, strides -- is checked here and refused with the same
-codes that the library uses (``PiError``); the library checks the rest.  A tensor that is not on the
+codes that the library uses (``PiError``), and so are numbers that do not fit its 32-bit arguments, which
+ctypes would take modulo 2^32; the library checks the rest.  A tensor that is not on the
 pages' device has no address there (``PI_ERR_NULL``).  The descriptors keep the tensors that they name
 alive.
 """
@@ -63,6 +64,16 @@ def kv_lib() -> ctypes.CDLL:
     return _kv_lib
 
 
+def _fits(*numbers: int) -> bool:
+    """Whether all of them are int32."""
+    return all(-2 ** 31 <= x < 2 ** 31 for x in numbers)
+
+
+def _int32(fn: str, *numbers: int) -> None:
+    if not _fits(*numbers):
+        raise PiError(fn, PI_ERR_SHAPE)
+
+
 def _ints(fn: str, t, n: int) -> int:
     """Address of a contiguous int32 tensor [n] (-1: any size)."""
     if t is None:
@@ -71,6 +82,8 @@ def _ints(fn: str, t, n: int) -> int:
         raise PiError(fn, PI_ERR_DTYPE)
     if t.dim() != 1 or (n >= 0 and t.shape[0] != n) or not t.is_contiguous():
         raise PiError(fn, PI_ERR_SHAPE)
+    if n < 0:
+        _int32(fn, t.shape[0])
     return t.data_ptr()
 
 
@@ -82,6 +95,7 @@ def _table(fn: str, t, n_req: int) -> tuple[int, int, int]:
         raise PiError(fn, PI_ERR_DTYPE)
     if t.dim() != 2 or t.shape[0] != n_req or t.shape[1] < 1 or t.stride(1) != 1:
         raise PiError(fn, PI_ERR_SHAPE)
+    _int32(fn, t.shape[1])
     return t.data_ptr(), t.shape[1], t.stride(0) if n_req > 1 else t.shape[1]
 
 
@@ -95,7 +109,7 @@ def _rows(fn: str, t, cache: pi_kv_cache) -> tuple[int, int, int, int, int]:
         raise PiError(fn, PI_ERR_SHAPE)
     n, heads, hd = t.shape
     ts, hs, one = t.stride()
-    if hd != cache.head_dim or one != 1:
+    if hd != cache.head_dim or one != 1 or n >= 2 ** 31 or heads >= 2 ** 31:
         raise PiError(fn, PI_ERR_SHAPE)
     # the stride along an axis of one element is never used
     return t.data_ptr(), ts if n > 1 else heads * hd, hs if heads > 1 else hd, n, heads
@@ -131,6 +145,7 @@ def make_kv_cache(k_pages: torch.Tensor, v_pages: torch.Tensor) -> pi_kv_cache:
     n_pages, n_kv, page, hd = k_pages.shape
     if tuple(v_pages.shape) != (n_pages, n_kv, hd, page):
         raise PiError("make_kv_cache", PI_ERR_SHAPE)
+    _int32("make_kv_cache", n_pages, n_kv, page, hd)
     c = pi_kv_cache(n_pages, n_kv, page, hd, KV_DTYPES[k_pages.dtype], k_pages.data_ptr(), v_pages.data_ptr())
     c._device = _device("make_kv_cache", k_pages, v_pages)
     c._keep = (k_pages, v_pages)
@@ -145,6 +160,7 @@ def make_kv_batch(block_table: torch.Tensor, q_start: torch.Tensor, kv_len: torc
     length = _ints(fn, kv_len, -1)
     n = kv_len.shape[0]
     table, cols, stride = _table(fn, block_table, n)
+    _int32(fn, max_q, max_kv)
     b = pi_kv_batch(n, cols, max_q, max_kv, stride, table, _ints(fn, q_start, n + 1), length)
     b._device = _device(fn, block_table, q_start, kv_len)
     b._keep = (block_table, q_start, kv_len)
@@ -161,6 +177,7 @@ def make_kv_tables(cached: torch.Tensor, fresh: torch.Tensor, free_ring: torch.T
     at = _ints(fn, cached, -1)
     n = cached.shape[0]
     table, cols, stride = _table(fn, block_table, n)
+    _int32(fn, page)
     ring, rows = _ints(fn, free_ring, -1), _ints(fn, slots, -1)
     t = pi_kv_tables(n, page, free_ring.shape[0], cols, slots.shape[0], stride, at, _ints(fn, fresh, n), ring,
                      _ints(fn, pool, 2), table, _ints(fn, q_start, n + 1), _ints(fn, kv_len, n), _ints(fn, cached_next, n),
@@ -192,7 +209,7 @@ def pi_kv_append(cache: pi_kv_cache, k: torch.Tensor, v: torch.Tensor, slots: to
 
 def pi_kv_attn_workspace_bytes(cache: pi_kv_cache, batch: pi_kv_batch, total_q: int, n_q: int) -> int:
     """Bytes of workspace pi_kv_attn needs for this batch, packed rows and query heads (0: invalid)."""
-    return int(kv_lib().pi_kv_attn_workspace_bytes(cache, batch, total_q, n_q))
+    return int(kv_lib().pi_kv_attn_workspace_bytes(cache, batch, total_q, n_q)) if _fits(total_q, n_q) else 0
 
 
 def pi_kv_attn(cache: pi_kv_cache, batch: pi_kv_batch, q: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, *, scale: float,
@@ -201,7 +218,7 @@ def pi_kv_attn(cache: pi_kv_cache, batch: pi_kv_batch, q: torch.Tensor, out: tor
     fn = "pi_kv_attn"
     qp, qt, qh, n, heads = _rows(fn, q, cache)
     op, ot, oh, n_o, heads_o = _rows(fn, out, cache)
-    if n_o != n or heads_o != heads:
+    if n_o != n or heads_o != heads or not -2 ** 31 <= window < 2 ** 31:
         raise PiError(fn, PI_ERR_SHAPE)
     device, wp, wn = cache._device, None, 0                  # (the library refuses a missing workspace if it needs one)
     if ws is not None:

@@ -191,3 +191,34 @@ def test_attn_reference_by_hand():
     assert torch.allclose(out[1], torch.full((1, 64), 5.0).double())
     out, _ = kv_util.attn_reference(q, k, v, [[0]], [0, 2], [1], 1.0, 0)       # the first token has no position
     assert out[0].abs().max() == 0 and torch.allclose(out[1], torch.ones(1, 64).double())
+
+
+@pytest.mark.parametrize("big", (2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 40, -2 ** 31 - 1, -2 ** 32 + 5))
+def test_numbers_past_32_bits_are_refused(big):
+    """What does not fit the library's 32-bit arguments is refused, and not taken modulo 2^32."""
+    k, v = torch.zeros(4, 2, 16, 64, dtype=torch.float16), torch.zeros(4, 2, 64, 16, dtype=torch.float16)
+    ints = lambda n: torch.zeros(n, dtype=torch.int32)
+    c, table = _kv.make_kv_cache(k, v), torch.zeros(3, 5, dtype=torch.int32)
+    b = _kv.make_kv_batch(table, ints(4), ints(3), max_q=1, max_kv=80)
+    x, ws = torch.zeros(3, 2, 64, dtype=torch.float16), torch.zeros(1 << 16, dtype=torch.uint8)
+    assert code(lambda: _kv.make_kv_batch(table, ints(4), ints(3), max_q=big, max_kv=80)) == _abi.PI_ERR_SHAPE
+    assert code(lambda: _kv.make_kv_batch(table, ints(4), ints(3), max_q=1, max_kv=big)) == _abi.PI_ERR_SHAPE
+    assert code(lambda: _kv.make_kv_tables(ints(3), ints(3), ints(7), ints(2), table, big, ints(4), ints(3), ints(3), ints(20),
+                                           ints(2), ints(4))) == _abi.PI_ERR_SHAPE
+    assert code(lambda: _kv.pi_kv_attn(c, b, x, x, ws, scale=1.0, window=big, stream=0)) == _abi.PI_ERR_SHAPE
+    assert _kv.pi_kv_attn_workspace_bytes(c, b, big, 2) == 0 and _kv.pi_kv_attn_workspace_bytes(c, b, 3, big) == 0
+    if big < 0:
+        return
+    # lengths of tensors (no memory behind them)
+    many, rows = torch.empty(big, dtype=torch.int32, device="meta"), x[:1].expand(big, 2, 64)
+    assert code(lambda: _kv.pi_kv_append(c, rows, rows, many, 0)) == _abi.PI_ERR_SHAPE
+    assert code(lambda: _kv.pi_kv_attn(c, b, rows, rows, ws, scale=1.0, stream=0)) == _abi.PI_ERR_SHAPE
+    assert code(lambda: _kv.make_kv_batch(table[:, :1].expand(3, 1), ints(4), many, max_q=1, max_kv=80)) == _abi.PI_ERR_SHAPE
+    pages = lambda *shape: torch.empty(shape, dtype=torch.float16, device="meta")
+    assert code(lambda: _kv.make_kv_cache(pages(big, 2, 16, 64), pages(big, 2, 64, 16))) == _abi.PI_ERR_SHAPE
+    wide = torch.empty((3, big), dtype=torch.int32, device="meta")
+    assert code(lambda: _kv.make_kv_batch(wide, ints(4), ints(3), max_q=1, max_kv=80)) == _abi.PI_ERR_SHAPE
+    for at in (2, 9):
+        args = [ints(3), ints(3), ints(7), ints(2), table, 16, ints(4), ints(3), ints(3), ints(20), ints(2), ints(4)]
+        args[at] = many
+        assert code(lambda: _kv.make_kv_tables(*args)) == _abi.PI_ERR_SHAPE
