@@ -15,6 +15,7 @@ import torch
 
 from ._abi import PI_ERR_DTYPE, PI_ERR_NULL, PI_ERR_SHAPE, PI_ERR_WORKSPACE, PI_OK, PiError, _check, lib
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 PI_KV_F16, PI_KV_BF16 = 1, 2
@@ -125,12 +126,20 @@ def _device(fn: str, *tensors) -> int:
 
 
 def _raw_stream(fn: str, stream, device: int) -> int:
-    """As ``_abi._stream``, the current stream of the device that holds the tensors."""
+    """As ``_abi._stream``, but the current stream of the device that holds the tensors."""
     if device < 0:
         raise PiError(fn, PI_ERR_NULL)
     if stream is None:
         return _current_stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _call(device: int, fn, *args) -> int:
+    """The library's call with `device` current: the default stream (address 0) is the current device's."""
+    if _current_device() == device:
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
 
 
 def make_kv_cache(k_pages: torch.Tensor, v_pages: torch.Tensor) -> pi_kv_cache:
@@ -189,7 +198,8 @@ def make_kv_tables(cached: torch.Tensor, fresh: torch.Tensor, free_ring: torch.T
 
 def pi_kv_step(tables: pi_kv_tables, stream=None) -> None:
     """One step of the block tables: pages for the new tokens, pages of ended requests back, slot map."""
-    _check("pi_kv_step", kv_lib().pi_kv_step(tables, _raw_stream("pi_kv_step", stream, tables._device)))
+    stream = _raw_stream("pi_kv_step", stream, tables._device)
+    _check("pi_kv_step", _call(tables._device, kv_lib().pi_kv_step, tables, stream))
 
 
 def pi_kv_append(cache: pi_kv_cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
@@ -202,7 +212,8 @@ def pi_kv_append(cache: pi_kv_cache, k: torch.Tensor, v: torch.Tensor, slots: to
     at, device = _ints(fn, slots, n), cache._device
     if k.get_device() != device or v.get_device() != device or slots.get_device() != device:
         raise PiError(fn, PI_ERR_NULL)
-    rc = kv_lib().pi_kv_append(cache, kp, kt, kh, vp, vt, vh, at, n, _raw_stream(fn, stream, device))
+    stream = _raw_stream(fn, stream, device)
+    rc = _call(device, kv_lib().pi_kv_append, cache, kp, kt, kh, vp, vt, vh, at, n, stream)
     if rc != PI_OK:
         raise PiError(fn, rc)
 
@@ -229,6 +240,7 @@ def pi_kv_attn(cache: pi_kv_cache, batch: pi_kv_batch, q: torch.Tensor, out: tor
         wp, wn = ws.data_ptr(), ws.nbytes
     if q.get_device() != device or out.get_device() != device or batch._device != device:
         raise PiError(fn, PI_ERR_NULL)
-    rc = kv_lib().pi_kv_attn(cache, batch, qp, qt, qh, op, ot, oh, n, heads, scale, window, wp, wn, _raw_stream(fn, stream, device))
+    stream = _raw_stream(fn, stream, device)
+    rc = _call(device, kv_lib().pi_kv_attn, cache, batch, qp, qt, qh, op, ot, oh, n, heads, scale, window, wp, wn, stream)
     if rc != PI_OK:
         raise PiError(fn, rc)

@@ -222,3 +222,52 @@ def test_numbers_past_32_bits_are_refused(big):
         args = [ints(3), ints(3), ints(7), ints(2), table, 16, ints(4), ints(3), ints(3), ints(20), ints(2), ints(4)]
         args[at] = many
         assert code(lambda: _kv.make_kv_tables(*args)) == _abi.PI_ERR_SHAPE
+
+
+class _OnDevice1(torch.Tensor):
+    """Host memory that says it is on device 1."""
+    def get_device(self):
+        return 1
+
+
+@pytest.mark.parametrize("current", (0, 1))
+def test_calls_run_on_the_device_of_the_tensors(monkeypatch, current):
+    """With another device current, a call is made with the tensors' device current, and it is set back."""
+    at, calls = [current], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, at[0] = at[0], self.index
+
+        def __exit__(self, *exc):
+            at[0] = self.before
+
+    class Lib:
+        def __getattr__(self, name):
+            def call(*args):
+                calls.append((name, at[0]))
+                return _abi.PI_OK if len(calls) % 2 else _abi.PI_ERR_HIP      # the second call of each fails
+            return call
+
+    monkeypatch.setattr(_kv, "_current_device", lambda: at[0], raising=False)
+    monkeypatch.setattr(_kv, "_current_stream", lambda device: 0)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(_kv, "_kv_lib", Lib())
+    here = lambda t: t.as_subclass(_OnDevice1)
+    ints = lambda *n: here(torch.zeros(n, dtype=torch.int32))
+    half = lambda *n: here(torch.zeros(n, dtype=torch.float16))
+    cache = _kv.make_kv_cache(half(4, 2, 16, 64), half(4, 2, 64, 16))
+    batch = _kv.make_kv_batch(ints(3, 5), ints(4), ints(3), max_q=1, max_kv=80)
+    tables = _kv.make_kv_tables(ints(3), ints(3), ints(7), ints(2), ints(3, 5), 16, ints(4), ints(3), ints(3), ints(20), ints(2),
+                                ints(4))
+    for name, fn in (("pi_kv_step", lambda: _kv.pi_kv_step(tables)),
+                     ("pi_kv_append", lambda: _kv.pi_kv_append(cache, half(3, 2, 64), half(3, 2, 64), ints(3))),
+                     ("pi_kv_attn", lambda: _kv.pi_kv_attn(cache, batch, half(3, 2, 64), half(3, 2, 64), ints(64), scale=1.0))):
+        del calls[:]
+        fn()
+        assert at == [current]
+        assert code(fn) == _abi.PI_ERR_HIP
+        assert calls == [(name, 1), (name, 1)] and at == [current]
