@@ -728,9 +728,10 @@ __device__ __forceinline__ uint4 kv_clear(uint4 x, uint32_t m) {
 }
 
 // 64 lanes x 16 bytes from base + off (per lane) to 1 KB of LDS at byte address `lds`.  The compiler
-// does not see the load in flight: kv_lds_wait before the barrier after which the bytes are read.
+// does not see the load in flight: kv_lds_wait before the barrier after which the bytes are read.  (m0 is an
+// operand, so that the compiler writes it: as a reserved register it may not be clobbered by the statement.)
 __device__ __forceinline__ void kv_lds_load(const uint16_t *base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ void kv_lds_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 

@@ -4,6 +4,7 @@ import ctypes
 import math
 import os
 import re
+import subprocess
 
 import pytest
 import torch
@@ -271,3 +272,14 @@ def test_calls_run_on_the_device_of_the_tensors(monkeypatch, current):
         assert at == [current]
         assert code(fn) == _abi.PI_ERR_HIP
         assert calls == [(name, 1), (name, 1)] and at == [current]
+
+
+@pytest.mark.parametrize("text,ok", [('asm volatile("s_mov_b32 m0, %0" ::"s"(x) : "m0");', False),
+                                     ('asm volatile("s_nop 0" ::"{m0}"(x));', True)])
+def test_build_refuses_clobbers_of_reserved_registers(tmp_path, text, ok):
+    """The flags that the kernels are built with end the build at an asm statement that clobbers m0."""
+    src = tmp_path / "t.hip"
+    src.write_text('#include <hip/hip_runtime.h>\n__global__ void k(int x) { ' + text + ' }\n')
+    res = subprocess.run([build.HIPCC, *build.FLAGS, "--cuda-device-only", "-S", str(src), "-o", str(tmp_path / "t.s")],
+                         capture_output=True, text=True)
+    assert (res.returncode == 0) == ok, res.stderr
