@@ -61,6 +61,18 @@ int check_strides(const void *p, int64_t ts, int64_t hs) {
     return PI_OK;
 }
 
+// Whether two of the rows [hd] at t * ts + h * hs, t < n, h < heads, share an element.
+bool rows_overlap(int64_t ts, int64_t hs, int n, int heads, int hd) {
+    if ((n > 1 && ts < hd) || (heads > 1 && hs < hd)) return true;
+    if (n < 2 || heads < 2) return false;
+    if (ts / hs >= heads) return false;              // whole tokens after one another
+    for (int h = 1; h < heads; ++h) {                // a row h heads on, and the nearest ones t tokens on
+        const __int128 x = (__int128)h * hs, t = x / ts;
+        if ((t < n && x - t * ts < hd) || (t + 1 < n && (t + 1) * ts - x < hd)) return true;
+    }
+    return false;
+}
+
 // Rows per workgroup by the most query rows that a request can have per kv head: single tokens and
 // drafts go to k_kv_rows, whose waves share out the keys; the rest, and whatever single tokens run
 // beside it, to k_kv_tile.
@@ -227,6 +239,7 @@ extern "C" int pi_kv_attn(const pi_kv_cache *cache, const pi_kv_batch *batch, co
     if (window < 0 || !(scale > 0.f) || !std::isfinite(scale)) return PI_ERR_SHAPE;
     if ((rc = check_strides(q, q_token_stride, q_head_stride)) || (rc = check_strides(out, out_token_stride, out_head_stride)))
         return rc;
+    if (rows_overlap(out_token_stride, out_head_stride, total_q, n_q, cache->head_dim)) return PI_ERR_SHAPE;
     const AttnPlan g = attn_plan(cache, batch, total_q, n_q);
     if (!ws || ws_bytes < g.bytes) return PI_ERR_WORKSPACE;
     if (!aligned16(ws)) return PI_ERR_ALIGN;

@@ -105,7 +105,8 @@ int pi_kv_append(const pi_kv_cache *cache, const void *k, int64_t k_token_stride
                  int32_t n_tokens, void *stream);
 
 /* q, out: [total_q][n_q][head_dim], strides in elements (multiples of 8, rows 16-byte aligned); n_q a
- * multiple of n_kv; window 0 = all keys.  Rows that belong to no request are not written.  The
+ * multiple of n_kv; window 0 = all keys; scale finite and above zero.  Rows of q may overlap, rows of
+ * out may not, nor out an input.  Rows that belong to no request are not written.  The
  * workspace (16-byte aligned, no zero fill) holds the partial sums of long key ranges; the size call
  * returns 0 on invalid arguments.  Results do not depend on timing (fixed summation orders). */
 size_t pi_kv_attn_workspace_bytes(const pi_kv_cache *cache, const pi_kv_batch *batch, int32_t total_q, int32_t n_q);

@@ -283,3 +283,28 @@ def test_build_refuses_clobbers_of_reserved_registers(tmp_path, text, ok):
     res = subprocess.run([build.HIPCC, *build.FLAGS, "--cuda-device-only", "-S", str(src), "-o", str(tmp_path / "t.s")],
                          capture_output=True, text=True)
     assert (res.returncode == 0) == ok, res.stderr
+
+
+def test_outputs_whose_rows_overlap_are_refused(L):
+    """Rows of the output that share elements would be written by several workgroups, in any order."""
+    def call(ot, oh, total=4, n_q=32, qt=0, qh=0):
+        return L.pi_kv_attn(cache(), batch(), A, qt, qh, A, ot, oh, total, n_q, 0.1, 0, 0, 0, None)
+    fine = _abi.PI_ERR_WORKSPACE                   # refused later, for the missing workspace
+    # (rows of queries may be shared: only reads)
+    assert call(4096, 128) == fine and call(4096, 128, qt=8, qh=0) == fine
+    assert call(128, 512) == fine and call(128, 520) == fine                  # heads outermost
+    assert call(0, 128, total=1) == fine and call(136, 0, n_q=8, total=1) == _abi.PI_ERR_SHAPE
+    for ot, oh in ((0, 128), (4096, 0), (120, 4096), (4096, 120), (0, 0), (128, 128), (4088, 128), (128, 504), (2048, 128),
+                   (1 << 62, 0)):
+        assert call(ot, oh) == _abi.PI_ERR_SHAPE, (ot, oh)
+    assert call(1 << 62, 128) == fine and call(128, 1 << 62) == fine
+    # interleaved: distinct as long as no multiple of one stride meets one of the other
+    assert call(3 * 128, 2 * 128, total=2, n_q=8) == fine
+    assert call(3 * 128, 2 * 128, total=3, n_q=8) == _abi.PI_ERR_SHAPE        # 2 x 3 = 3 x 2
+    assert call(17 * 128, 2 * 128, total=2, n_q=8) == fine and call(15 * 128, 2 * 128, total=2, n_q=8) == fine
+    # against every pair of rows
+    for ot in range(64, 900, 64):
+        for oh in range(64, 900, 64):
+            at = sorted(t * ot + h * oh for t in range(3) for h in range(8))
+            want = _abi.PI_ERR_SHAPE if min(b - a for a, b in zip(at, at[1:])) < 128 else fine
+            assert call(ot, oh, total=3, n_q=8) == want, (ot, oh)
