@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import activation_sparse_ffn_rank_amd as pi
+from activation_sparse_ffn_rank_amd import _kv
 import kv_util
 from gpu_util import announce
 
@@ -549,3 +550,105 @@ def test_attn_masked_values_far_into_the_table(n_q, n_kv, hd, page, dtype):
     clean = torch.arange(hd) % 5 != 0
     assert bool(((got.double() - want).abs() <= tol)[..., clean].all())
     assert not torch.isfinite(got[before:][..., ~clean]).any()
+
+
+# ------------------------------------------------------------------------------ tables longer than one read of 64 entries
+
+def look_at(c, r, i, j):
+    """Token i of request r asks for key j: its score there is about 12, and elsewhere of the order of 1."""
+    n_kv, page, hd = c["k"].shape[1:]
+    key = c["k"][c["table"][r][j // page], :, j % page].float() * (12 / math.sqrt(hd))
+    c["q"][c["starts"][r] + i] = key.repeat_interleave(c["q"].shape[1] // n_kv, 0).to(c["q"].dtype)
+
+
+def shared_pages_case(seed, lens, n_q, n_kv, hd, page, dtype):
+    """Requests whose tables name the same pages, each in an order of its own (long caches in little memory)."""
+    most = max(m for _, m in lens)
+    c = kv_util.attn_case(seed, [(0, most)] + [(n, 0) for n, _ in lens], n_q, n_kv, hd, page, dtype, extra_pages=0)
+    rng, cols = random.Random(seed), kv_util.ceil_div(most, page)
+    c["table"] = [rng.sample(range(cols), kv_util.ceil_div(m, page)) for _, m in lens]
+    c["table"] = [row + [-1] * (cols - len(row)) for row in c["table"]]
+    c["starts"], c["kv"] = c["starts"][1:], [m for _, m in lens]
+    return c
+
+
+def attn_uncut(c, window=0):
+    """The call, on bounds with which no key range is cut: an item, or a quarter of one, has more pages than one read of
+    its table."""
+    n, (n_pages, n_kv, page, hd) = [b - a for a, b in zip(c["starts"], c["starts"][1:])], c["k"].shape
+    dtype = {"f16": pi.PI_KV_F16, "bf16": pi.PI_KV_BF16}[c["dtype"]]
+    cache = _kv.pi_kv_cache(n_pages, n_kv, page, hd, dtype, 16, 16)
+    batch = _kv.pi_kv_batch(len(n), len(c["table"][0]), max(n), max(c["kv"]), len(c["table"][0]), 16, 16, 16)
+    assert pi.pi_kv_attn_workspace_bytes(cache, batch, *c["q"].shape[:2]) == 16, "key ranges are cut"
+    return attn(c, window)
+
+
+def reference_of(c, picks, heads, window):
+    """(rows, query heads, output, tolerance) of tokens `picks` = (request, token), for some kv heads."""
+    group = c["q"].shape[1] // c["k"].shape[1]
+    # a token is a request of one token, without the keys behind it
+    kv = [c["kv"][r] - (c["starts"][r + 1] - c["starts"][r]) + i + 1 for r, i in picks]
+    rows, qh = [c["starts"][r] + i for r, i in picks], [h * group + g for h in heads for g in range(group)]
+    want, mag = kv_util.attn_reference(c["q"][rows][:, qh], c["k"][:, heads], c["v"][:, heads], [c["table"][r] for r, _ in picks],
+                                       list(range(len(picks) + 1)), kv, c["scale"], window)
+    return rows, qh, want, kv_util.attn_tolerance(want, mag, c["q"].dtype, c["q"].shape[2], partial=20.0, keys=max(kv))
+
+
+def check_some(c, got, picks, heads, window=0):
+    rows, qh, want, tol = reference_of(c, picks, heads, window)
+    err = (got[rows][:, qh].double() - want).abs()
+    assert bool((err <= tol).all()), f"worst {float((err / tol).max()):.3f} of the tolerance"
+
+
+@pytest.mark.parametrize("n_q,n_kv,hd,page,dtype,m", [
+    (64, 64, 256, 16, "bf16", 1500), (64, 64, 256, 32, "f16", 2500), (100, 100, 128, 16, "f16", 1500), (100, 100, 128, 32, "bf16", 2500),
+    (150, 150, 64, 16, "bf16", 1500), (150, 150, 64, 64, "f16", 4600)])
+def test_attn_chunk_on_a_table_of_several_reads(n_q, n_kv, hd, page, dtype, m):
+    """A chunk whose tiles walk more than 64 pages, uncut; then with a missing page behind the 64th; then with values
+    that are not finite, which take the tiles through their keys a second time."""
+    n, heads, cols = 300, [0, n_kv // 2, n_kv - 1], kv_util.ceil_div(m, page)
+    announce(f"kv attn chunk, {cols} pages, heads={n_q}/{n_kv} hd={hd} page={page} {dtype}")
+    c = kv_util.attn_case(m, [(n, m)], n_q, n_kv, hd, page, dtype)
+    kv_util.past_end(c, math.nan)
+    picks = [(0, i) for i in (0, 1, 40, 127, 128, 190, 199, 200, 255, 256, 298, 299)]
+    for at, (_, i) in enumerate(picks):            # keys of the first read, and of the second one
+        look_at(c, 0, i, (3 * at + 1) * page + at if at % 2 else 65 * page + 3 * at)
+    for window in (0, 65 * page):
+        check_some(c, attn_uncut(c, window), picks, heads, window)
+
+    gone = dict(c, table=[list(c["table"][0])])
+    gone["table"][0][66] = -1
+    for window in (0, m - 67 * page - 20):         # seen by the first tokens, and not by the last ones
+        check_some(gone, attn_uncut(gone, window), picks, heads, window)
+
+    rows, qh, want, tol = reference_of(c, picks, heads, 0)
+    spot = m - 100
+    bad = dict(c, v=c["v"].clone())
+    bad["v"][c["table"][0][spot // page]][:, ::5, spot % page] = math.inf
+    got = attn_uncut(bad)[rows][:, qh]
+    near = (got.double() - want).abs() <= tol
+    clean = torch.arange(hd) % 5 != 0
+    before = torch.tensor([m - n + i < spot for _, i in picks])
+    assert bool(near[before].all()) and bool(near[..., clean].all())
+    assert not torch.isfinite(got[~before][..., ~clean]).any()
+
+
+@pytest.mark.parametrize("n_q,n_kv,hd,page,dtype,n_req,m", [
+    (64, 64, 128, 16, "f16", 64, 4400), (128, 64, 64, 16, "bf16", 96, 4400), (64, 64, 256, 16, "f16", 32, 4400),
+    (40, 40, 128, 32, "bf16", 103, 8500)])
+@pytest.mark.parametrize("chunk", (1, 200))
+def test_attn_single_tokens_on_tables_of_several_reads(n_q, n_kv, hd, page, dtype, n_req, m, chunk):
+    """Single tokens, alone or beside a chunk, whose waves walk more than 64 pages each, with a missing page behind the
+    64th of a wave."""
+    lens = [(chunk, m)] + [(1, m - 7 * r % 90) for r in range(1, n_req)]
+    announce(f"kv attn {n_req} requests on {m} keys, chunk={chunk} heads={n_q}/{n_kv} hd={hd} page={page} {dtype}")
+    c = shared_pages_case(m, lens, n_q, n_kv, hd, page, dtype)
+    picks = [(0, chunk - 1)] + [(r, 0) for r in (1, 2, 3, n_req // 2, n_req - 3, n_req - 2, n_req - 1)]
+    for r, i in picks:
+        part = (kv_util.ceil_div(lens[r][1], 4) + 31) & ~31             # keys of a wave
+        assert part > 65 * page + 8
+        look_at(c, r, i, r % 3 * part + 65 * page + 8)
+    for r in range(2, n_req, 3):
+        c["table"][r][64] = c["table"][r][(m - 90) // 4 // page + 67] = -1
+    for window in (0, m - 66 * page):              # (starting behind column 64 too)
+        check_some(c, attn_uncut(c, window), picks, [0, n_kv - 1], window)
