@@ -652,3 +652,22 @@ def test_attn_single_tokens_on_tables_of_several_reads(n_q, n_kv, hd, page, dtyp
         c["table"][r][64] = c["table"][r][(m - 90) // 4 // page + 67] = -1
     for window in (0, m - 66 * page):              # (starting behind column 64 too)
         check_some(c, attn_uncut(c, window), picks, [0, n_kv - 1], window)
+
+
+def test_attn_most_requests():
+    """As many requests as a step may have, some of them long enough to be cut, the last one among them."""
+    lens = [(1, 1 + 37 * r % 40) for r in range(pi._kv.PI_KV_MAX_REQ)]
+    for r in (0, 63, 64, 2000, 4095):
+        lens[r] = (1, 5000 - r % 1000)
+    lens[77], lens[4000] = (0, 33), (1, 0)
+    announce(f"kv attn {len(lens)} requests")
+    for n_q, n_kv, hd, dtype in ((2, 1, 64, "f16"), (4, 4, 128, "bf16")):
+        c = shared_pages_case(n_q, lens, n_q, n_kv, hd, 16, dtype)
+        picks = [(r, 0) for r in (0, 1, 62, 63, 64, 65, 78, 1999, 2000, 2001, 3999, 4000, 4001, 4094, 4095)]
+        for r, i in picks:
+            if lens[r][1]:
+                look_at(c, r, i, lens[r][1] * 5 // 8)
+        got = attn(c)
+        assert got[c["starts"][4000]].abs().max() == 0
+        check_some(c, got, picks, list(range(n_kv)))
+        assert torch.equal(got, attn(c)), "the result depends on timing"
