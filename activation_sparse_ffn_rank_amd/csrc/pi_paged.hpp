@@ -34,6 +34,7 @@ struct KvF16 {
     static constexpr float kShift = 8.f;
     // The reference may lag the true maximum by this many powers of two (weights stay <= 2^14 < 65504).
     static constexpr float kLag = 6.f;
+    static constexpr float kHead = 1.f - 0x1p-7f;       // of kv_weights
     static __device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
     }
@@ -49,6 +50,7 @@ struct KvBf16 {
     static constexpr uint32_t kExpMask = 0x7f807f80u;
     static constexpr float kShift = 0.f;                // bf16 has fp32's exponents
     static constexpr float kLag = 6.f;
+    static constexpr float kHead = 1.f - 0x1p-6f;
     static __device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
     }
@@ -62,6 +64,24 @@ template <class T>
 __device__ __forceinline__ uint32_t kv_pack(float a, float b) {
     const f32x2 x = {a, b};
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, typename T::v2));
+}
+
+// Eight weights as the sum of two operands of the element type: most of each, rounded, and the rest, rounded.  The
+// rest of a weight above zero is above zero too, down to the type's smallest numbers (the head is short of it by more
+// than it was rounded), so that an infinite value times either has its sign.  2^-18 (fp16) or 2^-13 (bf16) of a weight is lost, where the type alone
+// loses 2^-11 or 2^-8.
+template <class T>
+__device__ __forceinline__ void kv_weights(const float (&p)[8], uint4 &head, uint4 &rest) {
+    uint32_t h[4], r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = p[2 * i], b = p[2 * i + 1];
+        h[i] = kv_pack<T>(a * T::kHead, b * T::kHead);
+        const typename T::v2 x = __builtin_bit_cast(typename T::v2, h[i]);
+        r[i] = kv_pack<T>(a - (float)x[0], b - (float)x[1]);
+    }
+    head = make_uint4(h[0], h[1], h[2], h[3]);
+    rest = make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // ------------------------------------------------------------------------------ block tables
@@ -438,8 +458,11 @@ struct KvRowsLds {
 // take a part of the range each, 32 keys at a time, straight from the pages into registers: nothing of K or V
 // is read twice by one tile, so LDS would only add a step.  The next block's keys are loaded during the softmax and its values after
 // the second product, 16 KB in flight per wave for heads of 128.  A score more than `lag` powers of two
-// above the running reference moves it; smaller ones do not, so most blocks rescale nothing.  Weights are rounded to
-// the element type for the second product; sums, references and outputs stay in fp32.  Bound by HBM: 16 requests of 2k
+// above the running reference moves it; smaller ones do not, so most blocks rescale nothing.  Scores, sums, references
+// and outputs are fp32; a weight enters the second product as two numbers of the element type (kv_weights), as MFMA
+// waits for memory here: 16 x 2k keys 62.5 us with one and 62.6 with both, 4 x 60k grouped 85.2 and 84.9, and the
+// outputs are then as near to 64-bit ones as their type allows (16 x 2k: 3.2e-5 off in the mean square's root, now 2.4e-5,
+// which is the rounding of the output alone).  Bound by HBM: 16 requests of 2k
 // keys, 32 heads of 128, 275 MB in 58.7 us; 96 heads of 3k, 1.8 GB in 315 us (5.7 TB/s).  TR: rows of a split
 // item in the workspace.
 template <class T, int HD, int TR, int WAVES>
@@ -604,9 +627,12 @@ __device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &
             p[e] = __builtin_amdgcn_exp2f(s[e] - ref);
             st.sum += p[e];
         }
-        const uint4 pf = make_uint4(kv_pack<T>(p[0], p[1]), kv_pack<T>(p[2], p[3]), kv_pack<T>(p[4], p[5]), kv_pack<T>(p[6], p[7]));
+        uint4 head, rest;
+        kv_weights<T>(p, head, rest);
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) st.o[t] = T::mfma16(vf[t], pf, st.o[t]);
+        for (int t = 0; t < kTiles; ++t) st.o[t] = T::mfma16(vf[t], head, st.o[t]);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) st.o[t] = T::mfma16(vf[t], rest, st.o[t]);
 
         if (more) load_v(next);
 
@@ -698,7 +724,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_kv_rows(KvAttnArgs a) {
 // as MFMA operands.  Inside a row of either tile the 16-byte units are permuted by the row's number, on
 // the way in, so that the 16 lanes that read the same unit of 16 rows find them in 16 bank groups.
 // The products are those of k_kv_rows on 32x32x16 MFMA: tile row 16s + 8u + 4h + v is key 16s + 8h + 4u
-// + v, so that lane half h holds keys 16s + 8h .. +7 of its query row in accumulators 8s .. 8s+7.
+// + v, so that lane half h holds keys 16s + 8h .. +7 of its query row in accumulators 8s .. 8s+7.  The weights are rounded
+// to the element type for the second product, and their sums are of the unrounded ones: in two numbers each, as
+// k_kv_rows has them, a 4096-token chunk on 12204 cached keys takes 1330 us and not 963, drafts of 5 tokens 30.6 and not 28.7.
+// The outputs of that chunk are 6.1e-5 off 64-bit ones in the mean square's root, 4.3e-5 of it by their own rounding.
 // Bound by MFMA and softmax together at the clock that the card holds: a 4096-token chunk on 12204 cached
 // keys, 32 heads of 128, 910 to 960 us = 1000 to 1050 TFLOP/s (a library product of 8192^3 reaches 1270); MFMA is
 // busy half of the time, the vector units most of the other half, LDS a quarter.  More buffers in flight, other

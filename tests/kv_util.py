@@ -128,6 +128,15 @@ def attn_tolerance(out, mag, dtype, head_dim, partial=8.0, keys=4096):
     return half * (mag + out.abs() + half * mag) + exponent * mag + keys * 2.0 ** -30
 
 
+def attn_tolerance_of_few_rows(out, mag, dtype, head_dim, partial=8.0, keys=4096):
+    """As attn_tolerance, where a weight enters the second product as two numbers of the type: all but a share of
+    it, rounded, and the rest (the share, and what was rounded), of which half a step is lost."""
+    half = torch.finfo(dtype).eps / 2
+    share = 2.0 ** -7 if dtype == torch.float16 else 2.0 ** -6
+    weights = half * (share + half) * mag + 2 * head_dim * 2.0 ** -24 * partial * mag + keys * 2.0 ** -30
+    return half * out.abs() + (1 + half) * weights
+
+
 def attn_case(seed, lens, n_q, n_kv, hd, page, dtype, extra_pages=3, max_pages=None):
     """Random pages and queries of requests (new tokens, keys): dict of CPU tensors and lists."""
     gen = torch.Generator().manual_seed(seed)

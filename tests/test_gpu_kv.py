@@ -671,3 +671,45 @@ def test_attn_most_requests():
         assert got[c["starts"][4000]].abs().max() == 0
         check_some(c, got, picks, list(range(n_kv)))
         assert torch.equal(got, attn(c)), "the result depends on timing"
+
+
+# ------------------------------------------------------------------------------ precision of single tokens
+
+@pytest.mark.parametrize("dtype", ("f16", "bf16"))
+@pytest.mark.parametrize("n_q,n_kv,hd,page,lens", [
+    (16, 16, 64, 16, [(1, m) for m in range(2, 34)]),                           # few short ranges
+    (24, 12, 128, 32, [(1, 2 + r % 50) for r in range(90)]),                    # many short ranges
+    (8, 2, 64, 16, [(1, 4000), (1, 3), (1, 1200), (2, 700)]),                   # cut and joined
+    (4, 2, 256, 64, [(1, 12), (2, 5), (1, 300), (3, 40)]),
+    (4, 4, 128, 16, [(150, 150)] + [(1, 2 + r) for r in range(30)])])           # beside a chunk
+def test_attn_single_tokens_lose_no_bits_of_their_weights(n_q, n_kv, hd, page, lens, dtype):
+    """Off by no more than the output's own rounding and what 32-bit scores leave."""
+    announce(f"kv attn precision heads={n_q}/{n_kv} hd={hd} page={page} {dtype}")
+    c = kv_util.attn_case(hd + len(lens), lens, n_q, n_kv, hd, page, dtype)
+    kv_util.past_end(c, math.nan)
+    got = check_attn(c)
+    want, mag = kv_util.attn_reference(c["q"], c["k"], c["v"], c["table"], c["starts"], c["kv"], c["scale"], 0)
+    tol = kv_util.attn_tolerance_of_few_rows(want, mag, c["q"].dtype, hd)
+    rows = [c["starts"][r] + i for r, (n, _) in enumerate(lens) if n <= 3 for i in range(n)]
+    err = (got.double() - want).abs()[rows]
+    assert bool((err <= tol[rows]).all()), f"worst {float((err / tol[rows]).max()):.3f} of the tolerance"
+
+
+@pytest.mark.parametrize("dtype", ("f16", "bf16"))
+@pytest.mark.parametrize("n_q,n_kv,hd,page,lens", [
+    (4, 2, 64, 16, [(1, 40), (1, 300), (1, 3000)]), (2, 2, 128, 64, [(1, 33), (3, 900)]), (2, 1, 256, 32, [(1, 700)]),
+    (2, 1, 128, 16, [(150, 500), (1, 200)])])
+def test_attn_infinite_values_keep_their_sign(n_q, n_kv, hd, page, lens, dtype):
+    """A token that sees an infinite value gets that infinity, as its weight is above zero."""
+    announce(f"kv attn infinite values heads={n_q}/{n_kv} hd={hd} page={page} {dtype} lens={lens}")
+    c = kv_util.attn_case(hd, lens, n_q, n_kv, hd, page, dtype)
+    for r, (n, m) in enumerate(lens):
+        for at, d in ((0, 3), ((m - n) // 2, 5), (m - n, 9)):
+            c["v"][c["table"][r][at // page]][:, d, at % page] = math.inf
+            c["v"][c["table"][r][at // page]][:, d + 1, at % page] = -math.inf
+    got = attn(c)
+    for d in (3, 5, 9):
+        assert bool((got[..., d] == math.inf).all()) and bool((got[..., d + 1] == -math.inf).all()), d
+    finite = torch.ones(hd, dtype=torch.bool)
+    finite[[3, 4, 5, 6, 9, 10]] = False
+    assert torch.isfinite(got[..., finite]).all()
