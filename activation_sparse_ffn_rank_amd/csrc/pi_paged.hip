@@ -248,7 +248,7 @@ extern "C" int pi_kv_attn(const pi_kv_cache *cache, const pi_kv_batch *batch, co
     a.n_req = batch->n_req, a.max_pages = batch->max_pages, a.max_q = batch->max_q, a.max_kv = batch->max_kv;
     // positions stay below 2^31 - 2^19 - window: the lower ends of windows are computed in 32 bits
     a.total_q = total_q, a.n_q = n_q, a.group = n_q / cache->n_kv, a.window = std::min(window, INT32_MAX - PI_KV_MAX_TOKENS);
-    a.split_target = g.target, a.slots = g.slots;
+    a.split_target = g.target, a.slots = g.slots, a.items = g.items;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.table_stride = batch->table_stride;
     a.q_ts = q_token_stride, a.q_hs = q_head_stride, a.o_ts = out_token_stride, a.o_hs = out_head_stride;

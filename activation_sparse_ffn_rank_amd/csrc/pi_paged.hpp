@@ -295,6 +295,7 @@ struct KvAttnArgs {
     int n_req, max_pages, max_q, max_kv, total_q, n_q, group, window;
     int split_target;                 // 0: key ranges are not cut
     int slots;                        // split items per kv head that the workspace holds
+    int items;                        // items per kv head that the grid has
     float scale_log2;                 // scale / ln 2, > 0: weights are powers of two
     int64_t table_stride, q_ts, q_hs, o_ts, o_hs;
     const uint16_t *k, *v, *q;
@@ -381,12 +382,13 @@ struct KvItem {
     int piece;                      // keys of a piece
     KvReq q;
 };
-// ROWS > 0 counts groups of ROWS rows of the cut requests instead (for the join; split is then the group).
+// ROWS > 0 counts groups of ROWS rows of the cut requests instead (for the join; split is then the group), of those whose
+// items all had a workgroup.
 template <int HD, int TR, int ROWS>
 __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, KvCut aim, int lane) {
     KvItem it;
     it.r = -1;
-    int base = 0, base_slot = 0;
+    int base = 0, base_slot = 0, base_item = 0;
     for (int r0 = 0; r0 < a.n_req; r0 += 64) {
         KvReq q{};
         int tiles = 0, splits = 1, piece = 1;
@@ -400,6 +402,7 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, KvCut a
         const int mine = ROWS == 0 ? tiles * splits : splits > 1 ? (q.rows + ROWS - 1) / (ROWS == 0 ? 1 : ROWS) : 0;
         const int incl = wave_incl_scan(mine), total = __builtin_amdgcn_readlane(incl, 63);
         const int incl_slot = a.split_target ? wave_incl_scan(cut) : 0;
+        const int incl_item = ROWS != 0 ? wave_incl_scan(tiles * splits) : 0;
         if (want < base + total) {
             const uint64_t past = __ballot(incl > want - base);
             const int l = __builtin_ctzll(past);
@@ -419,12 +422,14 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, KvCut a
                 it.split = at;
             }
             it.slot = base_slot + bcast(incl_slot, l) - bcast(cut, l) + it.tile * it.splits;
-            // (row ranges that overlap can ask for more than the workspace holds; those are left out)
+            // (row ranges that overlap can ask for more than the workspace holds, or the grid; those are left out)
             if (it.splits > 1 && it.slot + it.splits > a.slots) it.r = -2;
+            if (ROWS != 0 && base_item + bcast(incl_item, l) > a.items) it.r = -2;
             return it;
         }
         base += total;
         base_slot += __builtin_amdgcn_readlane(incl_slot, 63);
+        if (ROWS != 0) base_item = min(base_item + __builtin_amdgcn_readlane(incl_item, 63), 1 << 30);
     }
     return it;
 }

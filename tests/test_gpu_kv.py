@@ -713,3 +713,19 @@ def test_attn_infinite_values_keep_their_sign(n_q, n_kv, hd, page, lens, dtype):
     finite = torch.ones(hd, dtype=torch.bool)
     finite[[3, 4, 5, 6, 9, 10]] = False
     assert torch.isfinite(got[..., finite]).all()
+
+
+def test_attn_overlapping_row_ranges_take_no_old_partial_sums():
+    """Row ranges that overlap ask for more items than a call has: what is left out is not joined from what the
+    workspace held before."""
+    announce("kv attn overlapping row ranges")
+    n_req = 4096
+    for group in (1, 4):
+        c = kv_util.attn_case(group, [(1, 60000)], group, 1, 64, 64, "f16")
+        # every other request has the one row there is; all have few keys, but for the last of them
+        c["starts"] = [r % 2 for r in range(n_req + 1)]
+        c["kv"] = [1 + r % 30 for r in range(n_req)]
+        c["kv"][n_req - 2] = 60000
+        c["table"] = c["table"] * n_req
+        got = run_attn(c, max_q=1)                 # (on a workspace of NaN)
+        assert torch.isfinite(got).all()
