@@ -110,7 +110,7 @@ def _rows(fn: str, t, cache: pi_kv_cache) -> tuple[int, int, int, int, int]:
         raise PiError(fn, PI_ERR_SHAPE)
     n, heads, hd = t.shape
     ts, hs, one = t.stride()
-    if hd != cache.head_dim or one != 1 or n >= 2 ** 31 or heads >= 2 ** 31:
+    if hd != cache.head_dim or one != 1:
         raise PiError(fn, PI_ERR_SHAPE)
     # the stride along an axis of one element is never used
     return t.data_ptr(), ts if n > 1 else heads * hd, hs if heads > 1 else hd, n, heads
@@ -126,20 +126,13 @@ def _device(fn: str, *tensors) -> int:
 
 
 def _raw_stream(fn: str, stream, device: int) -> int:
-    """As ``_abi._stream``, but the current stream of the device that holds the tensors."""
+    """As ``_abi._stream``, but the current stream of the device that holds the tensors.  The calls are made with that
+    device current: the default stream (address 0) is the current device's."""
     if device < 0:
         raise PiError(fn, PI_ERR_NULL)
     if stream is None:
         return _current_stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _call(device: int, fn, *args) -> int:
-    """The library's call with `device` current: the default stream (address 0) is the current device's."""
-    if _current_device() == device:
-        return fn(*args)
-    with torch.cuda.device(device):
-        return fn(*args)
 
 
 def make_kv_cache(k_pages: torch.Tensor, v_pages: torch.Tensor) -> pi_kv_cache:
@@ -199,7 +192,10 @@ def make_kv_tables(cached: torch.Tensor, fresh: torch.Tensor, free_ring: torch.T
 def pi_kv_step(tables: pi_kv_tables, stream=None) -> None:
     """One step of the block tables: pages for the new tokens, pages of ended requests back, slot map."""
     stream = _raw_stream("pi_kv_step", stream, tables._device)
-    _check("pi_kv_step", _call(tables._device, kv_lib().pi_kv_step, tables, stream))
+    if _current_device() != tables._device:
+        with torch.cuda.device(tables._device):
+            return pi_kv_step(tables, stream)
+    _check("pi_kv_step", kv_lib().pi_kv_step(tables, stream))
 
 
 def pi_kv_append(cache: pi_kv_cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
@@ -207,13 +203,16 @@ def pi_kv_append(cache: pi_kv_cache, k: torch.Tensor, v: torch.Tensor, slots: to
     fn = "pi_kv_append"
     kp, kt, kh, n, heads = _rows(fn, k, cache)
     vp, vt, vh, n_v, heads_v = _rows(fn, v, cache)
-    if heads != cache.n_kv or heads_v != heads or n_v != n:
+    if heads != cache.n_kv or heads_v != heads or n_v != n or n >= 2 ** 31:
         raise PiError(fn, PI_ERR_SHAPE)
     at, device = _ints(fn, slots, n), cache._device
     if k.get_device() != device or v.get_device() != device or slots.get_device() != device:
         raise PiError(fn, PI_ERR_NULL)
-    stream = _raw_stream(fn, stream, device)
-    rc = _call(device, kv_lib().pi_kv_append, cache, kp, kt, kh, vp, vt, vh, at, n, stream)
+    stream = _current_stream(device) if stream is None and device >= 0 else _raw_stream(fn, stream, device)
+    if _current_device() != device:
+        with torch.cuda.device(device):
+            return pi_kv_append(cache, k, v, slots, stream)
+    rc = (_kv_lib or kv_lib()).pi_kv_append(cache, kp, kt, kh, vp, vt, vh, at, n, stream)
     if rc != PI_OK:
         raise PiError(fn, rc)
 
@@ -229,7 +228,7 @@ def pi_kv_attn(cache: pi_kv_cache, batch: pi_kv_batch, q: torch.Tensor, out: tor
     fn = "pi_kv_attn"
     qp, qt, qh, n, heads = _rows(fn, q, cache)
     op, ot, oh, n_o, heads_o = _rows(fn, out, cache)
-    if n_o != n or heads_o != heads or not -2 ** 31 <= window < 2 ** 31:
+    if n_o != n or heads_o != heads or n >= 2 ** 31 or heads >= 2 ** 31 or not -2 ** 31 <= window < 2 ** 31:
         raise PiError(fn, PI_ERR_SHAPE)
     device, wp, wn = cache._device, None, 0                  # (the library refuses a missing workspace if it needs one)
     if ws is not None:
@@ -240,7 +239,10 @@ def pi_kv_attn(cache: pi_kv_cache, batch: pi_kv_batch, q: torch.Tensor, out: tor
         wp, wn = ws.data_ptr(), ws.nbytes
     if q.get_device() != device or out.get_device() != device or batch._device != device:
         raise PiError(fn, PI_ERR_NULL)
-    stream = _raw_stream(fn, stream, device)
-    rc = _call(device, kv_lib().pi_kv_attn, cache, batch, qp, qt, qh, op, ot, oh, n, heads, scale, window, wp, wn, stream)
+    stream = _current_stream(device) if stream is None and device >= 0 else _raw_stream(fn, stream, device)
+    if _current_device() != device:
+        with torch.cuda.device(device):
+            return pi_kv_attn(cache, batch, q, out, ws, scale=scale, window=window, stream=stream)
+    rc = (_kv_lib or kv_lib()).pi_kv_attn(cache, batch, qp, qt, qh, op, ot, oh, n, heads, scale, window, wp, wn, stream)
     if rc != PI_OK:
         raise PiError(fn, rc)
