@@ -68,8 +68,8 @@ __device__ __forceinline__ uint32_t kv_pack(float a, float b) {
 
 // Eight weights as the sum of two operands of the element type: most of each, rounded, and the rest, rounded.  The
 // rest of a weight above zero is above zero too, down to the type's smallest numbers (the head is short of it by more
-// than it was rounded), so that an infinite value times either has its sign.  2^-18 (fp16) or 2^-13 (bf16) of a weight is lost, where the type alone
-// loses 2^-11 or 2^-8.
+// than it was rounded), so that an infinite value times either has its sign.  At most 2^-17 (fp16) or 2^-13 (bf16) of a
+// weight is lost, where the type alone loses up to 2^-11 or 2^-8.
 template <class T>
 __device__ __forceinline__ void kv_weights(const float (&p)[8], uint4 &head, uint4 &rest) {
     uint32_t h[4], r[4];
@@ -120,7 +120,9 @@ __device__ __forceinline__ uint32_t kv_block_scan(uint32_t v, uint32_t *part, ui
 // the workgroups share out the pages and the rows: nothing waits on another workgroup.  With one
 // workgroup all inputs are read before the first output is written, so a step may run in place.
 // The row sums stay below 2^32: at most 4096 requests of at most 2^19 + 1 counted rows.  Bound by the
-// latency of its few dependent loads: 64 requests 6.4 us, 1500 with 66 thousand new tokens 9.1 us.
+// latency of its few dependent loads: a pass over 64 requests 6.4 us, 1500 with 66 thousand new tokens 9.2 us.  In place
+// the one workgroup finds all the slots: the same two take 9 and 119 us, with events around a call alone, and 9 and 12
+// with separate outputs.
 __global__ __launch_bounds__(kKvTableThreads) void k_kv_tables(KvTablesArgs a) {
     __shared__ uint32_t s_row[PI_KV_MAX_REQ + 1];   // first row
     __shared__ uint32_t s_need[PI_KV_MAX_REQ];      // pages asked for (ended: given back) by the requests before | flags
@@ -256,7 +258,7 @@ struct KvAppendArgs {
 // fused projection and fill whole pages (5000 tokens of 56 heads of 128: 96 us with token tiles fastest, 74
 // so).  Keys: 16-byte copies.  Values go through LDS so that a lane stands for a token on the way out: tokens in
 // neighbouring slots of a page then store neighbouring 2-byte elements of one V^T row.  (Runs of 8 slots stored as
-// 16 bytes were no faster.)  Bound by memory traffic: 4096 tokens of 96 heads of 128, 403 MB, 94 us.
+// 16 bytes were no faster.)  Bound by memory traffic: 4096 tokens of 96 heads of 128, 403 MB, 92 us.
 template <int TT>
 __global__ __launch_bounds__(256) void k_kv_append(KvAppendArgs a) {
     extern __shared__ uint32_t s_v[];                // [TT][hd/2 + 1]
@@ -465,10 +467,10 @@ struct KvRowsLds {
 // the second product, 16 KB in flight per wave for heads of 128.  A score more than `lag` powers of two
 // above the running reference moves it; smaller ones do not, so most blocks rescale nothing.  Scores, sums, references
 // and outputs are fp32; a weight enters the second product as two numbers of the element type (kv_weights), as MFMA
-// waits for memory here: 16 x 2k keys 62.5 us with one and 62.6 with both, 4 x 60k grouped 85.2 and 84.9, and the
-// outputs are then as near to 64-bit ones as their type allows (16 x 2k: 3.2e-5 off in the mean square's root, now 2.4e-5,
-// which is the rounding of the output alone).  Bound by HBM: 16 requests of 2k
-// keys, 32 heads of 128, 275 MB in 58.7 us; 96 heads of 3k, 1.8 GB in 315 us (5.7 TB/s).  TR: rows of a split
+// waits for memory here: 16 x 2k keys 61.1 us with one and 61.0 with both, 4 x 60k grouped 84.6 and 85.0 (1 x 513, all
+// latency, 7.4 and 7.5), and the outputs are then as near to 64-bit ones as their type allows (16 x 2k: 3.2e-5 off in the
+// mean square's root, now 2.4e-5, which is the rounding of the output alone).  Bound by HBM: 16 requests of 2k keys, 32
+// heads of 128, 275 MB in 54.7 us, and 58.7 a pass with the join; 96 heads of 3k, 1.8 GB in 315 us (5.7 TB/s).  TR: rows of a split
 // item in the workspace.
 template <class T, int HD, int TR, int WAVES>
 __device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &it, int h, KvRowsLds<HD, WAVES> &sh) {
@@ -734,12 +736,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_kv_rows(KvAttnArgs a) {
 // k_kv_rows has them, a 4096-token chunk on 12204 cached keys takes 1330 us and not 963, drafts of 5 tokens 30.6 and not 28.7.
 // The outputs of that chunk are 6.1e-5 off 64-bit ones in the mean square's root, 4.3e-5 of it by their own rounding.
 // Bound by MFMA and softmax together at the clock that the card holds: a 4096-token chunk on 12204 cached
-// keys, 32 heads of 128, 910 to 960 us = 1000 to 1050 TFLOP/s (a library product of 8192^3 reaches 1270); MFMA is
-// busy half of the time, the vector units most of the other half, LDS a quarter.  More buffers in flight, other
-// orders of the first product, wave priorities, and sums of the weights by dot products measured no faster.
+// keys, 32 heads of 128, 936 us in a run of passes = 1022 TFLOP/s (a library product of 8192^3 reaches 1270), 1014 in the
+// median of 24 passes under a trace; MFMA is busy half of the time, the vector units most of the other half, LDS a
+// quarter.  More buffers in flight, other orders of the first product, wave priorities, and sums of the weights by dot
+// products measured no faster.
 // P: positions that a page gives to a block, the page's or all of the block's.  K lies in LDS as [key][HD], V as in the
 // pages, [page][HD][P], so that every load reads 1 KB of one page from a scalar address (with V gathered as [HD][key],
-// pages of 16 took 16% longer than pages of 64: 2048 tokens on 8000 keys, 32 heads of 128; now 263 and 259 us).
+// pages of 16 took 16% longer than pages of 64: 2048 tokens on 8000 keys, 32 heads of 128; now 277 and 270 us).
 template <int HD, int P>
 struct KvTile {
     static constexpr int kKeys = HD == 256 ? 32 : 64;      // 64 KB of LDS for both buffers at most
@@ -779,8 +782,8 @@ __device__ __forceinline__ uint64_t kv_dead_bits(uint32_t m) {
 
 // P: as in KvTile.  MIXED: requests of few rows, single tokens beside
 // prompt chunks among them, are taken too, by kv_rows_item: they wait for memory, not for MFMA.  (14 single tokens
-// beside two chunks of 777, 56 heads of 128: 165 us without this path, 156 with it, 147 now.  Without such
-// requests it stays out of the kernel, whose registers then serve the one loop: a 4096-token chunk 1009 -> 953.)
+// beside two chunks of 777, 56 heads of 128: 165 us without this path, 156 with it, 147 a pass now, the join
+// included.  Without such requests it stays out of the kernel, whose registers then serve the one loop: a 4096-token chunk 1009 -> 953.)
 template <class T, int HD, int P, bool MIXED>
 __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_tile(KvAttnArgs a) {
     typedef KvTile<HD, P> L;
@@ -1102,7 +1105,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
 // Joins the split items, each scaled to the largest reference, and divides by the row's sum: a workgroup takes a
 // few rows of one kv head at a time (a row per HD / 4 lanes, 16 bytes each), its four waves a quarter of the pieces
 // each, kDeep of them in flight; the quarters are added in order.  The grid does not depend on how many requests are
-// cut: with none it ends at once.  Bound by latency, 5 to 8 us, of which 4 to find that there is nothing to do.
+// cut: with none it ends at once.  Bound by latency, 5 to 8 us, of which 4 to 5 to find that there is nothing to do.
 template <class T, int HD, int TR>
 __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
     constexpr int kLanes = HD / 4, kRows = 64 / kLanes, kDeep = 8, kWaves = 4;

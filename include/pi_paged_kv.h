@@ -16,7 +16,7 @@
  *   j <= p,   and   j > p - window when window > 0.
  * Query head h reads kv head h / (n_q / n_kv).  With s_j = scale * q . k_j over the keys seen,
  *   out = sum_j exp(s_j - max s) v_j / sum_j exp(s_j - max s),
- * and zero for a token that sees no key (m = 0, or p < 0).  What keys and values that a token does
+ * and zero for a token that sees no key (m = 0, or p < 0), or whose scores are all -infinity.  What keys and values that a token does
  * not see hold (infinities and NaN included) has no effect on its output.
  *
  * Conventions are those of pi_sparse_ffn.h: device memory owned by the caller, work only enqueued on
@@ -54,7 +54,8 @@ typedef struct pi_kv_cache {
  * new tokens.  max_q and max_kv bound the lengths on the host (they choose kernels and grids): a
  * request's new tokens past max_q and keys past max_kv are not read, nor keys past max_pages*page.
  * A table entry outside [0, n_pages) is a page without keys.  A request whose q_start range is
- * negative, decreasing or past the packed rows is left out, and of ranges that overlap some may be. */
+ * negative, decreasing or past the packed rows is left out, and of ranges that overlap some may be, or some
+ * of their rows. */
 typedef struct pi_kv_batch {
     int32_t n_req, max_pages, max_q, max_kv;
     int64_t table_stride;          /* entries from one request's table row to the next, >= max_pages */
