@@ -470,8 +470,8 @@ struct KvRowsLds {
 // waits for memory here: 16 x 2k keys 61.1 us with one and 61.0 with both, 4 x 60k grouped 84.6 and 85.0 (1 x 513, all
 // latency, 7.4 and 7.5), and the outputs are then as near to 64-bit ones as their type allows (16 x 2k: 3.2e-5 off in the
 // mean square's root, now 2.4e-5, which is the rounding of the output alone).  Bound by HBM: 16 requests of 2k keys, 32
-// heads of 128, 275 MB in 54.7 us, and 58.7 a pass with the join; 96 heads of 3k, 1.8 GB in 315 us (5.7 TB/s).  TR: rows of a split
-// item in the workspace.
+// heads of 128, 275 MB in 54.7 us, and 58.7 a pass with the join; 96 heads of 3k, 1.8 GB in 315 us (5.7 TB/s).  TR:
+// rows of a split item in the workspace.
 template <class T, int HD, int TR, int WAVES>
 __device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &it, int h, KvRowsLds<HD, WAVES> &sh) {
     constexpr int kSteps = HD / 32, kTiles = HD / 16, kWaves = WAVES;
@@ -783,7 +783,8 @@ __device__ __forceinline__ uint64_t kv_dead_bits(uint32_t m) {
 // P: as in KvTile.  MIXED: requests of few rows, single tokens beside
 // prompt chunks among them, are taken too, by kv_rows_item: they wait for memory, not for MFMA.  (14 single tokens
 // beside two chunks of 777, 56 heads of 128: 165 us without this path, 156 with it, 147 a pass now, the join
-// included.  Without such requests it stays out of the kernel, whose registers then serve the one loop: a 4096-token chunk 1009 -> 953.)
+// included.  Without such requests it stays out of the kernel, whose registers then serve the one loop: a 4096-token
+// chunk 1009 -> 953.)
 template <class T, int HD, int P, bool MIXED>
 __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_tile(KvAttnArgs a) {
     typedef KvTile<HD, P> L;

@@ -16,8 +16,9 @@
  *   j <= p,   and   j > p - window when window > 0.
  * Query head h reads kv head h / (n_q / n_kv).  With s_j = scale * q . k_j over the keys seen,
  *   out = sum_j exp(s_j - max s) v_j / sum_j exp(s_j - max s),
- * and zero for a token that sees no key (m = 0, or p < 0), or whose scores are all -infinity.  What keys and values that a token does
- * not see hold (infinities and NaN included) has no effect on its output.
+ * and zero for a token that sees no key (m = 0, or p < 0), or whose scores are all -infinity.  What
+ * keys and values that a token does not see hold (infinities and NaN included) has no effect on its
+ * output.
  *
  * Conventions are those of pi_sparse_ffn.h: device memory owned by the caller, work only enqueued on
  * `stream`, arguments checked on the host before any HIP call, nothing enqueued on a nonzero return
