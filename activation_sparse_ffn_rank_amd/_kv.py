@@ -20,10 +20,14 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 
 
 PI_KV_F16, PI_KV_BF16 = 1, 2
 PI_KV_MAX_REQ, PI_KV_MAX_TABLE, PI_KV_MAX_TOKENS = 4096, 1 << 17, 1 << 19
+PI_KV_MAX_VOCAB = 1 << 22
+PI_ROPE_HALF, PI_ROPE_PAIRS = 0, 1
 KV_DTYPES = {torch.float16: PI_KV_F16, torch.bfloat16: PI_KV_BF16}
 
 # Every function the header declares; the CPU tests check that libpi.so exports them all.
-KV_EXPORTS = ("pi_kv_step", "pi_kv_append", "pi_kv_attn_workspace_bytes", "pi_kv_attn")
+KV_EXPORTS = ("pi_kv_step", "pi_kv_append", "pi_kv_attn_workspace_bytes", "pi_kv_attn", "pi_rope_frequencies",
+              "pi_kv_rope_append", "pi_kv_attn_sinks_workspace_bytes", "pi_kv_attn_sinks", "pi_kv_verify_workspace_bytes",
+              "pi_kv_verify", "pi_kv_release", "pi_kv_fork", "pi_kv_copy")
 
 _i32, _i64, _vp, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
 
@@ -45,6 +49,22 @@ class pi_kv_tables(ctypes.Structure):
                 ("pool_next", _vp), ("counts", _vp)]
 
 
+class pi_kv_rope(ctypes.Structure):
+    _fields_ = [("rot_dim", _i32), ("layout", _i32), ("norm", _i32), ("scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("freq", _vp), ("q_weight", _vp), ("k_weight", _vp)]
+
+
+class pi_kv_drafts(ctypes.Structure):
+    _fields_ = [("n_req", _i32), ("rows", _i32), ("vocab", _i32), ("q_start", _vp), ("tokens", _vp), ("target", _vp),
+                ("target_stride", _i64), ("draft", _vp), ("draft_stride", _i64), ("u_accept", _vp), ("u_next", _vp)]
+
+
+class pi_kv_pages(ctypes.Structure):
+    _fields_ = [("n_req", _i32), ("page", _i32), ("n_pages", _i32), ("max_pages", _i32), ("table_stride", _i64),
+                ("cached", _vp), ("free_ring", _vp), ("pool", _vp), ("block_table", _vp), ("shares", _vp), ("cached_next", _vp),
+                ("pool_next", _vp), ("counts", _vp)]
+
+
 _kv_lib = None
 
 
@@ -61,6 +81,27 @@ def kv_lib() -> ctypes.CDLL:
         L.pi_kv_attn.restype = ctypes.c_int
         L.pi_kv_attn.argtypes = [P(pi_kv_cache), P(pi_kv_batch), _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32,
                                  ctypes.c_float, _i32, _vp, _sz, _vp]
+        f64 = ctypes.c_double
+        L.pi_rope_frequencies.restype = ctypes.c_int
+        L.pi_rope_frequencies.argtypes = [_i32, f64, f64, f64, f64, f64, _vp]
+        L.pi_kv_rope_append.restype = ctypes.c_int
+        L.pi_kv_rope_append.argtypes = [P(pi_kv_cache), P(pi_kv_batch), P(pi_kv_rope), _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64,
+                                        _i64, _vp, _vp, _i64, _i64, _i32, _i32, _vp]
+        L.pi_kv_attn_sinks_workspace_bytes.restype = _sz
+        L.pi_kv_attn_sinks_workspace_bytes.argtypes = [P(pi_kv_cache), P(pi_kv_batch), _i32, _i32, _i32, _i32]
+        L.pi_kv_attn_sinks.restype = ctypes.c_int
+        L.pi_kv_attn_sinks.argtypes = [P(pi_kv_cache), P(pi_kv_batch), _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32,
+                                       ctypes.c_float, _i32, _i32, _vp, _sz, _vp]
+        L.pi_kv_verify_workspace_bytes.restype = _sz
+        L.pi_kv_verify_workspace_bytes.argtypes = [P(pi_kv_drafts)]
+        L.pi_kv_verify.restype = ctypes.c_int
+        L.pi_kv_verify.argtypes = [P(pi_kv_drafts), _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+        L.pi_kv_release.restype = ctypes.c_int
+        L.pi_kv_release.argtypes = [P(pi_kv_pages), _vp, _vp, _vp, _vp]
+        L.pi_kv_fork.restype = ctypes.c_int
+        L.pi_kv_fork.argtypes = [P(pi_kv_pages), _vp, _vp, _i32, _vp, _vp]
+        L.pi_kv_copy.restype = ctypes.c_int
+        L.pi_kv_copy.argtypes = [P(pi_kv_cache), _vp, _i32, _vp]
         _kv_lib = L
     return _kv_lib
 
@@ -246,3 +287,252 @@ def pi_kv_attn(cache: pi_kv_cache, batch: pi_kv_batch, q: torch.Tensor, out: tor
     rc = (_kv_lib or kv_lib()).pi_kv_attn(cache, batch, qp, qt, qh, op, ot, oh, n, heads, scale, window, wp, wn, stream)
     if rc != PI_OK:
         raise PiError(fn, rc)
+
+
+# ------------------------------------------------------------------------------ rotary positions with the append
+
+def pi_rope_frequencies(rot_dim: int, *, base: float = 10000.0, factor: float = 1.0, trained: float = 4096.0, low: float = 0.0,
+                        high: float = 0.0) -> torch.Tensor:
+    """Radians per position of the rot_dim / 2 pairs (float64, host memory): base^(-2i/rot_dim); with low = high = 0 all
+    divided by factor, else those of fewer than `low` turns over `trained` positions divided, those of more than
+    `high` kept, a ramp between."""
+    fn = "pi_rope_frequencies"
+    _int32(fn, rot_dim)
+    freq = torch.empty(max(rot_dim // 2, 1), dtype=torch.float64)
+    _check(fn, kv_lib().pi_rope_frequencies(rot_dim, base, factor, trained, low, high, freq.data_ptr()))
+    return freq
+
+
+def make_kv_rope(freq: torch.Tensor | None, *, layout: int = PI_ROPE_HALF, scale: float = 1.0, norm: bool | None = None,
+                 eps: float = 1e-6, q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None) -> pi_kv_rope:
+    """Descriptor of what is done to heads of q and k: RMS norm (norm; by itself where a weight [head_dim] is given), then
+    rotation of the first 2 * len(freq) elements (freq: float64 radians per position on the pages' device; None: no
+    rotation) in pairs by layout, with cosines and sines times scale."""
+    fn = "make_kv_rope"
+    kept = [t for t in (freq, q_weight, k_weight) if t is not None]
+    if freq is not None and freq.dtype != torch.float64:
+        raise PiError(fn, PI_ERR_DTYPE)
+    weights = kept if freq is None else kept[1:]
+    if any(t.dtype not in KV_DTYPES or t.dtype != weights[0].dtype for t in weights) or (weights and norm is False):
+        raise PiError(fn, PI_ERR_DTYPE)
+    if any(t.dim() != 1 or not t.is_contiguous() for t in kept) or any(t.shape != weights[0].shape for t in weights):
+        raise PiError(fn, PI_ERR_SHAPE)
+    rot = 0 if freq is None else 2 * freq.shape[0]
+    _int32(fn, rot, layout)
+    at = lambda t: None if t is None else t.data_ptr()
+    r = pi_kv_rope(rot, layout, int(bool(weights) if norm is None else norm), scale, eps, at(freq), at(q_weight), at(k_weight))
+    r._device = _device(fn, *kept) if kept else None
+    r._weights = (weights[0].dtype, weights[0].shape[0]) if weights else None
+    r._keep = tuple(kept)
+    return r
+
+
+def pi_kv_rope_append(cache: pi_kv_cache, batch: pi_kv_batch, rope: pi_kv_rope, q: torch.Tensor, k: torch.Tensor,
+                      v: torch.Tensor, slots: torch.Tensor, q_out: torch.Tensor, stream=None) -> None:
+    """k (normed, rotated) and v [total_q][n_kv][head_dim] into slots [total_q], and q [total_q][n_q][head_dim] (normed,
+    rotated) to q_out, which may be q.  Positions follow from the batch."""
+    fn = "pi_kv_rope_append"
+    qp, qt, qh, n, heads = _rows(fn, q, cache)
+    kp, kt, kh, n_k, heads_k = _rows(fn, k, cache)
+    vp, vt, vh, n_v, heads_v = _rows(fn, v, cache)
+    op, ot, oh, n_o, heads_o = _rows(fn, q_out, cache)
+    if n_k != n or n_v != n or n_o != n or heads_k != cache.n_kv or heads_v != heads_k or heads_o != heads or n >= 2 ** 31 or heads >= 2 ** 31:
+        raise PiError(fn, PI_ERR_SHAPE)
+    if rope._weights is not None and rope._weights != (q.dtype, cache.head_dim):
+        raise PiError(fn, PI_ERR_DTYPE if rope._weights[0] != q.dtype else PI_ERR_SHAPE)
+    at, device = _ints(fn, slots, n), cache._device
+    if (q.get_device() != device or k.get_device() != device or v.get_device() != device or q_out.get_device() != device
+            or slots.get_device() != device or batch._device != device or rope._device not in (None, device)):
+        raise PiError(fn, PI_ERR_NULL)
+    stream = _current_stream(device) if stream is None and device >= 0 else _raw_stream(fn, stream, device)
+    if _current_device() != device:
+        with torch.cuda.device(device):
+            return pi_kv_rope_append(cache, batch, rope, q, k, v, slots, q_out, stream)
+    rc = (_kv_lib or kv_lib()).pi_kv_rope_append(cache, batch, rope, qp, qt, qh, kp, kt, kh, vp, vt, vh, at, op, ot, oh, n, heads, stream)
+    if rc != PI_OK:
+        raise PiError(fn, rc)
+
+
+# ------------------------------------------------------------------------------ a window and the first tokens
+
+def pi_kv_attn_sinks_workspace_bytes(cache: pi_kv_cache, batch: pi_kv_batch, total_q: int, n_q: int, window: int, sinks: int) -> int:
+    """Bytes of workspace pi_kv_attn_sinks needs (0: invalid)."""
+    if not _fits(total_q, n_q, window, sinks):
+        return 0
+    return int(kv_lib().pi_kv_attn_sinks_workspace_bytes(cache, batch, total_q, n_q, window, sinks))
+
+
+def pi_kv_attn_sinks(cache: pi_kv_cache, batch: pi_kv_batch, q: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, *,
+                     scale: float, window: int, sinks: int, stream=None) -> None:
+    """pi_kv_attn with a window, in which a request's first `sinks` keys stay visible."""
+    fn = "pi_kv_attn_sinks"
+    qp, qt, qh, n, heads = _rows(fn, q, cache)
+    op, ot, oh, n_o, heads_o = _rows(fn, out, cache)
+    if n_o != n or heads_o != heads or n >= 2 ** 31 or heads >= 2 ** 31 or not _fits(window, sinks):
+        raise PiError(fn, PI_ERR_SHAPE)
+    device, wp, wn = cache._device, None, 0
+    if ws is not None:
+        if not ws.is_contiguous():
+            raise PiError(fn, PI_ERR_WORKSPACE)
+        if ws.get_device() != device:
+            raise PiError(fn, PI_ERR_NULL)
+        wp, wn = ws.data_ptr(), ws.nbytes
+    if q.get_device() != device or out.get_device() != device or batch._device != device:
+        raise PiError(fn, PI_ERR_NULL)
+    stream = _current_stream(device) if stream is None and device >= 0 else _raw_stream(fn, stream, device)
+    if _current_device() != device:
+        with torch.cuda.device(device):
+            return pi_kv_attn_sinks(cache, batch, q, out, ws, scale=scale, window=window, sinks=sinks, stream=stream)
+    rc = (_kv_lib or kv_lib()).pi_kv_attn_sinks(cache, batch, qp, qt, qh, op, ot, oh, n, heads, scale, window, sinks, wp, wn, stream)
+    if rc != PI_OK:
+        raise PiError(fn, rc)
+
+
+# ------------------------------------------------------------------------------ drafted tokens
+
+def _floats(fn: str, t, n: int) -> int:
+    """Address of a contiguous float32 tensor [n]."""
+    if t is None:
+        raise PiError(fn, PI_ERR_NULL)
+    if t.dtype != torch.float32:
+        raise PiError(fn, PI_ERR_DTYPE)
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise PiError(fn, PI_ERR_SHAPE)
+    return t.data_ptr()
+
+
+def _probs(fn: str, t, rows: int, vocab: int) -> tuple[int, int]:
+    """(address, row stride) of float32 rows [rows][vocab], possibly slices of wider ones."""
+    if t.dtype != torch.float32:
+        raise PiError(fn, PI_ERR_DTYPE)
+    if t.dim() != 2 or tuple(t.shape) != (rows, vocab) or (t.stride(1) != 1 and vocab > 1):
+        raise PiError(fn, PI_ERR_SHAPE)
+    return t.data_ptr(), t.stride(0) if rows > 1 else vocab
+
+
+def make_kv_drafts(q_start: torch.Tensor, tokens: torch.Tensor, target: torch.Tensor, draft: torch.Tensor | None,
+                   u_accept: torch.Tensor, u_next: torch.Tensor) -> pi_kv_drafts:
+    """Descriptor of a step's drafted tokens: packed rows by q_start [n_req + 1], tokens [rows] (a request's last one, then its
+    drafts), probabilities target and draft [rows][vocab] (draft None: each draft had all of it), random
+    numbers u_accept [rows] and u_next [n_req] in [0, 1)."""
+    fn = "make_kv_drafts"
+    start, toks = _ints(fn, q_start, -1), _ints(fn, tokens, -1)
+    n, rows = q_start.shape[0] - 1, tokens.shape[0]
+    if target is None:
+        raise PiError(fn, PI_ERR_NULL)
+    if target.dim() != 2:
+        raise PiError(fn, PI_ERR_SHAPE)
+    vocab = target.shape[1]
+    _int32(fn, vocab)
+    p, p_stride = _probs(fn, target, rows, vocab)
+    q, q_stride = (None, 0) if draft is None else _probs(fn, draft, rows, vocab)
+    d = pi_kv_drafts(n, rows, vocab, start, toks, p, p_stride, q, q_stride, _floats(fn, u_accept, rows), _floats(fn, u_next, n))
+    d._keep = tuple(t for t in (q_start, tokens, target, draft, u_accept, u_next) if t is not None)
+    d._device = _device(fn, *d._keep)
+    return d
+
+
+def pi_kv_verify_workspace_bytes(drafts: pi_kv_drafts) -> int:
+    """Bytes of workspace pi_kv_verify needs (0: invalid)."""
+    return int(kv_lib().pi_kv_verify_workspace_bytes(drafts))
+
+
+def pi_kv_verify(drafts: pi_kv_drafts, accepted: torch.Tensor, next: torch.Tensor, ws: torch.Tensor, *,
+                 kv_len: torch.Tensor | None = None, keep: torch.Tensor | None = None, stream=None) -> None:
+    """accepted [n_req] drafts of each request, the next token [n_req] behind them, and with kv_len the positions that
+    stay, keep [n_req] (int32)."""
+    fn = "pi_kv_verify"
+    n, device = drafts.n_req, drafts._device
+    ap, np_ = _ints(fn, accepted, n), _ints(fn, next, n)
+    lp, kp = (None if t is None else _ints(fn, t, n) for t in (kv_len, keep))
+    wp, wn = None, 0
+    if ws is not None:
+        if not ws.is_contiguous():
+            raise PiError(fn, PI_ERR_WORKSPACE)
+        wp, wn = ws.data_ptr(), ws.nbytes
+    if any(t is not None and t.get_device() != device for t in (accepted, next, ws, kv_len, keep)):
+        raise PiError(fn, PI_ERR_NULL)
+    stream = _raw_stream(fn, stream, device)
+    if _current_device() != device:
+        with torch.cuda.device(device):
+            return pi_kv_verify(drafts, accepted, next, ws, kv_len=kv_len, keep=keep, stream=stream)
+    _check(fn, kv_lib().pi_kv_verify(drafts, lp, ap, np_, kp, wp, wn, stream))
+
+
+# ------------------------------------------------------------------------------ pages given back, shared and copied
+
+def make_kv_pages(cached: torch.Tensor, free_ring: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, page: int,
+                  shares: torch.Tensor, cached_next: torch.Tensor, pool_next: torch.Tensor, counts: torch.Tensor) -> pi_kv_pages:
+    """Descriptor of the block tables' state for pi_kv_release and pi_kv_fork (int32 tensors, as of make_kv_tables, and shares
+    [n_pages], the owners of each page beyond the first); cached_next may be cached and pool_next may be pool."""
+    fn = "make_kv_pages"
+    at = _ints(fn, cached, -1)
+    n = cached.shape[0]
+    table, cols, stride = _table(fn, block_table, n)
+    _int32(fn, page)
+    ring = _ints(fn, free_ring, -1)
+    n_pages = free_ring.shape[0]
+    p = pi_kv_pages(n, page, n_pages, cols, stride, at, ring, _ints(fn, pool, 2), table, _ints(fn, shares, n_pages),
+                    _ints(fn, cached_next, n), _ints(fn, pool_next, 2), _ints(fn, counts, 4))
+    p._keep = (cached, free_ring, pool, block_table, shares, cached_next, pool_next, counts)
+    p._device = _device(fn, *p._keep)
+    return p
+
+
+def _copies(fn: str, t, n: int) -> int:
+    """Address of contiguous int32 pairs [n][2] (n -1: any number)."""
+    if t is None:
+        raise PiError(fn, PI_ERR_NULL)
+    if t.dtype != torch.int32:
+        raise PiError(fn, PI_ERR_DTYPE)
+    if t.dim() != 2 or t.shape[1] != 2 or (n >= 0 and t.shape[0] != n) or not t.is_contiguous():
+        raise PiError(fn, PI_ERR_SHAPE)
+    return t.data_ptr()
+
+
+def _on(fn: str, device: int, *tensors) -> None:
+    if any(t.get_device() != device for t in tensors):
+        raise PiError(fn, PI_ERR_NULL)
+
+
+def pi_kv_release(pages: pi_kv_pages, drop_from: torch.Tensor, drop_to: torch.Tensor | None, copies: torch.Tensor, stream=None) -> None:
+    """Gives up positions drop_from .. drop_to - 1 [n_req] of every request (drop_to None: to the end); copies [n_req][2]
+    receives the page copies that are due (pi_kv_copy)."""
+    fn = "pi_kv_release"
+    n, device = pages.n_req, pages._device
+    fp, tp, cp = _ints(fn, drop_from, n), None if drop_to is None else _ints(fn, drop_to, n), _copies(fn, copies, n)
+    _on(fn, device, *(t for t in (drop_from, drop_to, copies) if t is not None))
+    stream = _raw_stream(fn, stream, device)
+    if _current_device() != device:
+        with torch.cuda.device(device):
+            return pi_kv_release(pages, drop_from, drop_to, copies, stream)
+    _check(fn, kv_lib().pi_kv_release(pages, fp, tp, cp, stream))
+
+
+def pi_kv_fork(pages: pi_kv_pages, src: torch.Tensor, dst: torch.Tensor, copies: torch.Tensor, stream=None) -> None:
+    """Makes the empty requests dst [n] copies of the requests src [n], sharing their full pages; copies [n][2] receives the
+    page copies that are due (pi_kv_copy)."""
+    fn = "pi_kv_fork"
+    sp, device = _ints(fn, src, -1), pages._device
+    n = src.shape[0]
+    dp, cp = _ints(fn, dst, n), _copies(fn, copies, n)
+    _on(fn, device, src, dst, copies)
+    stream = _raw_stream(fn, stream, device)
+    if _current_device() != device:
+        with torch.cuda.device(device):
+            return pi_kv_fork(pages, src, dst, copies, stream)
+    _check(fn, kv_lib().pi_kv_fork(pages, sp, dp, n, cp, stream))
+
+
+def pi_kv_copy(cache: pi_kv_cache, copies: torch.Tensor, stream=None) -> None:
+    """Keys and values of page copies[i][0] to page copies[i][1] (pairs with an entry out of range are skipped)."""
+    fn = "pi_kv_copy"
+    cp, device = _copies(fn, copies, -1), cache._device
+    n = copies.shape[0]
+    _int32(fn, n)
+    _on(fn, device, copies)
+    stream = _raw_stream(fn, stream, device)
+    if _current_device() != device:
+        with torch.cuda.device(device):
+            return pi_kv_copy(cache, copies, stream)
+    _check(fn, kv_lib().pi_kv_copy(cache, cp, n, stream))

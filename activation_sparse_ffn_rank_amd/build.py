@@ -15,11 +15,14 @@ ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libpi.so")
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, "pi_abi.hip"), os.path.join(CSRC, "pi_persist_b.hip"), os.path.join(CSRC, "pi_split.hip"),
-           os.path.join(CSRC, "pi_paged.hip")]
+           os.path.join(CSRC, "pi_paged.hip"), os.path.join(CSRC, "pi_paged_sinks.hip"),
+           os.path.join(CSRC, "pi_paged_rope.hip"), os.path.join(CSRC, "pi_paged_pages.hip"),
+           os.path.join(CSRC, "pi_paged_verify.hip")]
 HOST_SOURCES = [os.path.join(CSRC, "pi_cold.cpp"),   # host half of the hybrid split (g++, OpenMP)
                 os.path.join(CSRC, "pi_place.cpp"),  # offline placement under a memory budget
                 os.path.join(CSRC, "pi_ranks.cpp")]  # per-layer predictor rank under a memory budget
-DEPENDS = SOURCES + HOST_SOURCES + [os.path.join(CSRC, n) for n in ("pi_kernels.hpp", "pi_sync.hpp", "pi_occupancy.hpp", "pi_tail.hpp", "pi_split.hpp", "pi_wide.hpp", "pi_paged.hpp")] + [
+DEPENDS = SOURCES + HOST_SOURCES + [os.path.join(CSRC, n) for n in ("pi_kernels.hpp", "pi_sync.hpp", "pi_occupancy.hpp", "pi_tail.hpp", "pi_split.hpp", "pi_wide.hpp", "pi_paged.hpp", "pi_paged_host.hpp", "pi_paged_launch.hpp",
+    "pi_paged_rope.hpp", "pi_paged_pages.hpp", "pi_paged_verify.hpp")] + [
                      os.path.join(ROOT, "include", "pi_sparse_ffn.h"), os.path.join(ROOT, "include", "pi_paged_kv.h")]
 OBJDIR = os.path.join(ROOT, "_build")
 
@@ -38,12 +41,13 @@ HOST_OBJS = [os.path.join(OBJDIR, os.path.basename(p).replace(".cpp", ".o")) for
 
 def _units():
     """(source, object, extra flags): the ABI unit, one tail-kernel unit per batch width, the split
-    sparse-FFN unit, the paged-attention unit."""
+    sparse-FFN unit, the paged-cache units."""
     units = [(SOURCES[0], os.path.join(OBJDIR, "pi_abi.o"), [])]
     for b in range(1, 9):
         units.append((SOURCES[1], os.path.join(OBJDIR, f"pi_persist_b{b}.o"), [f"-DPIK_B={b}"]))
     units.append((SOURCES[2], os.path.join(OBJDIR, "pi_split.o"), []))
-    units.append((SOURCES[3], os.path.join(OBJDIR, "pi_paged.o"), []))
+    for src in SOURCES[3:]:
+        units.append((src, os.path.join(OBJDIR, os.path.basename(src).replace(".hip", ".o")), []))
     return units
 
 

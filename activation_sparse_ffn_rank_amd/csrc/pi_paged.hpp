@@ -123,7 +123,7 @@ __device__ __forceinline__ uint32_t kv_block_scan(uint32_t v, uint32_t *part, ui
 // latency of its few dependent loads: a pass over 64 requests 6.4 us, 1500 with 66 thousand new tokens 9.2 us.  In place
 // the one workgroup finds all the slots: the same two take 9 and 119 us, with events around a call alone, and 9 and 12
 // with separate outputs.
-__global__ __launch_bounds__(kKvTableThreads) void k_kv_tables(KvTablesArgs a) {
+static __global__ __launch_bounds__(kKvTableThreads) void k_kv_tables(KvTablesArgs a) {
     __shared__ uint32_t s_row[PI_KV_MAX_REQ + 1];   // first row
     __shared__ uint32_t s_need[PI_KV_MAX_REQ];      // pages asked for (ended: given back) by the requests before | flags
     __shared__ uint32_t s_held[PI_KV_MAX_REQ];      // cached
@@ -295,6 +295,7 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppendArgs a) {
 struct KvAttnArgs {
     int n_pages, n_kv, page_log;
     int n_req, max_pages, max_q, max_kv, total_q, n_q, group, window;
+    int sinks;                        // first keys that stay visible (kernels with SINKS; window > 0)
     int split_target;                 // 0: key ranges are not cut
     int slots;                        // split items per kv head that the workspace holds
     int items;                        // items per kv head that the grid has
@@ -312,7 +313,16 @@ struct KvReq {
     int q0, n, m;          // first packed row, new tokens, keys
     int rows;              // query rows per kv head
     int lo, hi;            // keys that any of its rows may see
+    int first;             // SINKS: and the keys [0, first) before lo, whole blocks of 64; 0: lo is 0 or there are none
+    __device__ __forceinline__ int keys() const { return first + hi - lo; }
 };
+
+// SINKS: the first a.sinks keys stay visible behind the window.  A request's keys are then an axis of two pieces, [0, first)
+// and [lo, hi), which is what is cut and shared out; kernels walk it in blocks and step from one piece to the other, so that
+// nothing between them is read and no block holds keys of both.
+__device__ __forceinline__ int kv_first_blocks(const KvAttnArgs &a, int hi) { return (min(a.sinks, hi) + 63) & ~63; }
+
+template <bool SINKS>
 __device__ __forceinline__ KvReq kv_req(const KvAttnArgs &a, int r) {
     KvReq x;
     const int q0 = a.q_start[r], q1 = a.q_start[r + 1];
@@ -323,6 +333,47 @@ __device__ __forceinline__ KvReq kv_req(const KvAttnArgs &a, int r) {
     x.rows = min(x.n, a.max_q) * a.group;
     x.hi = (int)min((int64_t)min(x.m, a.max_kv), (int64_t)a.max_pages << a.page_log);
     x.lo = a.window ? min(max(x.m - x.n - a.window + 1, 0), x.hi) & ~63 : 0;
+    x.first = 0;
+    if constexpr (SINKS) {
+        x.first = kv_first_blocks(a, x.hi);
+        if (x.first >= x.lo) x.lo = x.first = 0;
+    }
+    return x;
+}
+
+// Keys of a row tile in blocks of KT: [a0, a1), then [lo, hi), without those that lie outside the item's piece of the request's
+// axis.  tile_lo, tile_hi: the window's keys that some row of the tile sees.  a1 < 0 without SINKS or where the first keys
+// run on into the window.
+struct KvSpan {
+    int a0, a1, lo, hi;
+    __device__ __forceinline__ int after(int kb, int step) const { return kb + step == a1 ? lo : kb + step; }
+};
+template <bool SINKS, int KT>
+__device__ __forceinline__ KvSpan kv_span(const KvAttnArgs &a, const KvReq &q, int tile_lo, int tile_hi, int splits, int split,
+                                          int piece) {
+    KvSpan x;
+    x.a0 = x.a1 = -1;
+    x.lo = max(tile_lo & ~(KT - 1), q.lo), x.hi = tile_hi;
+    if constexpr (SINKS) {
+        const int past = q.lo - q.first, first = kv_first_blocks(a, q.hi);    // key = place on the axis + past, in [lo, hi)
+        const bool apart = x.lo - past > first && tile_hi > 0;
+        if (apart) x.a0 = 0, x.a1 = first;
+        else x.lo = q.first ? q.lo : 0;
+        // (not apart: either the tile's window begins at the request's, which follows the first keys on the axis, or all of it
+        // is one piece from key 0)
+        if (!apart && q.first && tile_hi > 0) x.a0 = 0, x.a1 = q.first;
+        if (splits > 1) {
+            const int from = split * piece, to = from + piece;
+            if (x.a1 >= 0) x.a0 = max(x.a0, from), x.a1 = min(x.a1, to);
+            x.lo = max(x.lo, from + past), x.hi = min(x.hi, to + past);
+            if (x.a1 >= 0 && x.a0 >= x.a1) x.a0 = x.a1 = -1;
+        }
+        if (x.a1 >= 0 && x.hi <= x.lo) x.lo = x.a0, x.hi = x.a1, x.a0 = x.a1 = -1;
+    } else if (splits > 1) {
+        const int from = q.lo + split * piece;
+        x.lo = max(x.lo, from);
+        x.hi = min(x.hi, from + piece);
+    }
     return x;
 }
 
@@ -345,16 +396,16 @@ struct KvCut {
     float rate;          // pieces per key; 0: none is cut
     float most2;         // square of pieces, at most, per key
 };
-template <int HD, int TR>
+template <int HD, int TR, bool SINKS>
 __device__ __forceinline__ KvCut kv_cut(const KvAttnArgs &a, int lane) {
     if (!a.split_target) return {0.f, 0.f};
     float sum = 0.f, rows = 0.f;
     for (int r0 = 0; r0 < a.n_req; r0 += 64) {
         float x = 0.f, y = 0.f;
         if (r0 + lane < a.n_req) {
-            const KvReq q = kv_req(a, r0 + lane);
-            x = (float)((q.rows + TR - 1) / TR) * (float)(q.hi - q.lo);
-            y = q.hi - q.lo >= kv_min_cut(HD) ? (float)q.rows : 0.f;
+            const KvReq q = kv_req<SINKS>(a, r0 + lane);
+            x = (float)((q.rows + TR - 1) / TR) * (float)q.keys();
+            y = q.keys() >= kv_min_cut(HD) ? (float)q.rows : 0.f;
         }
         sum += wave_sum(x);
         if (TR != kKvRowTile) rows += wave_sum(y);
@@ -386,7 +437,7 @@ struct KvItem {
 };
 // ROWS > 0 counts groups of ROWS rows of the cut requests instead (for the join; split is then the group), of those whose
 // items all had a workgroup.
-template <int HD, int TR, int ROWS>
+template <int HD, int TR, int ROWS, bool SINKS>
 __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, KvCut aim, int lane) {
     KvItem it;
     it.r = -1;
@@ -395,10 +446,10 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, KvCut a
         KvReq q{};
         int tiles = 0, splits = 1, piece = 1;
         if (r0 + lane < a.n_req) {
-            q = kv_req(a, r0 + lane);
+            q = kv_req<SINKS>(a, r0 + lane);
             tiles = (q.rows + TR - 1) / TR;
-            piece = kv_piece<HD, TR>(q.hi - q.lo, aim);
-            splits = max((q.hi - q.lo + piece - 1) / piece, 1);
+            piece = kv_piece<HD, TR>(q.keys(), aim);
+            splits = max((q.keys() + piece - 1) / piece, 1);
         }
         const int cut = splits > 1 ? tiles * splits : 0;
         const int mine = ROWS == 0 ? tiles * splits : splits > 1 ? (q.rows + ROWS - 1) / (ROWS == 0 ? 1 : ROWS) : 0;
@@ -414,6 +465,7 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, KvCut a
             it.piece = bcast(piece, l);
             it.q.q0 = bcast(q.q0, l), it.q.n = bcast(q.n, l), it.q.m = bcast(q.m, l);
             it.q.rows = bcast(q.rows, l), it.q.lo = bcast(q.lo, l), it.q.hi = bcast(q.hi, l);
+            it.q.first = SINKS ? bcast(q.first, l) : 0;
             if (ROWS == 0) {
                 it.tile = at / it.splits;
                 it.split = at - it.tile * it.splits;
@@ -472,7 +524,7 @@ struct KvRowsLds {
 // mean square's root, now 2.4e-5, which is the rounding of the output alone).  Bound by HBM: 16 requests of 2k keys, 32
 // heads of 128, 275 MB in 54.7 us, and 58.7 a pass with the join; 96 heads of 3k, 1.8 GB in 315 us (5.7 TB/s).  TR:
 // rows of a split item in the workspace.
-template <class T, int HD, int TR, int WAVES>
+template <class T, int HD, int TR, int WAVES, bool SINKS>
 __device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &it, int h, KvRowsLds<HD, WAVES> &sh) {
     constexpr int kSteps = HD / 32, kTiles = HD / 16, kWaves = WAVES;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -496,15 +548,18 @@ __device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &
     const int tile_hi = min(pos_b + 1, rq.hi), tile_lo = a.window ? max(pos_a - a.window + 1, 0) : 0;
     // every row of the tile sees keys in [all_lo, all_hi)
     const int all_hi = min(pos_a + 1, rq.hi), all_lo = a.window ? max(pos_b - a.window + 1, 0) : 0;
-    int lo = max(tile_lo & ~31, rq.lo), hi = tile_hi;
-    if (it.splits > 1) {
-        const int from = rq.lo + it.split * it.piece;
-        lo = max(lo, from);
-        hi = min(hi, from + it.piece);
-    }
+    const KvSpan sp = kv_span<SINKS, 32>(a, rq, tile_lo, tile_hi, it.splits, it.split, it.piece);
     // this wave's part
-    const int part = max((((hi - lo + kWaves - 1) / kWaves) + 31) & ~31, 32);
-    const int k_lo = lo + wave * part, k_hi = min(k_lo + part, hi);
+    const int before = SINKS && sp.a1 >= 0 ? sp.a1 - sp.a0 : 0, all = before + sp.hi - sp.lo;
+    const int part = max((((all + kWaves - 1) / kWaves) + 31) & ~31, 32);
+    int k_lo = sp.lo + wave * part, k_hi = min(k_lo + part, sp.hi);
+    if constexpr (SINKS) {               // (whole blocks of 64 keys are before)
+        const int from = wave * part, to = min(from + part, all);
+        k_lo = from < before ? sp.a0 + from : sp.lo + from - before;
+        k_hi = to <= before ? sp.a0 + to : sp.lo + to - before;
+        if (from >= to) k_hi = k_lo;
+    }
+    const int sinks = SINKS ? a.sinks : 0;
 
     KvRowState<HD> st;
 #pragma unroll
@@ -561,10 +616,11 @@ __device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &
         load_k(next);
         load_v(next);
     }
-    for (int kb = k_lo; kb < k_hi; kb += 32) {
+    for (int kb = k_lo, kn; kb < k_hi; kb = kn) {
         at = next;
         const bool dead0 = at.dead0, dead1 = at.dead1, more = kb + 32 < k_hi;
-        if (more) next = find(kb + 32);
+        kn = SINKS && more ? sp.after(kb, 32) : kb + 32;
+        if (more) next = find(kn);
         float s[8];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -578,12 +634,25 @@ __device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &
         if (more) load_k(next);          // in flight during the softmax and the second product
 
         uint32_t odd_keys = 0;                           // keys of the block with an infinite or NaN value somewhere
-        if (kb < all_lo || kb + 32 > all_hi || dead0 || dead1) {
+        if ((kb < all_lo && (!SINKS || kb + 32 > sinks)) || kb + 32 > all_hi || dead0 || dead1) {
             const bool dead = g & 2 ? dead1 : dead0;
+            uint32_t kept = 0;                           // SINKS: values that some row of the tile sees, a bit each
+            if constexpr (SINKS) {
+                // (as bits: with a branch around each score, as below, one of them stayed unmasked in the code built for
+                // heads of 64)
+                const int j0 = kb + 8 * g;
+                auto below = [&](int end) { return (1u << min(max(end - j0, 0), 8)) - 1u; };
+                const uint32_t first = below(sinks), live = dead ? 0u : 0xffu;
+                const uint32_t seen = live & below(see_hi) & (~below(see_lo) | first);
+                kept = live & below(tile_hi) & (~below(tile_lo) | first);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int j = kb + 8 * g + e;
-                if (dead || j < see_lo || j >= see_hi) s[e] = -INFINITY;
+                for (int e = 0; e < 8; ++e) s[e] = seen >> e & 1 ? s[e] : -INFINITY;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int j = kb + 8 * g + e;
+                    if (dead || j < see_lo || j >= see_hi) s[e] = -INFINITY;
+                }
             }
             // Values that no row of the tile sees are cleared (0 x infinity would be NaN); those
             // that some rows see and others do not, and that are not finite, are added row by row.
@@ -591,8 +660,9 @@ __device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &
 #pragma unroll
             for (int e2 = 0; e2 < 4; ++e2) {
                 const int j = kb + 8 * g + 2 * e2;
-                const uint32_t keep = (dead || j < tile_lo || j >= tile_hi ? 0u : 0xffffu) |
-                                      (dead || j + 1 < tile_lo || j + 1 >= tile_hi ? 0u : 0xffff0000u);
+                const uint32_t keep = SINKS ? (kept >> (2 * e2) & 1 ? 0xffffu : 0u) | (kept >> (2 * e2) & 2 ? 0xffff0000u : 0u)
+                                            : (dead || j < tile_lo || j >= tile_hi ? 0u : 0xffffu) |
+                                                  (dead || j + 1 < tile_lo || j + 1 >= tile_hi ? 0u : 0xffff0000u);
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
                     uint32_t &w = e2 == 0 ? vf[t].x : e2 == 1 ? vf[t].y : e2 == 2 ? vf[t].z : vf[t].w;
@@ -650,7 +720,7 @@ __device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &
 #pragma unroll
             for (int e = 1; e < 8; ++e) mine = (j & 7) == e ? p[e] : mine;
             const float w = __shfl(mine, (j >> 3) * 16 + col);
-            if (kb + j < see_lo || kb + j >= see_hi) continue;
+            if ((kb + j < see_lo && (!SINKS || kb + j >= sinks)) || kb + j >= see_hi) continue;
             int d0 = 4 * g;
             asm volatile("" : "+v"(d0));                // its addresses are not worth registers outside this loop
             const uint16_t *x = v_head + (j & 16 ? at.b1 + at.in1 + (j & 15) : at.b0 + at.in0 + j);
@@ -715,14 +785,14 @@ __device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &
 
 // Calls in which no request has many query rows per kv head.  WAVES: 4; more for few short ranges, 1 for
 // many short ones, neither of which are cut, so that no join follows.
-template <class T, int HD, int WAVES>
+template <class T, int HD, int WAVES, bool SINKS>
 __global__ __launch_bounds__(64 * WAVES) void k_kv_rows(KvAttnArgs a) {
     __shared__ KvRowsLds<HD, WAVES> sh;
     const int lane = threadIdx.x & 63;
     const int h = blockIdx.x % a.n_kv, want = blockIdx.x / a.n_kv;
-    const KvItem it = kv_item<HD, kKvRowTile, 0>(a, want, kv_cut<HD, kKvRowTile>(a, lane), lane);
+    const KvItem it = kv_item<HD, kKvRowTile, 0, SINKS>(a, want, kv_cut<HD, kKvRowTile, SINKS>(a, lane), lane);
     if (it.r < 0) return;
-    kv_rows_item<T, HD, kKvRowTile, WAVES>(a, it, h, sh);
+    kv_rows_item<T, HD, kKvRowTile, WAVES, SINKS>(a, it, h, sh);
 }
 
 // One workgroup: one item of 128 query rows of one kv head, 32 of them per wave, over one key
@@ -785,7 +855,7 @@ __device__ __forceinline__ uint64_t kv_dead_bits(uint32_t m) {
 // beside two chunks of 777, 56 heads of 128: 165 us without this path, 156 with it, 147 a pass now, the join
 // included.  Without such requests it stays out of the kernel, whose registers then serve the one loop: a 4096-token
 // chunk 1009 -> 953.)
-template <class T, int HD, int P, bool MIXED>
+template <class T, int HD, int P, bool MIXED, bool SINKS>
 __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_tile(KvAttnArgs a) {
     typedef KvTile<HD, P> L;
     constexpr int KT = L::kKeys, kSub = KT / 32, kSteps = HD / 16, kTiles = HD / 32;
@@ -798,12 +868,12 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 31, half = lane >> 5;
     const int h = blockIdx.x % a.n_kv, want = blockIdx.x / a.n_kv;
-    const KvItem it = kv_item<HD, kKvWideTile, 0>(a, want, kv_cut<HD, kKvWideTile>(a, lane), lane);
+    const KvItem it = kv_item<HD, kKvWideTile, 0, SINKS>(a, want, kv_cut<HD, kKvWideTile, SINKS>(a, lane), lane);
     if (it.r < 0) return;
     const KvReq &rq = it.q;
     if constexpr (MIXED) {
         if (rq.rows <= kKvRowTile) {
-            kv_rows_item<T, HD, kKvWideTile, kKvRowWaves>(a, it, h, s_mem.rows);
+            kv_rows_item<T, HD, kKvWideTile, kKvRowWaves, SINKS>(a, it, h, s_mem.rows);
             return;
         }
     }
@@ -823,13 +893,9 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
     // keys that some row of the workgroup sees, within the item's chunk
     const int pos_first = past + tile * kKvWideTile / a.group;
     const int pos_last = past + (min((tile + 1) * kKvWideTile, rq.rows) - 1) / a.group;
-    int lo = a.window ? max(pos_first - a.window + 1, 0) : 0, hi = min(pos_last + 1, rq.hi);
-    lo = max(lo & ~(KT - 1), rq.lo);
-    if (it.splits > 1) {
-        const int from = rq.lo + it.split * it.piece;
-        lo = max(lo, from);
-        hi = min(hi, from + it.piece);
-    }
+    const KvSpan sp = kv_span<SINKS, KT>(a, rq, a.window ? max(pos_first - a.window + 1, 0) : 0, min(pos_last + 1, rq.hi), it.splits,
+                                         it.split, it.piece);
+    const int lo = SINKS && sp.a1 >= 0 ? sp.a0 : sp.lo, hi = sp.hi, sinks = SINKS ? a.sinks : 0;
     // keys that some row of this wave sees, and those that all of them see
     const int wrow = tile * kKvWideTile + wave * 32;
     const int pos_a = past + min(wrow, rq.rows - 1) / a.group, pos_b = past + (min(wrow + 32, rq.rows) - 1) / a.group;
@@ -912,11 +978,12 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
     uint32_t dead_next = 0;
     int buf = 0;
     if (lo < hi) dead_next = load(lo, 0);
-    for (int kb = lo; kb < hi; kb += KT, buf ^= 1) {
+    for (int kb = lo, kn; kb < hi; kb = kn, buf ^= 1) {
+        kn = SINKS ? sp.after(kb, KT) : kb + KT;
         const uint32_t dead = dead_next;
         kv_lds_wait();
         __syncthreads();                 // block kb is in LDS, and every wave is done with the buffer before it
-        if (kb + KT < hi) dead_next = load(kb + KT, buf ^ 1);
+        if (kn < hi) dead_next = load(kn, buf ^ 1);
         uint16_t *const sk = s_kv[buf][0], *const sv = s_kv[buf][1];
         // Values past the request's keys and of missing pages may hold anything and are cleared (0 x infinity would be
         // NaN), in LDS, by all waves.
@@ -929,7 +996,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
             }
             __syncthreads();
         }
-        if (kb >= wave_hi || kb + KT <= wave_lo) continue;
+        if (kb >= wave_hi || (kb + KT <= wave_lo && (!SINKS || kb >= sinks))) continue;
 
         f32x16 s[kSub];
 #pragma unroll
@@ -943,12 +1010,13 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
                 s[u] = T::mfma32(*reinterpret_cast<const uint4 *>(sk + key * HD + unit * 8), qf[t], s[u]);
             }
         }
-        const bool edge = kb < all_lo || kb + KT > all_hi || dead != 0;
+        const bool edge = (kb < all_lo && (!SINKS || kb + KT > sinks)) || kb + KT > all_hi || dead != 0;
+        const uint64_t kept = SINKS ? kv_bits((uint32_t)min(max(sinks - kb, 0), KT)) : 0;    // first keys of the block
         if (edge) {
             // the keys that this lane's row sees, a bit each; its half holds every other 8 of them
             const uint32_t n_all = KT == 64 ? 64 : 32;
             const uint32_t from = (uint32_t)min(max(see_lo - kb, 0), (int)n_all), to = (uint32_t)min(max(see_hi - kb, 0), (int)n_all);
-            uint64_t see = kv_bits(to) & ~kv_bits(from) & ~kv_dead_bits(dead);
+            uint64_t see = kv_bits(to) & (~kv_bits(from) | kept) & ~kv_dead_bits(dead);
             see >>= 8 * half;
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
@@ -991,7 +1059,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
         };
         auto clear = [&](uint4 x, int j) -> uint4 { return kv_clear(x, (uint32_t)(drop >> (16 * j + 8 * half))); };
         if (careful && edge) {
-            drop = ~kv_bits((uint32_t)min(wave_hi - kb, KT)) | kv_bits((uint32_t)min(max(wave_lo - kb, 0), KT));
+            drop = ~kv_bits((uint32_t)min(wave_hi - kb, KT)) | (kv_bits((uint32_t)min(max(wave_lo - kb, 0), KT)) & ~kept);
             uint64_t odd_keys = 0;
 #pragma unroll 1
             for (int j = 0; j < 2 * kSub; ++j) {
@@ -1021,7 +1089,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
 #pragma unroll
                     for (int i = 0; i < 16; ++i) mine = (32 * u + 16 * (i >> 3) + (i & 7)) == (j & ~8) ? s[u][i] : mine;
                 const float w = __shfl(mine, (j & 8 ? 32 : 0) + col);
-                if (kb + j < see_lo || kb + j >= see_hi) continue;
+                if ((kb + j < see_lo && (!SINKS || kb + j >= sinks)) || kb + j >= see_hi) continue;
                 int d0 = 4 * half;
                 asm volatile("" : "+v"(d0));        // its addresses are not worth registers outside this loop
 #pragma unroll
@@ -1107,18 +1175,18 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
 // few rows of one kv head at a time (a row per HD / 4 lanes, 16 bytes each), its four waves a quarter of the pieces
 // each, kDeep of them in flight; the quarters are added in order.  The grid does not depend on how many requests are
 // cut: with none it ends at once.  Bound by latency, 5 to 8 us, of which 4 to 5 to find that there is nothing to do.
-template <class T, int HD, int TR>
+template <class T, int HD, int TR, bool SINKS>
 __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
     constexpr int kLanes = HD / 4, kRows = 64 / kLanes, kDeep = 8, kWaves = 4;
     __shared__ f32x4 s_o[kWaves][64];
     __shared__ float s_ref[kWaves][64], s_sum[kWaves][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const KvCut cut = kv_cut<HD, TR>(a, lane);
+    const KvCut cut = kv_cut<HD, TR, SINKS>(a, lane);
     const int64_t stride = (int64_t)a.n_kv * (TR * (HD + 2));
     const int d = (lane % kLanes) * 4;
     for (int u = blockIdx.x;; u += gridDim.x) {
         const int h = u % a.n_kv, want = u / a.n_kv;
-        const KvItem it = kv_item<HD, TR, kRows>(a, want, cut, lane);
+        const KvItem it = kv_item<HD, TR, kRows, SINKS>(a, want, cut, lane);
         if (it.r == -1) return;
         if (it.r < 0) continue;
         const int row = it.split * kRows + lane / kLanes, row_c = min(row, it.q.rows - 1), prow = row_c - it.tile * TR;

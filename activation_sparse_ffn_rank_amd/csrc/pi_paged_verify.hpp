@@ -1,0 +1,224 @@
+// pi_paged_verify.hpp -- gfx950 kernels that decide which drafted tokens stay and draw the next one (k_kv_verify_sum,
+// k_kv_verify_pick).
+//
+// The acceptance tests need two numbers each; the sample needs one row of the target's probabilities and, after a
+// rejection, one of the draft's.  That row is cut into pieces of kKvPiece entries whose weights are summed first; the piece in
+// which the running sum passes its mark is then read once more, from L2.
+#pragma once
+
+#include "pi_paged.hpp"
+
+namespace pik {
+
+constexpr int kKvPieceLog = 10, kKvPiece = 1 << kKvPieceLog;
+constexpr int kKvMaxPieces = PI_KV_MAX_VOCAB / kKvPiece;
+
+struct KvVerifyArgs {
+    int n_req, rows, vocab, pieces, per_wave;
+    int64_t p_stride, q_stride;
+    const int *q_start, *tokens, *kv_len;
+    const float *p, *q, *u_accept, *u_next;
+    int *accepted, *next, *keep;
+    double *sums;                  // [n_req][pieces]
+};
+
+struct KvVerdict {
+    int rows, accepted;            // of the request; rows = 0: none, or a range out of bounds
+    int at;                        // the row after the accepted drafts
+    bool rejected;
+    int token;                     // the rejected draft
+};
+// Lanes test 64 drafts at a time.  All lanes return the same.
+__device__ __forceinline__ KvVerdict kv_verdict(const KvVerifyArgs &a, int r, int lane) {
+    KvVerdict x{0, 0, 0, false, -1};
+    const int start = a.q_start[r], end = a.q_start[r + 1];
+    if (start < 0 || end <= start || end > a.rows) return x;
+    x.rows = end - start;
+    for (int i0 = 0; i0 < x.rows - 1; i0 += 64) {
+        const int i = i0 + lane, t = start + i;
+        bool ok = true;
+        int token = -1;
+        if (i < x.rows - 1) {
+            token = a.tokens[t + 1];
+            ok = false;
+            if ((uint32_t)token < (uint32_t)a.vocab) {
+                const double q = a.q ? (double)a.q[t * a.q_stride + token] : 1.0;
+                ok = (double)a.u_accept[t] * q < (double)a.p[t * a.p_stride + token];
+            }
+        }
+        const uint64_t bad = __ballot(!ok);
+        if (bad) {
+            const int l = __builtin_ctzll(bad);
+            x.accepted = i0 + l;
+            x.rejected = true;
+            x.token = bcast(token, l);
+            break;
+        }
+        x.accepted = min(i0 + 64, x.rows - 1);
+    }
+    x.at = start + x.accepted;
+    return x;
+}
+
+// Four neighbouring floats at a 4-byte aligned address.
+struct KvQuad {
+    float v[4];
+} __attribute__((packed, aligned(4)));
+
+// Weights of entries j .. j+3 of the row that is drawn from.  q NULL: all of the draft's probability is on `token`.
+struct KvWeights {
+    const float *p, *q;
+    int vocab, token;              // token < 0: none is left out
+    __device__ __forceinline__ double weight(double p_j, double q_j, int j) const {
+        const double w = p_j - q_j;
+        return w > 0.0 && j != token ? w : 0.0;            // (NaN: 0)
+    }
+    __device__ __forceinline__ void load(int j, KvQuad &x, KvQuad &y) const {
+        y = KvQuad{{0.f, 0.f, 0.f, 0.f}};
+        if (j + 4 <= vocab) {
+            x = *reinterpret_cast<const KvQuad *>(p + j);
+            if (q) y = *reinterpret_cast<const KvQuad *>(q + j);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x.v[i] = j + i < vocab ? p[j + i] : 0.f;
+                if (q) y.v[i] = j + i < vocab ? q[j + i] : 0.f;
+            }
+        }
+    }
+};
+__device__ __forceinline__ KvWeights kv_weights_of(const KvVerifyArgs &a, const KvVerdict &v, bool rest) {
+    return {a.p + v.at * a.p_stride, rest && a.q ? a.q + v.at * a.q_stride : nullptr, a.vocab, rest && !a.q ? v.token : -1};
+}
+
+__device__ __forceinline__ double kv_wave_sum(double x) {
+#pragma unroll
+    for (int b = 1; b < 64; b <<= 1) x += __shfl_xor(x, b);
+    return x;
+}
+
+// Sum of piece i of a row, by one wave.
+__device__ __forceinline__ double kv_piece_sum(const KvWeights &w, int i, int lane) {
+    constexpr int kLoads = kKvPiece / 256;
+    KvQuad x[kLoads], y[kLoads];
+    const int j0 = (i << kKvPieceLog) + lane * 4;
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) w.load(j0 + k * 256, x[k], y[k]);
+    double sum = 0.0;
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum += w.weight(x[k].v[e], y[k].v[e], j0 + k * 256 + e);
+    return kv_wave_sum(sum);
+}
+
+static __global__ __launch_bounds__(256) void k_kv_verify_sum(KvVerifyArgs a) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = blockIdx.y;
+    const int i0 = (blockIdx.x * 4 + wave) * a.per_wave, i1 = min(i0 + a.per_wave, a.pieces);
+    if (i0 >= i1) return;
+    const KvVerdict v = kv_verdict(a, r, lane);
+    if (v.rows == 0) return;
+    const KvWeights w = kv_weights_of(a, v, v.rejected);
+    for (int i = i0; i < i1; ++i) {
+        const double sum = kv_piece_sum(w, i, lane);
+        if (lane == 0) a.sums[(int64_t)r * a.pieces + i] = sum;
+    }
+}
+
+// Sum over the threads before this one, in a fixed order; *total: of all.  sums: one per thread.
+__device__ __forceinline__ double kv_block_sums(double x, double *sums, double *part, double *total) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
+#pragma unroll
+    for (int b = 1; b < 64; b <<= 1) {
+        const double y = __shfl_up(x, b);
+        if (lane >= b) x += y;
+    }
+    __syncthreads();                       // what the call before left may still be read
+    if (lane == 63) part[wave] = x;
+    __syncthreads();
+    double before = 0.0, all = 0.0;
+    for (int w = 0; w < waves; ++w) {
+        before += w < wave ? part[w] : 0.0;
+        all += part[w];
+    }
+    *total = all;
+    sums[tid] = before + x;
+    __syncthreads();
+    return tid ? sums[tid - 1] : 0.0;
+}
+
+// One workgroup per request: the piece, and the entry in it.  An entry without weight is never taken, and where rounding
+// leaves none above the mark it is the last one with weight.
+static __global__ __launch_bounds__(256) void k_kv_verify_pick(KvVerifyArgs a) {
+    __shared__ double s_part[4], s_sums[256], s_piece[kKvMaxPieces], s_before;
+    __shared__ int s_first, s_last;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = blockIdx.x;
+    const KvVerdict v = kv_verdict(a, r, lane);
+    if (tid == 0) {
+        a.accepted[r] = v.accepted;
+        if (a.keep) a.keep[r] = a.kv_len[r] - max(v.rows - 1 - v.accepted, 0);
+        if (v.rows == 0) a.next[r] = -1;
+        s_first = INT32_MAX, s_last = -1;
+    }
+    if (v.rows == 0) return;
+    KvWeights w = kv_weights_of(a, v, v.rejected);
+    for (int i = tid; i < a.pieces; i += 256) s_piece[i] = a.sums[(int64_t)r * a.pieces + i];
+    const int per = (a.pieces + 255) / 256, i0 = tid * per, i1 = min(i0 + per, a.pieces);
+    double upto, total;
+    for (bool again = false;; again = true) {
+        __syncthreads();
+        double mine = 0.0;
+        for (int i = i0; i < i1; ++i) mine += s_piece[i];
+        upto = kv_block_sums(mine, s_sums, s_part, &total);
+        if (total > 0.0 || again || !v.rejected) break;
+        // nothing is left of the rest: the target's own weights
+        w = kv_weights_of(a, v, false);
+        for (int i = wave; i < a.pieces; i += 4) {
+            const double sum = kv_piece_sum(w, i, lane);
+            if (lane == 0) s_piece[i] = sum;
+        }
+    }
+    if (!(total > 0.0)) {
+        if (tid == 0) a.next[r] = -1;
+        return;
+    }
+    const double mark = (double)a.u_next[r] * total;
+    // the first of this thread's pieces to pass the mark, and its last one, with the sums before them
+    int first = INT32_MAX, last = -1;
+    double to_first = 0.0, to_last = 0.0;
+    for (int i = i0; i < i1; ++i) {
+        if (!(s_piece[i] > 0.0)) continue;
+        last = i, to_last = upto;
+        if (first == INT32_MAX && upto + s_piece[i] > mark) first = i, to_first = upto;
+        upto += s_piece[i];
+    }
+    if (first != INT32_MAX) atomicMin(&s_first, first);
+    if (last >= 0) atomicMax(&s_last, last);
+    __syncthreads();
+    const int piece = s_first != INT32_MAX ? s_first : s_last;
+    if (piece == first) s_before = to_first;
+    else if (piece == last) s_before = to_last;
+    __syncthreads();
+    if (tid == 0) s_first = INT32_MAX, s_last = -1;
+    const int j0 = (piece << kKvPieceLog) + tid * 4;
+    KvQuad x, y;
+    w.load(j0, x, y);
+    double each[4], sum = 0.0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum += each[e] = w.weight(x.v[e], y.v[e], j0 + e);
+    double at = kv_block_sums(sum, s_sums, s_part, &total) + s_before;
+    first = INT32_MAX, last = -1;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        at += each[e];
+        if (!(each[e] > 0.0)) continue;
+        last = j0 + e;
+        if (first == INT32_MAX && at > mark) first = j0 + e;
+    }
+    if (first != INT32_MAX) atomicMin(&s_first, first);
+    if (last >= 0) atomicMax(&s_last, last);
+    __syncthreads();
+    if (tid == 0) a.next[r] = s_first != INT32_MAX ? s_first : s_last;
+}
+
+}  // namespace pik

@@ -10,6 +10,9 @@
  *   pi_kv_step    lengths -> block tables, slot map, packed row starts, key counts
  *   pi_kv_append  the step's new keys and values into their slots
  *   pi_kv_attn    attention of the step's new tokens over the pages
+ * Around it: pi_kv_rope_append (the append with rotary positions and head norms), pi_kv_attn_sinks (attention over a window
+ * and the first tokens), pi_kv_verify (which drafted tokens stay), pi_kv_release, pi_kv_fork and pi_kv_copy (pages given back,
+ * shared and copied).
  *
  * Attention of one request with n new tokens and m = kv_len keys (the new ones included): its token
  * i (0 <= i < n) stands at position p = m - n + i and sees the keys j with
@@ -115,6 +118,132 @@ size_t pi_kv_attn_workspace_bytes(const pi_kv_cache *cache, const pi_kv_batch *b
 int pi_kv_attn(const pi_kv_cache *cache, const pi_kv_batch *batch, const void *q, int64_t q_token_stride,
                int64_t q_head_stride, void *out, int64_t out_token_stride, int64_t out_head_stride,
                int32_t total_q, int32_t n_q, float scale, int32_t window, void *ws, size_t ws_bytes, void *stream);
+
+/* ---- rotary positions and head norms with the append ----
+ *
+ * Frequencies of rotary positions, in radians per position: freq[i] = f_i, i < rot_dim / 2, with
+ *   b_i = base^(-2 i / rot_dim),   t_i = trained * b_i / (2 pi)   (turns over the trained positions),
+ *   g_i = min(max((t_i - low) / (high - low), 0), 1),             f_i = b_i (g_i + (1 - g_i) / factor).
+ * factor 1 gives b_i; low = high = 0 divides all of them by factor (positions interpolated evenly); otherwise those of
+ * fewer than `low` turns are divided and those of more than `high` kept.  rot_dim: even, 2 to 256; base, factor, trained
+ * finite and above zero, 0 <= low < high (or both 0).  freq is HOST memory; synchronous. */
+int pi_rope_frequencies(int32_t rot_dim, double base, double factor, double trained, double low, double high, double *freq);
+
+/* Which elements of a head form pairs: i and i + rot_dim/2, or 2i and 2i + 1. */
+typedef enum { PI_ROPE_HALF = 0, PI_ROPE_PAIRS = 1 } pi_rope_layout;
+
+/* What is done to a head x of q and k.  With norm != 0 first x <- x / sqrt(mean(x^2) + eps) * weight over all of its
+ * head_dim elements (a weight of NULL: ones; weights in the cache's element type, 16-byte aligned).  Then the pairs (a, b) of its
+ * first rot_dim elements (a multiple of 16, at most head_dim; 0: none) become scale * (a cos - b sin, a sin + b cos) of the
+ * angle position * freq[i]; the other elements stay.  All in fp32 (angles reduced in fp64), rounded once.  eps >= 0 and
+ * scale are finite. */
+typedef struct pi_kv_rope {
+    int32_t rot_dim, layout, norm;
+    float scale, eps;
+    const double *freq;              /* [rot_dim / 2] radians per position, device memory */
+    const void *q_weight, *k_weight; /* [head_dim] each, or NULL */
+} pi_kv_rope;
+
+/* pi_kv_append of new keys turned as `rope` says and of new values, and the step's queries turned the same way to q_out, in
+ * one pass.  Row q_start[r] + i of the packed rows stands at position kv_len[r] - n + i (of batch, max_q and max_kv bound
+ * nothing here and the table is not read).  Rows that belong to no request are left alone: not appended, q_out not written.
+ * q_start must not decrease (rows of ranges that do may be left out).  Slots, strides and pointers are as in pi_kv_append and
+ * pi_kv_attn; q_out may be q itself with the same strides, and overlaps no other argument.  total_q = 0 does nothing. */
+int pi_kv_rope_append(const pi_kv_cache *cache, const pi_kv_batch *batch, const pi_kv_rope *rope, const void *q,
+                      int64_t q_token_stride, int64_t q_head_stride, const void *k, int64_t k_token_stride,
+                      int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                      const int32_t *slots, void *q_out, int64_t out_token_stride, int64_t out_head_stride, int32_t total_q,
+                      int32_t n_q, void *stream);
+
+/* ---- attention over a window and the first tokens ----
+ *
+ * pi_kv_attn in which the first `sinks` keys of a request stay visible: the token at position p sees the keys j with
+ *   j <= p  and  (j > p - window  or  j < sinks).
+ * sinks >= 0 (0: pi_kv_attn with this window), window > 0 with sinks.  Pages between the first tokens and the windows of a step's tokens
+ * are not read: their table entries may be out of range (pi_kv_release).  All else, the workspace included, is as in
+ * pi_kv_attn; its size depends on window and sinks. */
+size_t pi_kv_attn_sinks_workspace_bytes(const pi_kv_cache *cache, const pi_kv_batch *batch, int32_t total_q, int32_t n_q,
+                                        int32_t window, int32_t sinks);
+int pi_kv_attn_sinks(const pi_kv_cache *cache, const pi_kv_batch *batch, const void *q, int64_t q_token_stride,
+                     int64_t q_head_stride, void *out, int64_t out_token_stride, int64_t out_head_stride, int32_t total_q,
+                     int32_t n_q, float scale, int32_t window, int32_t sinks, void *ws, size_t ws_bytes, void *stream);
+
+/* ---- drafted tokens ----
+ *
+ * A step whose requests carry their last token and then their drafts (rows q_start[r] .. q_start[r+1]-1 of the packed
+ * tokens) gives the target's probabilities of what follows each row.  The draft in row t + 1, x = tokens[t + 1], is accepted if
+ *   u_accept[t] * q[t][x] < p[t][x]
+ * and all drafts before it are; q is the distribution that it was drawn from (NULL: all of it on x).  With a the number
+ * accepted of n - 1 drafts and t = q_start[r] + a the row after them, the next token is drawn from the weights
+ *   w_j = max(p[t][j] - q[t][j], 0)  if a draft was rejected,   w_j = max(p[t][j], 0)  if none was (or the former are all 0)
+ * as the first j with w_0 + .. + w_j > u_next[r] * (w_0 + w_1 + ..) -- which leaves every token with the target's
+ * probability.  Products, differences and sums are in 64 bits; a NaN counts as a weight of 0 and rejects; where no j passes (u_next
+ * at or above 1) it is the last one with a weight above 0.  tokens outside [0, vocab) are rejected, and have no part of w.
+ * accepted [n_req] = a; next [n_req], -1 if all weights are 0 or the request has no rows (q_start negative,
+ * decreasing or past `rows` included); keep [n_req], with kv_len the keys of the step's attention, = kv_len - (n - 1 - a), the
+ * positions that stay (pi_kv_release's drop_from).  kv_len and keep: both or neither NULL, and keep may be kv_len. */
+#define PI_KV_MAX_VOCAB (1 << 22)
+typedef struct pi_kv_drafts {
+    int32_t n_req, rows, vocab;
+    const int32_t *q_start;          /* [n_req + 1] */
+    const int32_t *tokens;           /* [rows] */
+    const float *target;             /* [rows][vocab] p, row stride in elements, 4-byte aligned */
+    int64_t target_stride;
+    const float *draft;              /* [rows][vocab] q or NULL; the last row of a request is not read */
+    int64_t draft_stride;
+    const float *u_accept;           /* [rows], in [0, 1); the last one of a request is not read */
+    const float *u_next;             /* [n_req], in [0, 1) */
+} pi_kv_drafts;
+
+/* The workspace is 16-byte aligned and needs no zero fill.  Results do not depend on timing. */
+size_t pi_kv_verify_workspace_bytes(const pi_kv_drafts *drafts);
+int pi_kv_verify(const pi_kv_drafts *drafts, const int32_t *kv_len, int32_t *accepted, int32_t *next, int32_t *keep, void *ws,
+                 size_t ws_bytes, void *stream);
+
+/* ---- pages given back, shared and copied ----
+ *
+ * Requests may share pages: shares[p] counts the owners of page p beyond the first (0 for a page that pi_kv_step hands out,
+ * which knows nothing of shares).  Only full pages are shared, so appends never touch one.  A request that
+ * shares pages, or has given pages back from its middle, ends by pi_kv_release (drop_from 0), not by fresh < 0 of pi_kv_step.
+ *
+ * The state is pi_kv_step's: pages of positions below cached[r] in block_table, the free ones in the ring.  Both calls judge
+ * it as it stands before them.  cached_next may be cached and pool_next may be pool, itself in both cases; no other arrays may
+ * overlap. */
+typedef struct pi_kv_pages {
+    int32_t n_req, page, n_pages, max_pages;
+    int64_t table_stride;
+    const int32_t *cached;           /* [n_req] */
+    int32_t *free_ring;              /* [n_pages] */
+    const int32_t *pool;             /* [2] */
+    int32_t *block_table;            /* [n_req][max_pages] */
+    int32_t *shares;                 /* [n_pages] */
+    int32_t *cached_next;            /* [n_req] */
+    int32_t *pool_next;              /* [2] */
+    int32_t *counts;                 /* [4] */
+} pi_kv_pages;
+
+/* Gives up the positions drop_from[r] .. drop_to[r]-1 of every request (drop_to NULL: to the end; a negative drop_from is 0;
+ * none where drop_from >= cached): the pages all of whose held positions lie among them.
+ *  - drop_to >= cached cuts the request: cached_next = drop_from (what its table holds past that is void).  If that lies inside
+ *    a page with further owners, the request gives up that page too and takes a free one in its place: copies[r] = {old, new}
+ *    (pi_kv_copy makes the copy, before the next append), else {-1, -1}.  Such a request is refused, and nothing of it
+ *    changes, if the free pages do not suffice; requests are served in order.
+ *  - drop_to < cached drops from the middle: cached_next = cached, the dropped entries become -1 (pages without keys).
+ * A page given up once more than it has further owners goes behind the free ones, in the order of first mention (requests in order,
+ * a page given up for a copy before the later ones); entries outside [0, n_pages) are skipped.  cached outside [0, max_pages * page]
+ * is refused.  counts = {entries given up, pages gone back, pages taken, requests refused}. */
+int pi_kv_release(const pi_kv_pages *pages, const int32_t *drop_from, const int32_t *drop_to, int32_t *copies, void *stream);
+
+/* Makes request dst[i], which must hold nothing (cached 0), a copy of request src[i], i < n_fork: its full pages are shared, of
+ * a partly filled last one a copy is due: copies[i] = {old, new}, else {-1, -1}.  Refused, with nothing changed: src or dst out
+ * of range or equal, dst holding something or named by an earlier fork, cached[src] out of range, free pages that do not suffice
+ * (forks are served in order).  cached_next = cached but for the forks.  counts = {forks made, entries shared, pages taken,
+ * forks refused}.  0 <= n_fork <= PI_KV_MAX_REQ. */
+int pi_kv_fork(const pi_kv_pages *pages, const int32_t *src, const int32_t *dst, int32_t n_fork, int32_t *copies, void *stream);
+
+/* Copies keys and values of page copies[i][0] to page copies[i][1], i < n.  Pairs with an entry out of range are skipped; no
+ * destination may be named twice or be a source. */
+int pi_kv_copy(const pi_kv_cache *cache, const int32_t *copies, int32_t n, void *stream);
 
 #ifdef __cplusplus
 }
