@@ -30,7 +30,8 @@ from ._abi import (PI_F16, PI_MAX_BATCH, PI_Q4_0, PiError, make_ffn, make_predic
                    pi_status_string, pi_version, pi_workspace_bytes)
 from ._kv import (PI_KV_BF16, PI_KV_F16, PI_ROPE_HALF, PI_ROPE_PAIRS, make_kv_batch, make_kv_cache, make_kv_drafts, make_kv_pages,
                   make_kv_rope, make_kv_tables, pi_kv_append, pi_kv_attn, pi_kv_attn_sinks,
-                  pi_kv_attn_sinks_workspace_bytes, pi_kv_attn_workspace_bytes, pi_kv_copy, pi_kv_fork, pi_kv_release,
+                  pi_kv_attn_sinks_workspace_bytes, pi_kv_attn_workspace_bytes, pi_kv_copy, pi_kv_fork,
+                  pi_kv_pages_workspace_bytes, pi_kv_release,
                   pi_kv_rope_append, pi_kv_step, pi_kv_verify, pi_kv_verify_workspace_bytes, pi_rope_frequencies)
 from .layer import DeviceLayer
 
@@ -38,5 +39,5 @@ __all__ = ["PI_F16", "PI_Q4_0", "PI_MAX_BATCH", "PiError", "make_ffn", "make_pre
            "pi_ffn_layer", "pi_ffn_layer_from_hidden", "pi_predict_hidden", "pi_predict", "pi_sparse_ffn", "pi_status_string", "pi_version", "pi_workspace_bytes",
            "DeviceLayer", "PI_KV_F16", "PI_KV_BF16", "make_kv_batch", "make_kv_cache", "make_kv_tables", "pi_kv_append",
            "pi_kv_attn", "pi_kv_attn_workspace_bytes", "pi_kv_step", "PI_ROPE_HALF", "PI_ROPE_PAIRS", "make_kv_drafts", "make_kv_pages",
-           "make_kv_rope", "pi_kv_attn_sinks", "pi_kv_attn_sinks_workspace_bytes", "pi_kv_copy", "pi_kv_fork", "pi_kv_release",
+           "make_kv_rope", "pi_kv_attn_sinks", "pi_kv_attn_sinks_workspace_bytes", "pi_kv_copy", "pi_kv_fork", "pi_kv_pages_workspace_bytes", "pi_kv_release",
            "pi_kv_rope_append", "pi_kv_verify", "pi_kv_verify_workspace_bytes", "pi_rope_frequencies"]

@@ -27,7 +27,7 @@ KV_DTYPES = {torch.float16: PI_KV_F16, torch.bfloat16: PI_KV_BF16}
 # Every function the header declares; the CPU tests check that libpi.so exports them all.
 KV_EXPORTS = ("pi_kv_step", "pi_kv_append", "pi_kv_attn_workspace_bytes", "pi_kv_attn", "pi_rope_frequencies",
               "pi_kv_rope_append", "pi_kv_attn_sinks_workspace_bytes", "pi_kv_attn_sinks", "pi_kv_verify_workspace_bytes",
-              "pi_kv_verify", "pi_kv_release", "pi_kv_fork", "pi_kv_copy")
+              "pi_kv_verify", "pi_kv_pages_workspace_bytes", "pi_kv_release", "pi_kv_fork", "pi_kv_copy")
 
 _i32, _i64, _vp, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
 
@@ -62,7 +62,7 @@ class pi_kv_drafts(ctypes.Structure):
 class pi_kv_pages(ctypes.Structure):
     _fields_ = [("n_req", _i32), ("page", _i32), ("n_pages", _i32), ("max_pages", _i32), ("table_stride", _i64),
                 ("cached", _vp), ("free_ring", _vp), ("pool", _vp), ("block_table", _vp), ("shares", _vp), ("cached_next", _vp),
-                ("pool_next", _vp), ("counts", _vp)]
+                ("pool_next", _vp), ("counts", _vp), ("ws", _vp), ("ws_bytes", _sz)]
 
 
 _kv_lib = None
@@ -96,6 +96,8 @@ def kv_lib() -> ctypes.CDLL:
         L.pi_kv_verify_workspace_bytes.argtypes = [P(pi_kv_drafts)]
         L.pi_kv_verify.restype = ctypes.c_int
         L.pi_kv_verify.argtypes = [P(pi_kv_drafts), _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+        L.pi_kv_pages_workspace_bytes.restype = _sz
+        L.pi_kv_pages_workspace_bytes.argtypes = [P(pi_kv_pages)]
         L.pi_kv_release.restype = ctypes.c_int
         L.pi_kv_release.argtypes = [P(pi_kv_pages), _vp, _vp, _vp, _vp]
         L.pi_kv_fork.restype = ctypes.c_int
@@ -462,9 +464,11 @@ def pi_kv_verify(drafts: pi_kv_drafts, accepted: torch.Tensor, next: torch.Tenso
 # ------------------------------------------------------------------------------ pages given back, shared and copied
 
 def make_kv_pages(cached: torch.Tensor, free_ring: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, page: int,
-                  shares: torch.Tensor, cached_next: torch.Tensor, pool_next: torch.Tensor, counts: torch.Tensor) -> pi_kv_pages:
+                  shares: torch.Tensor, cached_next: torch.Tensor, pool_next: torch.Tensor, counts: torch.Tensor,
+                  ws: torch.Tensor | None = None) -> pi_kv_pages:
     """Descriptor of the block tables' state for pi_kv_release and pi_kv_fork (int32 tensors, as of make_kv_tables, and shares
-    [n_pages], the owners of each page beyond the first); cached_next may be cached and pool_next may be pool."""
+    [n_pages], the owners of each page beyond the first); cached_next may be cached and pool_next may be pool.  Without ws
+    (at least pi_kv_pages_workspace_bytes of any type) the descriptor has a workspace of its own."""
     fn = "make_kv_pages"
     at = _ints(fn, cached, -1)
     n = cached.shape[0]
@@ -474,9 +478,19 @@ def make_kv_pages(cached: torch.Tensor, free_ring: torch.Tensor, pool: torch.Ten
     n_pages = free_ring.shape[0]
     p = pi_kv_pages(n, page, n_pages, cols, stride, at, ring, _ints(fn, pool, 2), table, _ints(fn, shares, n_pages),
                     _ints(fn, cached_next, n), _ints(fn, pool_next, 2), _ints(fn, counts, 4))
-    p._keep = (cached, free_ring, pool, block_table, shares, cached_next, pool_next, counts)
+    if ws is None:
+        ws = torch.empty(max(16, pi_kv_pages_workspace_bytes(p)), dtype=torch.uint8, device=cached.device)
+    if not ws.is_contiguous():
+        raise PiError(fn, PI_ERR_WORKSPACE)
+    p.ws, p.ws_bytes = ws.data_ptr(), ws.nbytes
+    p._keep = (cached, free_ring, pool, block_table, shares, cached_next, pool_next, counts, ws)
     p._device = _device(fn, *p._keep)
     return p
+
+
+def pi_kv_pages_workspace_bytes(pages: pi_kv_pages) -> int:
+    """Bytes of workspace the state's calls need (0: invalid)."""
+    return int(kv_lib().pi_kv_pages_workspace_bytes(pages))
 
 
 def _copies(fn: str, t, n: int) -> int:

@@ -18,6 +18,15 @@ int check_pages(const pi_kv_pages *p) {
     return PI_OK;
 }
 
+// Entries of all requests at most beyond which the list may be long: the launches for that follow.
+constexpr int64_t kShortTables = 32768;
+bool long_lists(const pi_kv_pages *p) { return (int64_t)p->n_req * p->max_pages > kShortTables; }
+
+size_t bytes_of(const pi_kv_pages *p) { return long_lists(p) ? KvReleaseWs::kInts * sizeof(int32_t) : 16; }
+
+// Threads of a workgroup that holds four requests or forks each at most: few where there are few, for the barriers' sake.
+int threads_for(int n) { return n <= 256 ? 256 : kKvTableThreads; }
+
 KvPagesArgs args_of(const pi_kv_pages *p) {
     return {p->n_req, page_log(p->page), p->n_pages, p->max_pages, p->table_stride, p->cached, p->free_ring, p->pool,
             p->block_table, p->shares, p->cached_next, p->pool_next, p->counts};
@@ -25,12 +34,24 @@ KvPagesArgs args_of(const pi_kv_pages *p) {
 
 }  // namespace
 
+extern "C" size_t pi_kv_pages_workspace_bytes(const pi_kv_pages *pages) { return check_pages(pages) ? 0 : bytes_of(pages); }
+
 extern "C" int pi_kv_release(const pi_kv_pages *pages, const int32_t *drop_from, const int32_t *drop_to, int32_t *copies,
                              void *stream) {
     if (int rc = check_pages(pages)) return rc;
     if (!drop_from || !copies) return PI_ERR_NULL;
-    const KvReleaseArgs a{args_of(pages), drop_from, drop_to, copies};
-    hipLaunchKernelGGL(k_kv_release, dim3(1), dim3(kKvTableThreads), 0, static_cast<hipStream_t>(stream), a);
+    if (!pages->ws || pages->ws_bytes < bytes_of(pages)) return PI_ERR_WORKSPACE;
+    if (!aligned16(pages->ws)) return PI_ERR_ALIGN;
+    const bool more = long_lists(pages);
+    const KvReleaseArgs a{args_of(pages), drop_from, drop_to, copies, more ? static_cast<int32_t *>(pages->ws) : nullptr};
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipLaunchKernelGGL(k_kv_release, dim3(1), dim3(threads_for(pages->n_req)), 0, st, a);
+    if (more) {
+        hipLaunchKernelGGL(k_kv_release_pass<0>, dim3(kKvReleaseGroups), dim3(256), 0, st, a);
+        hipLaunchKernelGGL(k_kv_release_pass<1>, dim3(kKvReleaseGroups), dim3(256), 0, st, a);
+        hipLaunchKernelGGL(k_kv_release_pass<2>, dim3(kKvReleaseGroups), dim3(256), 0, st, a);
+        hipLaunchKernelGGL(k_kv_release_pass<3>, dim3(kKvReleaseGroups), dim3(256), 0, st, a);
+    }
     return hipGetLastError() == hipSuccess ? PI_OK : PI_ERR_HIP;
 }
 
@@ -40,7 +61,11 @@ extern "C" int pi_kv_fork(const pi_kv_pages *pages, const int32_t *src, const in
     if (n_fork < 0 || n_fork > PI_KV_MAX_REQ) return PI_ERR_SHAPE;
     if (n_fork > 0 && (!src || !dst || !copies)) return PI_ERR_NULL;
     const KvForkArgs a{args_of(pages), src, dst, n_fork, copies};
-    hipLaunchKernelGGL(k_kv_fork, dim3(1), dim3(kKvTableThreads), 0, static_cast<hipStream_t>(stream), a);
+    const bool in_place = pages->cached_next == pages->cached || pages->pool_next == pages->pool;
+    const int threads = threads_for(n_fork);
+    const int64_t rounds = ((int64_t)n_fork * pages->max_pages + threads * kKvEach - 1) / (threads * kKvEach);
+    const int groups = in_place ? 1 : (int)std::min<int64_t>(32, std::max<int64_t>(1, rounds));
+    hipLaunchKernelGGL(k_kv_fork, dim3(groups), dim3(threads), 0, static_cast<hipStream_t>(stream), a);
     return hipGetLastError() == hipSuccess ? PI_OK : PI_ERR_HIP;
 }
 
@@ -51,8 +76,10 @@ extern "C" int pi_kv_copy(const pi_kv_cache *cache, const int32_t *copies, int32
     if (!copies) return PI_ERR_NULL;
     const int64_t units = (int64_t)cache->n_kv * cache->page * cache->head_dim / 8;
     const KvCopyArgs a{copies, cache->n_pages, units, static_cast<uint4 *>(cache->k_pages), static_cast<uint4 *>(cache->v_pages)};
-    const int64_t parts = (units + 1023) / 1024, share = std::max<int64_t>(1, 2048 / (2 * (int64_t)n));
-    hipLaunchKernelGGL(k_kv_copy, dim3((uint32_t)(2 * (int64_t)n), (uint32_t)std::min(parts, share)), dim3(256), 0,
+    // 16 KB a round: as many workgroups for a page as make 4096 of them all, the rounds shared out evenly
+    const int64_t rounds = (units + 1023) / 1024, most = std::max<int64_t>(1, 4096 / (2 * (int64_t)n));
+    const int64_t each = (rounds + most - 1) / most, parts = (rounds + each - 1) / each;
+    hipLaunchKernelGGL(k_kv_copy, dim3((uint32_t)(2 * (int64_t)n), (uint32_t)parts), dim3(256), 0,
                        static_cast<hipStream_t>(stream), a);
     return hipGetLastError() == hipSuccess ? PI_OK : PI_ERR_HIP;
 }

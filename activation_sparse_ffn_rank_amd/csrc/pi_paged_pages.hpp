@@ -17,6 +17,7 @@ struct KvReleaseArgs {
     KvPagesArgs p;
     const int *from, *to;
     int *copies;
+    int *ws;               // KvReleaseWs, or null: one workgroup does it all
 };
 struct KvForkArgs {
     KvPagesArgs p;
@@ -25,7 +26,16 @@ struct KvForkArgs {
     int *copies;
 };
 
-__device__ __forceinline__ int kv_load(const int *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+// Shares are changed and read by atomics of one workgroup, which its XCD's L2 serves, or of many (MANY), which are coherent over
+// the whole device.
+template <bool MANY>
+struct KvShares {
+    static constexpr int kScope = MANY ? __HIP_MEMORY_SCOPE_AGENT : __HIP_MEMORY_SCOPE_WORKGROUP;
+    static __device__ __forceinline__ int load(const int *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, kScope); }
+    static __device__ __forceinline__ void store(int *p, int v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, kScope); }
+    static __device__ __forceinline__ int less(int *p) { return __hip_atomic_fetch_add(p, -1, __ATOMIC_RELAXED, kScope); }
+    static __device__ __forceinline__ void lower(int *p, int v) { __hip_atomic_fetch_min(p, v, __ATOMIC_RELAXED, kScope); }
+};
 
 // The request (or fork) of entry e: the last r with first[r] <= e.
 __device__ __forceinline__ int kv_owner_of(const uint32_t *first, int n, uint32_t e) {
@@ -38,50 +48,195 @@ __device__ __forceinline__ int kv_owner_of(const uint32_t *first, int n, uint32_
     return lo;
 }
 
-constexpr int kKvMiddle = INT32_MIN;       // flag: the entries become -1
+constexpr int kKvMiddle = INT32_MIN;       // flag of a first column: the entries become -1
+constexpr int kKvEach = 4;                 // entries per thread and round
+constexpr int kKvReleaseGroups = 256;      // workgroups of a long list
+// Lists longer than this many entries per thread of the first workgroup go on to the launches behind it.
+constexpr int kKvShortList = 8;
 
-// One workgroup: ranges of entries per request by scans, then the entries, four per thread and round, three times over:
-//  1. one owner less for each (whole numbers: any order gives the same),
-//  2. of the pages that have run out of owners the first entry that names it, by a minimum over INT32_MIN + entry,
-//  3. those entries' pages behind the free ones, by a scan.
-// Nothing is kept in scratch memory: a page's count of further owners below zero says that it is free, and serves as the place of
-// the minimum.  At most 4096 * 2^17 = 2^29 entries.
+// What the first launch leaves for the ones behind it: ints at these places.
+struct KvReleaseWs {
+    static constexpr int kTotal = 0, kHead = 1, kCount = 2, kTaken = 3, kDenied = 4, kGiven = 5, kWins = 8;
+    static constexpr int kFirst = kWins + kKvReleaseGroups;                // [n_req + 1] first entry of each request
+    static constexpr int kCol = kFirst + PI_KV_MAX_REQ + 1;                // [n_req] its first column, | kKvMiddle
+    static constexpr int kFresh = kCol + PI_KV_MAX_REQ;                    // [n_req] page for its first column, -1: none
+    static constexpr int kInts = kFresh + PI_KV_MAX_REQ;
+};
+
+// Entries e0 .. e0 + kKvEach - 1: their places in the table, pages (-1: none, or out of range), and whether they become -1.
+struct KvEntries {
+    int *at[kKvEach], p[kKvEach];
+    bool middle[kKvEach];
+};
+__device__ __forceinline__ KvEntries kv_entries(const KvPagesArgs &a, const uint32_t *first, const int *col, uint32_t total, uint32_t e0) {
+    KvEntries x;
+#pragma unroll
+    for (int i = 0; i < kKvEach; ++i) x.p[i] = -1, x.middle[i] = false, x.at[i] = a.table;
+    if (e0 >= total) return x;
+    int r = kv_owner_of(first, a.n_req, e0);
+#pragma unroll
+    for (int i = 0; i < kKvEach; ++i) {
+        const uint32_t e = e0 + i;
+        if (e < total) {
+            while (r + 1 < a.n_req && first[r + 1] <= e) ++r;
+            x.at[i] = a.table + (int64_t)r * a.table_stride + (col[r] & INT32_MAX) + (e - first[r]);
+            x.middle[i] = col[r] < 0;
+            x.p[i] = *x.at[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kKvEach; ++i)
+        if ((uint32_t)x.p[i] >= (uint32_t)a.n_pages) x.p[i] = -1;
+    return x;
+}
+// each(i, e, place in the table, page, whether it becomes -1) for those with a page.
+template <class F>
+__device__ __forceinline__ void kv_walk(const KvPagesArgs &a, const uint32_t *first, const int *col, uint32_t total, uint32_t e0,
+                                        F &&each) {
+    const KvEntries x = kv_entries(a, first, col, total, e0);
+#pragma unroll
+    for (int i = 0; i < kKvEach; ++i)
+        if (x.p[i] >= 0) each(i, e0 + i, x.at[i], x.p[i], x.middle[i]);
+}
+
+// The three passes over the entries, for a range [from, to) of them in rounds of a workgroup:
+//  1. one owner less for each (whole numbers: any order gives the same); returns this thread's number of valid ones,
+template <bool MANY>
+__device__ __forceinline__ uint32_t kv_give(const KvPagesArgs &a, const uint32_t *first, const int *col, uint32_t from, uint32_t to) {
+    uint32_t given = 0;
+    for (uint32_t e = from + threadIdx.x * kKvEach; e < to; e += blockDim.x * kKvEach)
+        kv_walk(a, first, col, to, e, [&](int, uint32_t, int *, int p, bool) {
+            KvShares<MANY>::less(a.shares + p);
+            ++given;
+        });
+    return given;
+}
+//  2. of the pages that have run out of owners the first entry that names it, as the minimum over INT32_MIN + entry,
+template <bool MANY>
+__device__ __forceinline__ void kv_lead(const KvPagesArgs &a, const uint32_t *first, const int *col, uint32_t from, uint32_t to) {
+    for (uint32_t e = from + threadIdx.x * kKvEach; e < to; e += blockDim.x * kKvEach)
+        kv_walk(a, first, col, to, e, [&](int, uint32_t e, int *, int p, bool) {
+            if (KvShares<MANY>::load(a.shares + p) < 0) KvShares<MANY>::lower(a.shares + p, INT32_MIN + (int)e);
+        });
+}
+//  3. the pages of those entries behind the free ones, from place `at` of the ring on; returns how many.
+template <bool MANY>
+__device__ __forceinline__ uint32_t kv_push(const KvPagesArgs &a, const uint32_t *first, const int *col, uint32_t from, uint32_t to,
+                                            int64_t at, uint32_t *part) {
+    uint32_t back = 0;
+    for (uint32_t base = from; base < to; base += blockDim.x * kKvEach) {
+        int won[kKvEach];
+        uint32_t wins = 0;
+#pragma unroll
+        for (int i = 0; i < kKvEach; ++i) won[i] = -1;
+        kv_walk(a, first, col, to, base + threadIdx.x * kKvEach, [&](int i, uint32_t e, int *place, int p, bool middle) {
+            if (KvShares<MANY>::load(a.shares + p) == INT32_MIN + (int)e) won[i] = p, ++wins;
+            if (middle) *place = -1;
+        });
+        uint32_t all;
+        uint32_t rank = kv_block_scan(wins, part, &all) + back;
+#pragma unroll
+        for (int i = 0; i < kKvEach; ++i) {
+            if (won[i] < 0) continue;
+            a.ring[(at + rank++) % a.n_pages] = won[i];
+            KvShares<MANY>::store(a.shares + won[i], 0);
+        }
+        back += all;
+    }
+    return back;
+}
+
+// The same passes by one workgroup over a list of one round, with the entries read once.  Where no page that is given up has
+// further owners and none is named twice -- every count was 0 -- all of them go back, and the second pass and its reads are left out;
+// likewise where those with further owners keep some.
+__device__ __forceinline__ uint32_t kv_one_round(const KvPagesArgs &a, const uint32_t *first, const int *col, uint32_t total,
+                                                 int64_t at, uint32_t *part, uint32_t *given) {
+    const uint32_t e0 = threadIdx.x * kKvEach;
+    const KvEntries x = kv_entries(a, first, col, total, e0);
+    int before[kKvEach];
+    uint32_t mine = 0, wins = 0;
+    bool plain = true, odd = false;
+#pragma unroll
+    for (int i = 0; i < kKvEach; ++i) before[i] = x.p[i] >= 0 ? KvShares<false>::less(a.shares + x.p[i]) : 0;
+#pragma unroll
+    for (int i = 0; i < kKvEach; ++i) mine += x.p[i] >= 0, plain = plain && before[i] == 0;
+    if (mine) atomicAdd(given, mine);
+    bool won[kKvEach];
+#pragma unroll
+    for (int i = 0; i < kKvEach; ++i) won[i] = x.p[i] >= 0 && before[i] == 0;
+    if (!__syncthreads_and(plain)) {
+        int left[kKvEach];
+#pragma unroll
+        for (int i = 0; i < kKvEach; ++i) left[i] = x.p[i] >= 0 ? KvShares<false>::load(a.shares + x.p[i]) : 0;
+#pragma unroll
+        for (int i = 0; i < kKvEach; ++i) odd = odd || (left[i] < 0 && (left[i] != -1 || before[i] != 0));
+        if (__syncthreads_or(odd)) {
+#pragma unroll
+            for (int i = 0; i < kKvEach; ++i)
+                if (left[i] < 0) KvShares<false>::lower(a.shares + x.p[i], INT32_MIN + (int)(e0 + i));
+            kv_lds_wait();
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kKvEach; ++i)
+                won[i] = left[i] < 0 && KvShares<false>::load(a.shares + x.p[i]) == INT32_MIN + (int)(e0 + i);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kKvEach; ++i) wins += won[i];
+    uint32_t all;
+    uint32_t rank = kv_block_scan(wins, part, &all);
+#pragma unroll
+    for (int i = 0; i < kKvEach; ++i) {
+        if (x.middle[i] && x.p[i] >= 0) *x.at[i] = -1;
+        if (!won[i]) continue;
+        a.ring[(at + rank++) % a.n_pages] = x.p[i];
+        KvShares<false>::store(a.shares + x.p[i], 0);
+    }
+    return all;
+}
+
+// The first launch, one workgroup: ranges of entries per request by scans; then, if the list is short, all of it (64 requests,
+// 13 entries: a chain of dependent loads, and three atomics in turn).
+// Nothing but these ranges is kept in scratch memory: a page's count of further owners below zero says that it is free, and serves
+// as the place of the minimum.  At most 4096 * 2^17 = 2^29 entries.
 static __global__ __launch_bounds__(kKvTableThreads) void k_kv_release(KvReleaseArgs x) {
     const KvPagesArgs &a = x.p;
     __shared__ uint32_t s_first[PI_KV_MAX_REQ + 1];
     __shared__ int s_col[PI_KV_MAX_REQ];              // first column, | kKvMiddle
     __shared__ uint32_t s_part[kKvTableThreads / 64];
-    __shared__ uint32_t s_given;
-    const int tid = threadIdx.x, n = a.n_req, per = (n + kKvTableThreads - 1) / kKvTableThreads, page = 1 << a.page_log;
+    __shared__ uint32_t s_given, s_denied;
+    const int tid = threadIdx.x, n = a.n_req, per = (n + (int)blockDim.x - 1) / (int)blockDim.x, page = 1 << a.page_log;
     const int64_t room = (int64_t)a.max_pages << a.page_log;
-    int head = a.pool[0] % a.n_pages;
-    if (head < 0) head += a.n_pages;
-    const int count = min(max(a.pool[1], 0), a.n_pages);
-    if (tid == 0) s_given = 0;
+    const int pool0 = a.pool[0], pool1 = a.pool[1];
+    if (tid == 0) s_given = s_denied = 0;
 
-    int c[kKvReqPerThread], f[kKvReqPerThread], old[kKvReqPerThread];
+    int c[kKvReqPerThread], f[kKvReqPerThread], t[kKvReqPerThread], old[kKvReqPerThread];
     bool bad[kKvReqPerThread], tail[kKvReqPerThread], split[kKvReqPerThread];
-    int end[kKvReqPerThread];
-    uint32_t asks = 0;
 #pragma unroll
     for (int k = 0; k < kKvReqPerThread; ++k) {
         const int r = tid * per + k;
         const bool in = k < per && r < n;
         c[k] = in ? a.cached[r] : 0;
-        f[k] = in ? max(x.from[r], 0) : 0;
-        const int t = in && x.to ? x.to[r] : INT32_MAX;
+        f[k] = in ? x.from[r] : 0;
+        t[k] = in && x.to ? x.to[r] : INT32_MAX;
+    }
+#pragma unroll
+    for (int k = 0; k < kKvReqPerThread; ++k) {
+        const int r = tid * per + k;
+        f[k] = max(f[k], 0);
         bad[k] = c[k] < 0 || c[k] > room;
-        tail[k] = in && !bad[k] && t >= c[k] && f[k] < c[k];
-        end[k] = !in || bad[k] || f[k] >= c[k] ? 0 : tail[k] ? (c[k] + page - 1) >> a.page_log : max(t, 0) >> a.page_log;
-        old[k] = -1;
-        split[k] = false;
-        if (tail[k] && (f[k] & (page - 1))) {
-            old[k] = a.table[(int64_t)r * a.table_stride + (f[k] >> a.page_log)];
-            split[k] = (uint32_t)old[k] < (uint32_t)a.n_pages && a.shares[old[k]] > 0;
-        }
+        tail[k] = k < per && r < n && !bad[k] && t[k] >= c[k] && f[k] < c[k];
+        old[k] = tail[k] && (f[k] & (page - 1)) ? a.table[(int64_t)r * a.table_stride + (f[k] >> a.page_log)] : -1;
+    }
+    int head = pool0 % a.n_pages;
+    if (head < 0) head += a.n_pages;
+    const int count = min(max(pool1, 0), a.n_pages);
+    uint32_t asks = 0, total_asks, total;
+#pragma unroll
+    for (int k = 0; k < kKvReqPerThread; ++k) {
+        split[k] = (uint32_t)old[k] < (uint32_t)a.n_pages && a.shares[old[k]] > 0;
         asks += split[k];
     }
-    uint32_t total_asks, total;
     uint32_t rank = kv_block_scan(asks, s_part, &total_asks);
     uint32_t entries = 0, denied = 0, mine[kKvReqPerThread];
     int fresh[kKvReqPerThread];
@@ -99,111 +254,143 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_release(KvRelease
         }
         denied += refused;
         const int first = split[k] ? f[k] >> a.page_log : (int)(((int64_t)f[k] + page - 1) >> a.page_log);
-        if (!refused) mine[k] = (uint32_t)max(end[k] - first, 0);
+        const int end = f[k] >= c[k] ? 0 : tail[k] ? (c[k] + page - 1) >> a.page_log : max(t[k], 0) >> a.page_log;
+        if (!refused) mine[k] = (uint32_t)max(end - first, 0);
         split[k] = split[k] && !refused;
         tail[k] = tail[k] && !refused;
         s_col[r] = first | (tail[k] ? 0 : kKvMiddle);
         entries += mine[k];
-        x.copies[2 * r] = split[k] ? old[k] : -1;
-        x.copies[2 * r + 1] = split[k] ? fresh[k] : -1;
-        a.cached_next[r] = tail[k] ? f[k] : c[k];
     }
-    uint32_t at = kv_block_scan(entries, s_part, &total);
+    if (denied) atomicAdd(&s_denied, denied);
+    uint32_t at = kv_block_scan(entries, s_part, &total);       // (its barriers order s_col and the reads of the ring, too)
+    const bool go_on = x.ws && total > blockDim.x * kKvShortList;
 #pragma unroll
     for (int k = 0; k < kKvReqPerThread; ++k) {
         const int r = tid * per + k;
-        if (k < per && r < n) s_first[r] = at;
+        if (k >= per || r >= n) continue;
+        x.copies[2 * r] = split[k] ? old[k] : -1;
+        x.copies[2 * r + 1] = split[k] ? fresh[k] : -1;
+        a.cached_next[r] = tail[k] ? f[k] : c[k];
+        s_first[r] = at;
+        if (go_on) {
+            x.ws[KvReleaseWs::kFirst + r] = (int)at;
+            x.ws[KvReleaseWs::kCol + r] = s_col[r];
+            x.ws[KvReleaseWs::kFresh + r] = split[k] ? fresh[k] : INT32_MIN;
+        }
         at += mine[k];
     }
-    uint32_t total_denied;
-    kv_block_scan(denied, s_part, &total_denied);       // (its barriers order s_first and the reads of the ring, too)
-
-    // entry e .. e+3 of this thread: f(place in the table, page, whether it becomes -1), pages out of range left out
-    constexpr int kEach = 4;
-    auto walk = [&](uint32_t e0, auto &&each) {
-        if (e0 >= total) return;
-        int r = kv_owner_of(s_first, n, e0);
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const uint32_t e = e0 + i;
-            if (e >= total) return;
-            while (r + 1 < n && s_first[r + 1] <= e) ++r;
-            int *const at = a.table + (int64_t)r * a.table_stride + (s_col[r] & INT32_MAX) + (e - s_first[r]);
-            const int p = *at;
-            if ((uint32_t)p < (uint32_t)a.n_pages) each(i, e, at, p, s_col[r] < 0);
-        }
-    };
-    uint32_t given = 0;
-    for (uint32_t e = tid * kEach; e < total; e += kKvTableThreads * kEach)
-        walk(e, [&](int, uint32_t, int *, int p, bool) {
-            atomicSub(a.shares + p, 1);
-            ++given;
-        });
-    if (given) atomicAdd(&s_given, given);
-    __threadfence();
     __syncthreads();
-    for (uint32_t e = tid * kEach; e < total; e += kKvTableThreads * kEach)
-        walk(e, [&](int, uint32_t e, int *, int p, bool) {
-            if (kv_load(a.shares + p) < 0) atomicMin(a.shares + p, INT32_MIN + (int)e);
-        });
-    __threadfence();
-    __syncthreads();
-    uint32_t back = 0;
-    for (uint32_t base = 0; base < total; base += kKvTableThreads * kEach) {
-        int won[kEach];
-        uint32_t wins = 0;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) won[i] = -1;
-        walk(base + tid * kEach, [&](int i, uint32_t e, int *at, int p, bool middle) {
-            if (kv_load(a.shares + p) == INT32_MIN + (int)e) won[i] = p, ++wins;
-            if (middle) *at = -1;
-        });
-        uint32_t all;
-        uint32_t to = kv_block_scan(wins, s_part, &all) + back;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            if (won[i] < 0) continue;
-            a.ring[((int64_t)head + count + to++) % a.n_pages] = won[i];
-            __hip_atomic_store(a.shares + won[i], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-        back += all;
+    const uint32_t taken = min(total_asks, (uint32_t)count);
+    if (x.ws && tid == 0) {
+        x.ws[KvReleaseWs::kTotal] = go_on ? (int)total : 0;
+        x.ws[KvReleaseWs::kHead] = head;
+        x.ws[KvReleaseWs::kCount] = count;
+        x.ws[KvReleaseWs::kTaken] = (int)taken;
+        x.ws[KvReleaseWs::kDenied] = (int)s_denied;
+        x.ws[KvReleaseWs::kGiven] = 0;
     }
-    __syncthreads();
+    if (go_on) return;
+    uint32_t back = 0;
+    if (total && total <= blockDim.x * kKvEach) {
+        back = kv_one_round(a, s_first, s_col, total, (int64_t)head + count, s_part, &s_given);
+        __syncthreads();
+    } else if (total) {
+        const uint32_t given = kv_give<false>(a, s_first, s_col, 0, total);
+        if (given) atomicAdd(&s_given, given);
+        kv_lds_wait();
+        __syncthreads();
+        kv_lead<false>(a, s_first, s_col, 0, total);
+        kv_lds_wait();
+        __syncthreads();
+        back = kv_push<false>(a, s_first, s_col, 0, total, (int64_t)head + count, s_part);
+        __syncthreads();
+    }
 #pragma unroll
     for (int k = 0; k < kKvReqPerThread; ++k)
         if (split[k]) a.table[(int64_t)(tid * per + k) * a.table_stride + (f[k] >> a.page_log)] = fresh[k];
     if (tid == 0) {
-        const uint32_t taken = min(total_asks, (uint32_t)count);
         a.pool_next[0] = (int)(((int64_t)head + taken) % a.n_pages);
         a.pool_next[1] = (int)min((int64_t)count - taken + back, (int64_t)a.n_pages);
         a.counts[0] = (int)s_given;
         a.counts[1] = (int)back;
         a.counts[2] = (int)taken;
-        a.counts[3] = (int)total_denied;
+        a.counts[3] = (int)s_denied;
     }
 }
 
-// One workgroup: which forks are made, by scans; then the shared entries, four per thread and round.
+// The launches behind it, for a long list: each workgroup takes its share of the entries, in order.  PASS 0: owners less; 1: first
+// entries; 2: how many of them; 3: their pages into the ring.
+template <int PASS>
+__global__ __launch_bounds__(256) void k_kv_release_pass(KvReleaseArgs x) {
+    const KvPagesArgs &a = x.p;
+    __shared__ uint32_t s_first[PI_KV_MAX_REQ];
+    __shared__ int s_col[PI_KV_MAX_REQ];
+    __shared__ uint32_t s_part[4];
+    const int tid = threadIdx.x, b = blockIdx.x;
+    const uint32_t total = (uint32_t)x.ws[KvReleaseWs::kTotal];
+    if (total == 0) return;
+    for (int r = tid; r < a.n_req; r += 256) {
+        s_first[r] = (uint32_t)x.ws[KvReleaseWs::kFirst + r];
+        s_col[r] = x.ws[KvReleaseWs::kCol + r];
+    }
+    const uint32_t share = ((total + kKvReleaseGroups - 1) / kKvReleaseGroups + kKvEach - 1) & ~(uint32_t)(kKvEach - 1);
+    const uint32_t from = min(b * share, total), to = min(from + share, total);
+    __syncthreads();
+    if constexpr (PASS == 0) {
+        const uint32_t given = kv_give<true>(a, s_first, s_col, from, to);
+        uint32_t all;
+        kv_block_scan(given, s_part, &all);
+        if (tid == 0 && all) atomicAdd(x.ws + KvReleaseWs::kGiven, (int)all);
+    } else if constexpr (PASS == 1) {
+        kv_lead<true>(a, s_first, s_col, from, to);
+    } else if constexpr (PASS == 2) {
+        uint32_t wins = 0, all;
+        for (uint32_t e = from + tid * kKvEach; e < to; e += 256 * kKvEach)
+            kv_walk(a, s_first, s_col, to, e, [&](int, uint32_t e, int *, int p, bool) { wins += a.shares[p] == INT32_MIN + (int)e; });
+        kv_block_scan(wins, s_part, &all);
+        if (tid == 0) x.ws[KvReleaseWs::kWins + b] = (int)all;
+    } else {
+        uint32_t back, before = (uint32_t)x.ws[KvReleaseWs::kWins + tid];      // 256 threads, as many workgroups
+        before = kv_block_scan(before, s_part, &back);
+        __syncthreads();
+        if (tid == b) s_part[0] = before;
+        __syncthreads();
+        before = s_part[0];
+        __syncthreads();
+        const int head = x.ws[KvReleaseWs::kHead], count = x.ws[KvReleaseWs::kCount];
+        kv_push<true>(a, s_first, s_col, from, to, (int64_t)head + count + before, s_part);
+        __syncthreads();
+        // pages in the place of those that were cut inside of: by the workgroup whose entries begin with them
+        for (int r = tid; r < a.n_req; r += 256) {
+            const int fresh = x.ws[KvReleaseWs::kFresh + r];
+            if (fresh != INT32_MIN && s_first[r] >= from && s_first[r] < to)
+                a.table[(int64_t)r * a.table_stride + (s_col[r] & INT32_MAX)] = fresh;
+        }
+        if (b == 0 && tid == 0) {
+            const int taken = x.ws[KvReleaseWs::kTaken];
+            a.pool_next[0] = (int)(((int64_t)head + taken) % a.n_pages);
+            a.pool_next[1] = (int)min((int64_t)count - taken + back, (int64_t)a.n_pages);
+            a.counts[0] = x.ws[KvReleaseWs::kGiven];
+            a.counts[1] = (int)back;
+            a.counts[2] = taken;
+            a.counts[3] = x.ws[KvReleaseWs::kDenied];
+        }
+    }
+}
+
+// Every workgroup finds out by scans which forks are made; they share out the shared entries, four per thread and round.  What is
+// read here is not written here, unless the call works in place: then one workgroup reads all of it first.
 static __global__ __launch_bounds__(kKvTableThreads) void k_kv_fork(KvForkArgs x) {
     const KvPagesArgs &a = x.p;
     __shared__ uint32_t s_first[PI_KV_MAX_REQ + 1];
     __shared__ uint32_t s_pair[PI_KV_MAX_REQ];        // source | destination << 16
     __shared__ int s_claim[PI_KV_MAX_REQ];            // first fork to name a destination
     __shared__ uint32_t s_part[kKvTableThreads / 64];
-    __shared__ uint32_t s_shared;
-    const int tid = threadIdx.x, n = x.n_fork, per = (n + kKvTableThreads - 1) / kKvTableThreads, page = 1 << a.page_log;
+    __shared__ uint32_t s_done, s_denied;
+    const int tid = threadIdx.x, threads = blockDim.x, n = x.n_fork, per = (n + threads - 1) / threads, page = 1 << a.page_log;
     const int64_t room = (int64_t)a.max_pages << a.page_log;
-    int head = a.pool[0] % a.n_pages;
-    if (head < 0) head += a.n_pages;
-    const int count = min(max(a.pool[1], 0), a.n_pages);
-    if (tid == 0) s_shared = 0;
-    int keep[kKvReqPerThread];                        // cached of all requests
-#pragma unroll
-    for (int r = tid, k = 0; k < kKvReqPerThread; r += kKvTableThreads, ++k) {
-        keep[k] = r < a.n_req ? a.cached[r] : 0;
-        if (r < a.n_req) s_claim[r] = INT32_MAX;
-    }
-    __syncthreads();
+    const int pool0 = a.pool[0], pool1 = a.pool[1];
+    if (tid == 0) s_done = s_denied = 0;
     int s[kKvReqPerThread], d[kKvReqPerThread];
 #pragma unroll
     for (int k = 0; k < kKvReqPerThread; ++k) {
@@ -211,24 +398,35 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_fork(KvForkArgs x
         const bool in = k < per && i < n;
         s[k] = in ? x.src[i] : -1;
         d[k] = in ? x.dst[i] : -1;
-        if ((uint32_t)d[k] < (uint32_t)a.n_req) atomicMin(&s_claim[d[k]], i);
     }
+    for (int r = tid; r < a.n_req; r += threads) s_claim[r] = INT32_MAX;
     __syncthreads();
-    int len[kKvReqPerThread], old[kKvReqPerThread], fresh[kKvReqPerThread];
+    int len[kKvReqPerThread], there[kKvReqPerThread], old[kKvReqPerThread], fresh[kKvReqPerThread];
     bool ok[kKvReqPerThread], part[kKvReqPerThread];
+#pragma unroll
+    for (int k = 0; k < kKvReqPerThread; ++k) {
+        if ((uint32_t)d[k] < (uint32_t)a.n_req) atomicMin(&s_claim[d[k]], tid * per + k);
+        ok[k] = (uint32_t)s[k] < (uint32_t)a.n_req && (uint32_t)d[k] < (uint32_t)a.n_req && s[k] != d[k];
+        len[k] = ok[k] ? a.cached[s[k]] : 0;
+        there[k] = ok[k] ? a.cached[d[k]] : 0;
+    }
+    int head = pool0 % a.n_pages;
+    if (head < 0) head += a.n_pages;
+    const int count = min(max(pool1, 0), a.n_pages);
+    __syncthreads();
     uint32_t asks = 0;
 #pragma unroll
     for (int k = 0; k < kKvReqPerThread; ++k) {
-        const int i = tid * per + k;
-        ok[k] = (uint32_t)s[k] < (uint32_t)a.n_req && (uint32_t)d[k] < (uint32_t)a.n_req && s[k] != d[k];
-        len[k] = ok[k] ? a.cached[s[k]] : 0;
-        ok[k] = ok[k] && len[k] >= 0 && len[k] <= room && a.cached[d[k]] == 0 && s_claim[d[k]] == i;
+        ok[k] = ok[k] && len[k] >= 0 && len[k] <= room && there[k] == 0 && s_claim[d[k]] == tid * per + k;
         part[k] = ok[k] && (len[k] & (page - 1));
         old[k] = part[k] ? a.table[(int64_t)s[k] * a.table_stride + (len[k] >> a.page_log)] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kKvReqPerThread; ++k) {
         if ((uint32_t)old[k] >= (uint32_t)a.n_pages) old[k] = -1;
         asks += old[k] >= 0;
     }
-    uint32_t total_asks, total, total_denied, total_done;
+    uint32_t total_asks, total;
     uint32_t rank = kv_block_scan(asks, s_part, &total_asks);
     uint32_t entries = 0, denied = 0, done = 0, mine[kKvReqPerThread];
 #pragma unroll
@@ -246,9 +444,9 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_fork(KvForkArgs x
         else ++denied;
         entries += mine[k];
         s_pair[i] = ok[k] ? (uint32_t)s[k] | (uint32_t)d[k] << 16 : 0u;
-        x.copies[2 * i] = old[k];
-        x.copies[2 * i + 1] = fresh[k];
     }
+    if (done) atomicAdd(&s_done, done);
+    if (denied) atomicAdd(&s_denied, denied);
     uint32_t at = kv_block_scan(entries, s_part, &total);
 #pragma unroll
     for (int k = 0; k < kKvReqPerThread; ++k) {
@@ -256,47 +454,51 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_fork(KvForkArgs x
         if (k < per && i < n) s_first[i] = at;
         at += mine[k];
     }
-    kv_block_scan(denied, s_part, &total_denied);
-    kv_block_scan(done, s_part, &total_done);         // (their barriers order the arrays above and the reads of cached, too)
-    if (a.cached_next != a.cached)
+    if (blockIdx.x == 0) {
+        if (a.cached_next != a.cached)
+            for (int r = tid; r < a.n_req; r += threads) a.cached_next[r] = a.cached[r];
+        __syncthreads();
 #pragma unroll
-        for (int r = tid, k = 0; k < kKvReqPerThread; r += kKvTableThreads, ++k)
-            if (r < a.n_req) a.cached_next[r] = keep[k];
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kKvReqPerThread; ++k) {
-        if (!ok[k] || k >= per || tid * per + k >= n) continue;
-        a.cached_next[d[k]] = len[k];
-        if (part[k]) a.table[(int64_t)d[k] * a.table_stride + (len[k] >> a.page_log)] = fresh[k];
-    }
-    constexpr int kEach = 4;
-    uint32_t shared = 0;
-    for (uint32_t e0 = tid * kEach; e0 < total; e0 += kKvTableThreads * kEach) {
-        int i = kv_owner_of(s_first, n, e0);
-#pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-            const uint32_t e = e0 + j;
-            if (e >= total) break;
-            while (i + 1 < n && s_first[i + 1] <= e) ++i;
-            const uint32_t pair = s_pair[i], col = e - s_first[i];
-            const int p = a.table[(int64_t)(pair & 0xffff) * a.table_stride + col];
-            a.table[(int64_t)(pair >> 16) * a.table_stride + col] = p;
-            if ((uint32_t)p < (uint32_t)a.n_pages) {
-                atomicAdd(a.shares + p, 1);
-                ++shared;
-            }
+        for (int k = 0; k < kKvReqPerThread; ++k) {
+            const int i = tid * per + k;
+            if (k >= per || i >= n) continue;
+            x.copies[2 * i] = old[k];
+            x.copies[2 * i + 1] = fresh[k];
+            if (!ok[k]) continue;
+            a.cached_next[d[k]] = len[k];
+            if (part[k]) a.table[(int64_t)d[k] * a.table_stride + (len[k] >> a.page_log)] = fresh[k];
+        }
+        if (tid == 0) {
+            const uint32_t taken = min(total_asks, (uint32_t)count);
+            a.pool_next[0] = (int)(((int64_t)head + taken) % a.n_pages);
+            a.pool_next[1] = (int)((int64_t)count - taken);
+            a.counts[0] = (int)s_done;
+            a.counts[1] = (int)total;
+            a.counts[2] = (int)taken;
+            a.counts[3] = (int)s_denied;
         }
     }
-    if (shared) atomicAdd(&s_shared, shared);
     __syncthreads();
-    if (tid == 0) {
-        const uint32_t taken = min(total_asks, (uint32_t)count);
-        a.pool_next[0] = (int)(((int64_t)head + taken) % a.n_pages);
-        a.pool_next[1] = (int)((int64_t)count - taken);
-        a.counts[0] = (int)total_done;
-        a.counts[1] = (int)s_shared;
-        a.counts[2] = (int)taken;
-        a.counts[3] = (int)total_denied;
+    const uint32_t stride = gridDim.x * threads * kKvEach;
+    for (uint32_t e0 = (blockIdx.x * threads + tid) * kKvEach; e0 < total; e0 += stride) {
+        int i = kv_owner_of(s_first, n, e0);
+        int *to[kKvEach], p[kKvEach];
+#pragma unroll
+        for (int j = 0; j < kKvEach; ++j) {
+            const uint32_t e = e0 + j;
+            to[j] = nullptr;
+            if (e >= total) continue;
+            while (i + 1 < n && s_first[i + 1] <= e) ++i;
+            const uint32_t pair = s_pair[i], col = e - s_first[i];
+            p[j] = a.table[(int64_t)(pair & 0xffff) * a.table_stride + col];
+            to[j] = a.table + (int64_t)(pair >> 16) * a.table_stride + col;
+        }
+#pragma unroll
+        for (int j = 0; j < kKvEach; ++j) {
+            if (!to[j]) continue;
+            *to[j] = p[j];
+            if ((uint32_t)p[j] < (uint32_t)a.n_pages) atomicAdd(a.shares + p[j], 1);
+        }
     }
 }
 

@@ -220,7 +220,12 @@ typedef struct pi_kv_pages {
     int32_t *cached_next;            /* [n_req] */
     int32_t *pool_next;              /* [2] */
     int32_t *counts;                 /* [4] */
+    void *ws;                        /* pi_kv_pages_workspace_bytes, 16-byte aligned, no zero fill (pi_kv_release) */
+    size_t ws_bytes;
 } pi_kv_pages;
+
+/* Bytes of workspace for this state (0: invalid).  It must not be shared by calls in flight at the same time. */
+size_t pi_kv_pages_workspace_bytes(const pi_kv_pages *pages);
 
 /* Gives up the positions drop_from[r] .. drop_to[r]-1 of every request (drop_to NULL: to the end; a negative drop_from is 0;
  * none where drop_from >= cached): the pages all of whose held positions lie among them.
@@ -237,8 +242,8 @@ int pi_kv_release(const pi_kv_pages *pages, const int32_t *drop_from, const int3
 /* Makes request dst[i], which must hold nothing (cached 0), a copy of request src[i], i < n_fork: its full pages are shared, of
  * a partly filled last one a copy is due: copies[i] = {old, new}, else {-1, -1}.  Refused, with nothing changed: src or dst out
  * of range or equal, dst holding something or named by an earlier fork, cached[src] out of range, free pages that do not suffice
- * (forks are served in order).  cached_next = cached but for the forks.  counts = {forks made, entries shared, pages taken,
- * forks refused}.  0 <= n_fork <= PI_KV_MAX_REQ. */
+ * (forks are served in order).  cached_next = cached but for the forks.  counts = {forks made, entries shared
+ * (missing pages among them), pages taken, forks refused}.  0 <= n_fork <= PI_KV_MAX_REQ. */
 int pi_kv_fork(const pi_kv_pages *pages, const int32_t *src, const int32_t *dst, int32_t n_fork, int32_t *copies, void *stream);
 
 /* Copies keys and values of page copies[i][0] to page copies[i][1], i < n.  Pairs with an entry out of range are skipped; no

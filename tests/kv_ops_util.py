@@ -212,7 +212,7 @@ def fork_reference(st, src, dst):
             p = table[d][col] = st["table"][s][col]
             if 0 <= p < n_pages:
                 shares[p] += 1
-                more += 1
+        more += full
         if part:
             table[d][full] = copy[1]
     taken = min(asked, count)

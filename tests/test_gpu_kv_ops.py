@@ -562,7 +562,7 @@ def check_state(d, want):
     assert bool((d["wide"][:, d["wide"].shape[1] - d["slack"]:] == -7).all())
 
 
-PAGE_CASES = [(1, 16, 1), (1, 256, 5), (9, 16, 6), (64, 32, 40), (200, 16, 9), (1025, 64, 4), (1500, 16, 30), (4096, 16, 5)]
+PAGE_CASES = [(1, 16, 1), (1, 256, 5), (9, 16, 6), (64, 32, 40), (200, 16, 9), (1025, 64, 4), (1500, 16, 30), (2000, 32, 64), (4096, 16, 5), (4096, 16, 9)]
 
 
 @pytest.mark.parametrize("in_place", (False, True))

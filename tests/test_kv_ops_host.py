@@ -41,7 +41,7 @@ def drafts(**kw):
 
 
 def pages(**kw):
-    base = dict(n_req=4, page=16, n_pages=100, max_pages=50, table_stride=50)
+    base = dict(n_req=4, page=16, n_pages=100, max_pages=50, table_stride=50, ws=A, ws_bytes=1 << 20)
     base.update({f: A for f in ("cached", "free_ring", "pool", "block_table", "shares", "cached_next", "pool_next", "counts")})
     base.update(kw)
     return _kv.pi_kv_pages(**base)
@@ -129,6 +129,10 @@ def test_pages_reject(L):
     for kw in (dict(n_req=0), dict(n_req=4097), dict(page=24), dict(n_pages=0), dict(max_pages=0), dict(max_pages=(1 << 17) + 1),
                dict(table_stride=49), dict(n_pages=1 << 27)):
         assert release(pages(**kw)) == SHAPE and fork(pages(**kw)) == SHAPE, kw
+    size = L.pi_kv_pages_workspace_bytes
+    assert size(None) == 0 and size(pages(page=24)) == 0 and size(pages()) == 16 and size(pages(n_req=1000, max_pages=1000, table_stride=1000)) > 4000
+    assert release(pages(ws=0)) == WS and release(pages(ws_bytes=15)) == WS and release(pages(ws=A8)) == ALIGN
+    assert release(pages(n_req=1000, max_pages=1000, table_stride=1000, ws_bytes=4000)) == WS
     assert fork(n=-1) == SHAPE and fork(n=4097) == SHAPE
     copy = lambda c=None, p=A, n=3: L.pi_kv_copy(c or cache(), p, n, None)
     assert copy(n=0) == _abi.PI_OK and copy(n=0, p=0) == _abi.PI_OK and L.pi_kv_copy(None, A, 3, None) == NULL and copy(p=0) == NULL
@@ -192,7 +196,8 @@ def test_tensors_are_checked():
     mk = lambda **kw: _kv.make_kv_pages(**{**dict(cached=i32(3), free_ring=i32(9), pool=i32(2), block_table=i32(3, 4), page=16, shares=i32(9),
                                                cached_next=i32(3), pool_next=i32(2), counts=i32(4)), **kw})
     st = mk(block_table=i32(3, 7)[:, :4])
-    assert (st.n_req, st.n_pages, st.max_pages, st.table_stride) == (3, 9, 4, 7)
+    assert (st.n_req, st.n_pages, st.max_pages, st.table_stride, st.ws_bytes) == (3, 9, 4, 7, 16)
+    assert mk(ws=torch.zeros(99, dtype=torch.uint8)).ws_bytes == 99 and code(lambda: mk(ws=i32(8)[::2])) == WS
     assert code(lambda: mk(shares=i32(8))) == SHAPE and code(lambda: mk(counts=i32(3))) == SHAPE and code(lambda: mk(pool=None)) == NULL
     assert code(lambda: mk(cached_next=i32(2))) == SHAPE and code(lambda: mk(shares=f32(9))) == DTYPE and code(lambda: mk(page=2 ** 31)) == SHAPE
     assert code(lambda: _kv.pi_kv_release(st, i32(2), None, i32(3, 2), 0)) == SHAPE
