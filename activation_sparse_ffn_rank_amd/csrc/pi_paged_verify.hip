@@ -19,7 +19,9 @@ int check_drafts(const pi_kv_drafts *d) {
 
 int pieces_of(const pi_kv_drafts *d) { return (d->vocab + kKvPiece - 1) / kKvPiece; }
 
-size_t bytes_of(const pi_kv_drafts *d) { return std::max<size_t>(16, (size_t)d->n_req * pieces_of(d) * sizeof(double)); }
+// Tickets first, as many for any call, so that the calls that share a workspace find theirs at zero.
+constexpr size_t kTicketBytes = PI_KV_MAX_REQ * sizeof(int32_t);
+size_t bytes_of(const pi_kv_drafts *d) { return kTicketBytes + (size_t)d->n_req * pieces_of(d) * sizeof(double); }
 
 }  // namespace
 
@@ -37,14 +39,13 @@ extern "C" int pi_kv_verify(const pi_kv_drafts *drafts, const int32_t *kv_len, i
     a.p_stride = drafts->target_stride, a.q_stride = drafts->draft_stride;
     a.q_start = drafts->q_start, a.tokens = drafts->tokens, a.kv_len = kv_len;
     a.p = drafts->target, a.q = drafts->draft, a.u_accept = drafts->u_accept, a.u_next = drafts->u_next;
-    a.accepted = accepted, a.next = next, a.keep = keep, a.sums = static_cast<double *>(ws);
+    a.accepted = accepted, a.next = next, a.keep = keep, a.tickets = static_cast<int32_t *>(ws);
+    a.sums = reinterpret_cast<double *>(static_cast<char *>(ws) + kTicketBytes);
     // pieces a wave takes one after another: one while the chip holds all waves
     a.per_wave = 1;
     while (a.per_wave < 16 && (int64_t)a.n_req * a.pieces > (int64_t)a.per_wave * 8192) a.per_wave *= 2;
     hipStream_t st = static_cast<hipStream_t>(stream);
     const int groups = (a.pieces + 4 * a.per_wave - 1) / (4 * a.per_wave);
-    hipLaunchKernelGGL(k_kv_verify_sum, dim3(groups, a.n_req), dim3(256), 0, st, a);
-    if (hipGetLastError() != hipSuccess) return PI_ERR_HIP;
-    hipLaunchKernelGGL(k_kv_verify_pick, dim3(a.n_req), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(k_kv_verify, dim3(groups, a.n_req), dim3(256), 0, st, a);
     return hipGetLastError() == hipSuccess ? PI_OK : PI_ERR_HIP;
 }

@@ -1,9 +1,8 @@
-// pi_paged_verify.hpp -- gfx950 kernels that decide which drafted tokens stay and draw the next one (k_kv_verify_sum,
-// k_kv_verify_pick).
+// pi_paged_verify.hpp -- gfx950 kernel that decides which drafted tokens stay and draws the next one (k_kv_verify).
 //
 // The acceptance tests need two numbers each; the sample needs one row of the target's probabilities and, after a
-// rejection, one of the draft's.  That row is cut into pieces of kKvPiece entries whose weights are summed first; the piece in
-// which the running sum passes its mark is then read once more, from L2.
+// rejection, one of the draft's.  That row is cut into pieces of kKvPiece entries whose weights the request's workgroups sum;
+// the last of them to finish adds the sums up in order and reads the piece in which the running sum passes its mark once more.
 #pragma once
 
 #include "pi_paged.hpp"
@@ -19,8 +18,15 @@ struct KvVerifyArgs {
     const int *q_start, *tokens, *kv_len;
     const float *p, *q, *u_accept, *u_next;
     int *accepted, *next, *keep;
+    int *tickets;                  // [n_req] workgroups that have finished; zero between calls
     double *sums;                  // [n_req][pieces]
 };
+
+// Sums pass between workgroups of any XCD: written and read past the L2 of either.
+__device__ __forceinline__ void kv_put(double *p, double x) { __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ double kv_get(const double *p) {
+    return __hip_atomic_load(const_cast<double *>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 
 struct KvVerdict {
     int rows, accepted;            // of the request; rows = 0: none, or a range out of bounds
@@ -112,19 +118,6 @@ __device__ __forceinline__ double kv_piece_sum(const KvWeights &w, int i, int la
     return kv_wave_sum(sum);
 }
 
-static __global__ __launch_bounds__(256) void k_kv_verify_sum(KvVerifyArgs a) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = blockIdx.y;
-    const int i0 = (blockIdx.x * 4 + wave) * a.per_wave, i1 = min(i0 + a.per_wave, a.pieces);
-    if (i0 >= i1) return;
-    const KvVerdict v = kv_verdict(a, r, lane);
-    if (v.rows == 0) return;
-    const KvWeights w = kv_weights_of(a, v, v.rejected);
-    for (int i = i0; i < i1; ++i) {
-        const double sum = kv_piece_sum(w, i, lane);
-        if (lane == 0) a.sums[(int64_t)r * a.pieces + i] = sum;
-    }
-}
-
 // Sum over the threads before this one, in a fixed order; *total: of all.  sums: one per thread.
 __device__ __forceinline__ double kv_block_sums(double x, double *sums, double *part, double *total) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
@@ -147,66 +140,99 @@ __device__ __forceinline__ double kv_block_sums(double x, double *sums, double *
     return tid ? sums[tid - 1] : 0.0;
 }
 
-// One workgroup per request: the piece, and the entry in it.  An entry without weight is never taken, and where rounding
-// leaves none above the mark it is the last one with weight.
-static __global__ __launch_bounds__(256) void k_kv_verify_pick(KvVerifyArgs a) {
-    __shared__ double s_part[4], s_sums[256], s_piece[kKvMaxPieces], s_before;
-    __shared__ int s_first, s_last;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = blockIdx.x;
+// The lowest thread's `first` that is not INT32_MAX, else the highest thread's `last` that is not -1, else -1; both grow with the
+// thread.  (By votes: minima in LDS took 5 us here, a step per lane.)  found: two ints per wave.
+__device__ __forceinline__ int kv_first_or_last(int first, int last, int *found) {
+    const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const uint64_t some = __ballot(first != INT32_MAX), any = __ballot(last >= 0);
+    if ((threadIdx.x & 63) == 0) {
+        found[2 * wave] = INT32_MAX;
+        found[2 * wave + 1] = -1;
+    }
+    if (some) found[2 * wave] = bcast(first, __builtin_ctzll(some));
+    if (any) found[2 * wave + 1] = bcast(last, 63 - __builtin_clzll(any));
+    __syncthreads();
+    int low = INT32_MAX, high = -1;
+    for (int w = 0; w < waves; ++w) {
+        low = min(low, found[2 * w]);
+        high = max(high, found[2 * w + 1]);
+    }
+    return low != INT32_MAX ? low : high;
+}
+
+// Workgroup (group of pieces, request).  The last one of a request draws: an entry without weight is never taken, and where
+// rounding leaves none above the mark it is the last one with weight.
+static __global__ __launch_bounds__(256) void k_kv_verify(KvVerifyArgs a) {
+    __shared__ double s_part[4], s_sums[256], s_before;
+    __shared__ int s_found[2][8], s_end;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = blockIdx.y;
+    const float u_next = a.u_next[r];
     const KvVerdict v = kv_verdict(a, r, lane);
-    if (tid == 0) {
+    if (tid == 0 && blockIdx.x == 0) {
         a.accepted[r] = v.accepted;
         if (a.keep) a.keep[r] = a.kv_len[r] - max(v.rows - 1 - v.accepted, 0);
         if (v.rows == 0) a.next[r] = -1;
-        s_first = INT32_MAX, s_last = -1;
     }
     if (v.rows == 0) return;
     KvWeights w = kv_weights_of(a, v, v.rejected);
-    for (int i = tid; i < a.pieces; i += 256) s_piece[i] = a.sums[(int64_t)r * a.pieces + i];
-    const int per = (a.pieces + 255) / 256, i0 = tid * per, i1 = min(i0 + per, a.pieces);
-    double upto, total;
-    for (bool again = false;; again = true) {
+    double *const sums = a.sums + (int64_t)r * a.pieces;
+    {
+        const int from = (blockIdx.x * 4 + wave) * a.per_wave, to = min(from + a.per_wave, a.pieces);
+        for (int i = from; i < to; ++i) {
+            const double sum = kv_piece_sum(w, i, lane);
+            if (lane == 0) kv_put(sums + i, sum);
+        }
+    }
+    kv_lds_wait();                         // this wave's sums are out
+    __syncthreads();                       // ... and so are the others'
+    if (gridDim.x > 1) {
+        if (tid == 0) s_end = atomicAdd(a.tickets + r, 1) == (int)gridDim.x - 1;
         __syncthreads();
-        double mine = 0.0;
-        for (int i = i0; i < i1; ++i) mine += s_piece[i];
+        if (!s_end) return;
+        if (tid == 0) a.tickets[r] = 0;
+    }
+    const int per = (a.pieces + 255) / 256, i0 = tid * per, i1 = min(i0 + per, a.pieces);
+    double upto, total, one;               // one: of the thread's first piece, most often its only one
+    for (bool again = false;; again = true) {
+        one = i0 < i1 ? kv_get(sums + i0) : 0.0;
+        double mine = one;
+        for (int i = i0 + 1; i < i1; ++i) mine += kv_get(sums + i);
         upto = kv_block_sums(mine, s_sums, s_part, &total);
         if (total > 0.0 || again || !v.rejected) break;
         // nothing is left of the rest: the target's own weights
         w = kv_weights_of(a, v, false);
         for (int i = wave; i < a.pieces; i += 4) {
             const double sum = kv_piece_sum(w, i, lane);
-            if (lane == 0) s_piece[i] = sum;
+            if (lane == 0) kv_put(sums + i, sum);
         }
+        kv_lds_wait();
+        __syncthreads();
     }
     if (!(total > 0.0)) {
         if (tid == 0) a.next[r] = -1;
         return;
     }
-    const double mark = (double)a.u_next[r] * total;
+    const double mark = (double)u_next * total;
     // the first of this thread's pieces to pass the mark, and its last one, with the sums before them
     int first = INT32_MAX, last = -1;
     double to_first = 0.0, to_last = 0.0;
     for (int i = i0; i < i1; ++i) {
-        if (!(s_piece[i] > 0.0)) continue;
+        const double x = i == i0 ? one : kv_get(sums + i);
+        if (!(x > 0.0)) continue;
         last = i, to_last = upto;
-        if (first == INT32_MAX && upto + s_piece[i] > mark) first = i, to_first = upto;
-        upto += s_piece[i];
+        if (first == INT32_MAX && upto + x > mark) first = i, to_first = upto;
+        upto += x;
     }
-    if (first != INT32_MAX) atomicMin(&s_first, first);
-    if (last >= 0) atomicMax(&s_last, last);
-    __syncthreads();
-    const int piece = s_first != INT32_MAX ? s_first : s_last;
+    const int piece = kv_first_or_last(first, last, s_found[0]);
     if (piece == first) s_before = to_first;
     else if (piece == last) s_before = to_last;
-    __syncthreads();
-    if (tid == 0) s_first = INT32_MAX, s_last = -1;
     const int j0 = (piece << kKvPieceLog) + tid * 4;
     KvQuad x, y;
     w.load(j0, x, y);
     double each[4], sum = 0.0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum += each[e] = w.weight(x.v[e], y.v[e], j0 + e);
-    double at = kv_block_sums(sum, s_sums, s_part, &total) + s_before;
+    double at = kv_block_sums(sum, s_sums, s_part, &total) + s_before;      // (its barriers order s_before, too)
     first = INT32_MAX, last = -1;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -215,10 +241,8 @@ static __global__ __launch_bounds__(256) void k_kv_verify_pick(KvVerifyArgs a) {
         last = j0 + e;
         if (first == INT32_MAX && at > mark) first = j0 + e;
     }
-    if (first != INT32_MAX) atomicMin(&s_first, first);
-    if (last >= 0) atomicMax(&s_last, last);
-    __syncthreads();
-    if (tid == 0) a.next[r] = s_first != INT32_MAX ? s_first : s_last;
+    const int token = kv_first_or_last(first, last, s_found[1]);
+    if (tid == 0) a.next[r] = token;
 }
 
 }  // namespace pik

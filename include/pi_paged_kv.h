@@ -195,7 +195,8 @@ typedef struct pi_kv_drafts {
     const float *u_next;             /* [n_req], in [0, 1) */
 } pi_kv_drafts;
 
-/* The workspace is 16-byte aligned and needs no zero fill.  Results do not depend on timing. */
+/* The workspace is 16-byte aligned and zero-filled before the first call that uses it; each call leaves it ready for the next
+ * one, of any size (never clear or share it while a call is in flight).  Results do not depend on timing. */
 size_t pi_kv_verify_workspace_bytes(const pi_kv_drafts *drafts);
 int pi_kv_verify(const pi_kv_drafts *drafts, const int32_t *kv_len, int32_t *accepted, int32_t *next, int32_t *keep, void *ws,
                  size_t ws_bytes, void *stream);

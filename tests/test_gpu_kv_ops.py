@@ -398,11 +398,13 @@ def run_verify(starts, tokens, target, draft, u, un, kv_len=None, *, offset=0, s
     n = len(starts) - 1
     d = pi.make_kv_drafts(dev(starts), dev(tokens), put(target), put(draft), dev(u, torch.float32), dev(un, torch.float32))
     ws = torch.full((pi.pi_kv_verify_workspace_bytes(d),), 255, dtype=torch.uint8, device="cuda")
+    ws[: 4 * 4096] = 0                       # (what else it holds does not matter)
     new = lambda: torch.full((n,), -77, dtype=torch.int32, device="cuda")
     accepted, nxt = new(), new()
     keep = None if kv_len is None else dev(kv_len)                          # in place
     pi.pi_kv_verify(d, accepted, nxt, ws, kv_len=keep, keep=keep, stream=stream)
     torch.cuda.synchronize()
+    assert not bool(ws[: 4 * 4096].any()), "not ready for the next call"
     return accepted.tolist(), nxt.tolist(), [None] * n if keep is None else keep.tolist()
 
 
@@ -521,6 +523,22 @@ def test_verify_leaves_the_targets_distribution():
     total = n * trials
     sigma = torch.sqrt(total * p * (1 - p))
     assert bool(((seen - total * p).abs() <= 5 * sigma).all())
+
+
+def test_verify_calls_of_any_size_share_a_workspace():
+    announce("verify shared workspace")
+    cases = [verify_case(s, counts, vocab) for s, (counts, vocab) in enumerate((([3, 2, 5], 40000), ([2] * 300, 700), ([4], 9000), ([1, 3] * 20, 3000)))]
+    sets = []
+    for starts, tokens, target, draft, u, un in cases:
+        sets.append(pi.make_kv_drafts(dev(starts), dev(tokens), target.cuda(), draft.cuda(), dev(u, torch.float32), dev(un, torch.float32)))
+    ws = torch.zeros(max(pi.pi_kv_verify_workspace_bytes(d) for d in sets), dtype=torch.uint8, device="cuda")
+    outs = [torch.full((2, d.n_req), -77, dtype=torch.int32, device="cuda") for _ in range(3) for d in sets]
+    for out, d in zip(outs, sets * 3):
+        pi.pi_kv_verify(d, out[0], out[1], ws)
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        want = U.verify_reference(*cases[i % len(cases)])
+        assert (out[0].tolist(), out[1].tolist()) == want[:2], i
 
 
 def test_verify_large():
@@ -671,7 +689,7 @@ class Drafting:
         self.rope = pi.make_kv_rope(pi.pi_rope_frequencies(hd).cuda(), norm=True)
         self.ws = torch.empty(pi.pi_kv_attn_sinks_workspace_bytes(self.cache, self.batch, self.rows, n_q, window, sinks), dtype=torch.uint8, device="cuda")
         self.drafts = pi.make_kv_drafts(self.q_start, self.tokens, self.target, self.draft, self.u, self.un)
-        self.vws = torch.empty(pi.pi_kv_verify_workspace_bytes(self.drafts), dtype=torch.uint8, device="cuda")
+        self.vws = torch.zeros(pi.pi_kv_verify_workspace_bytes(self.drafts), dtype=torch.uint8, device="cuda")
 
     def step(self):
         """One step of all requests, each with its last token and its drafts."""
