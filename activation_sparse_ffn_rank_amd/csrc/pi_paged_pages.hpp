@@ -150,7 +150,7 @@ __device__ __forceinline__ uint32_t kv_push(const KvPagesArgs &a, const uint32_t
 // further owners and none is named twice -- every count was 0 -- all of them go back, and the second pass and its reads are left out;
 // likewise where those with further owners keep some.
 __device__ __forceinline__ uint32_t kv_one_round(const KvPagesArgs &a, const uint32_t *first, const int *col, uint32_t total,
-                                                 int64_t at, uint32_t *part, uint32_t *given) {
+                                                 int64_t at, uint32_t *part, uint32_t &given) {
     const uint32_t e0 = threadIdx.x * kKvEach;
     const KvEntries x = kv_entries(a, first, col, total, e0);
     int before[kKvEach];
@@ -160,7 +160,6 @@ __device__ __forceinline__ uint32_t kv_one_round(const KvPagesArgs &a, const uin
     for (int i = 0; i < kKvEach; ++i) before[i] = x.p[i] >= 0 ? KvShares<false>::less(a.shares + x.p[i]) : 0;
 #pragma unroll
     for (int i = 0; i < kKvEach; ++i) mine += x.p[i] >= 0, plain = plain && before[i] == 0;
-    if (mine) atomicAdd(given, mine);
     bool won[kKvEach];
 #pragma unroll
     for (int i = 0; i < kKvEach; ++i) won[i] = x.p[i] >= 0 && before[i] == 0;
@@ -183,8 +182,9 @@ __device__ __forceinline__ uint32_t kv_one_round(const KvPagesArgs &a, const uin
     }
 #pragma unroll
     for (int i = 0; i < kKvEach; ++i) wins += won[i];
-    uint32_t all;
-    uint32_t rank = kv_block_scan(wins, part, &all);
+    uint32_t all;                              // both numbers in one scan: at most 4096 each
+    uint32_t rank = kv_block_scan(wins | mine << 16, part, &all) & 0xffff;
+    given = all >> 16, all &= 0xffff;
 #pragma unroll
     for (int i = 0; i < kKvEach; ++i) {
         if (x.middle[i] && x.p[i] >= 0) *x.at[i] = -1;
@@ -204,11 +204,11 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_release(KvRelease
     __shared__ uint32_t s_first[PI_KV_MAX_REQ + 1];
     __shared__ int s_col[PI_KV_MAX_REQ];              // first column, | kKvMiddle
     __shared__ uint32_t s_part[kKvTableThreads / 64];
-    __shared__ uint32_t s_given, s_denied;
+    __shared__ uint32_t s_denied;
     const int tid = threadIdx.x, n = a.n_req, per = (n + (int)blockDim.x - 1) / (int)blockDim.x, page = 1 << a.page_log;
     const int64_t room = (int64_t)a.max_pages << a.page_log;
     const int pool0 = a.pool[0], pool1 = a.pool[1];
-    if (tid == 0) s_given = s_denied = 0;
+    if (tid == 0) s_denied = 0;
 
     int c[kKvReqPerThread], f[kKvReqPerThread], t[kKvReqPerThread], old[kKvReqPerThread];
     bool bad[kKvReqPerThread], tail[kKvReqPerThread], split[kKvReqPerThread];
@@ -290,13 +290,13 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_release(KvRelease
         x.ws[KvReleaseWs::kGiven] = 0;
     }
     if (go_on) return;
-    uint32_t back = 0;
+    uint32_t back = 0, given = 0;
     if (total && total <= blockDim.x * kKvEach) {
-        back = kv_one_round(a, s_first, s_col, total, (int64_t)head + count, s_part, &s_given);
+        back = kv_one_round(a, s_first, s_col, total, (int64_t)head + count, s_part, given);
         __syncthreads();
     } else if (total) {
-        const uint32_t given = kv_give<false>(a, s_first, s_col, 0, total);
-        if (given) atomicAdd(&s_given, given);
+        const uint32_t mine = kv_give<false>(a, s_first, s_col, 0, total);
+        kv_block_scan(mine, s_part, &given);
         kv_lds_wait();
         __syncthreads();
         kv_lead<false>(a, s_first, s_col, 0, total);
@@ -311,7 +311,7 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_release(KvRelease
     if (tid == 0) {
         a.pool_next[0] = (int)(((int64_t)head + taken) % a.n_pages);
         a.pool_next[1] = (int)min((int64_t)count - taken + back, (int64_t)a.n_pages);
-        a.counts[0] = (int)s_given;
+        a.counts[0] = (int)given;
         a.counts[1] = (int)back;
         a.counts[2] = (int)taken;
         a.counts[3] = (int)s_denied;
@@ -386,11 +386,11 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_fork(KvForkArgs x
     __shared__ uint32_t s_pair[PI_KV_MAX_REQ];        // source | destination << 16
     __shared__ int s_claim[PI_KV_MAX_REQ];            // first fork to name a destination
     __shared__ uint32_t s_part[kKvTableThreads / 64];
-    __shared__ uint32_t s_done, s_denied;
+    __shared__ uint32_t s_done;
     const int tid = threadIdx.x, threads = blockDim.x, n = x.n_fork, per = (n + threads - 1) / threads, page = 1 << a.page_log;
     const int64_t room = (int64_t)a.max_pages << a.page_log;
     const int pool0 = a.pool[0], pool1 = a.pool[1];
-    if (tid == 0) s_done = s_denied = 0;
+    if (tid == 0) s_done = 0;
     int s[kKvReqPerThread], d[kKvReqPerThread];
 #pragma unroll
     for (int k = 0; k < kKvReqPerThread; ++k) {
@@ -428,7 +428,7 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_fork(KvForkArgs x
     }
     uint32_t total_asks, total;
     uint32_t rank = kv_block_scan(asks, s_part, &total_asks);
-    uint32_t entries = 0, denied = 0, done = 0, mine[kKvReqPerThread];
+    uint32_t entries = 0, mine[kKvReqPerThread];
 #pragma unroll
     for (int k = 0; k < kKvReqPerThread; ++k) {
         const int i = tid * per + k;
@@ -440,13 +440,14 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_fork(KvForkArgs x
             else fresh[k] = a.ring[((int64_t)head + rank) % a.n_pages];
             ++rank;
         }
-        if (ok[k]) mine[k] = (uint32_t)(len[k] >> a.page_log), ++done;
-        else ++denied;
+        if (ok[k]) mine[k] = (uint32_t)(len[k] >> a.page_log);
         entries += mine[k];
         s_pair[i] = ok[k] ? (uint32_t)s[k] | (uint32_t)d[k] << 16 : 0u;
     }
-    if (done) atomicAdd(&s_done, done);
-    if (denied) atomicAdd(&s_denied, denied);
+    uint32_t done = 0;
+#pragma unroll
+    for (int k = 0; k < kKvReqPerThread; ++k) done += (uint32_t)__popcll(__ballot(k < per && tid * per + k < n && ok[k]));
+    if ((tid & 63) == 0 && done) atomicAdd(&s_done, done);
     uint32_t at = kv_block_scan(entries, s_part, &total);
 #pragma unroll
     for (int k = 0; k < kKvReqPerThread; ++k) {
@@ -475,7 +476,7 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_fork(KvForkArgs x
             a.counts[0] = (int)s_done;
             a.counts[1] = (int)total;
             a.counts[2] = (int)taken;
-            a.counts[3] = (int)s_denied;
+            a.counts[3] = n - (int)s_done;
         }
     }
     __syncthreads();
