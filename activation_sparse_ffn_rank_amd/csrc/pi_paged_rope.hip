@@ -22,8 +22,9 @@ int check_rope(const pi_kv_cache *c, const pi_kv_rope *r) {
 
 template <class T, int HD>
 void launch(const KvRopeArgs &a, bool pairs, dim3 grid, hipStream_t st) {
-    if (pairs) hipLaunchKernelGGL((k_kv_rope<T, HD, true>), grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((k_kv_rope<T, HD, false>), grid, dim3(256), 0, st, a);
+    const size_t lds = (size_t)a.v_tile * (HD / 2 + 1) * sizeof(uint32_t);
+    if (pairs) hipLaunchKernelGGL((k_kv_rope<T, HD, true>), grid, dim3(256), lds, st, a);
+    else hipLaunchKernelGGL((k_kv_rope<T, HD, false>), grid, dim3(256), lds, st, a);
 }
 template <class T>
 void launch_hd(int hd, const KvRopeArgs &a, bool pairs, dim3 grid, hipStream_t st) {
@@ -85,7 +86,9 @@ extern "C" int pi_kv_rope_append(const pi_kv_cache *cache, const pi_kv_batch *ba
     // enough waves to fill the chip, then heads one after another for the angles' sake
     while (a.per_wave < 8 && tokens * (n_q + a.n_kv) / (a.per_wave * side) > 16384) a.per_wave *= 2;
     a.q_parts = (n_q + a.per_wave * side - 1) / (a.per_wave * side), a.k_parts = (a.n_kv + a.per_wave * side - 1) / (a.per_wave * side);
-    a.v_groups = (total_q + 15) / 16 * a.n_kv;
+    // values: tiles as of pi_kv_append
+    a.v_tile = (int64_t)((total_q + 63) / 64) * cache->n_kv >= 2 * kCus ? 64 : 16;
+    a.v_groups = (total_q + a.v_tile - 1) / a.v_tile * a.n_kv;
     const int64_t waves = tokens * (a.q_parts + a.k_parts);
     const dim3 grid((uint32_t)(a.v_groups + (waves + 3) / 4));
     hipStream_t st = static_cast<hipStream_t>(stream);
