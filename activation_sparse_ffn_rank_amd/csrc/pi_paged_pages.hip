@@ -75,7 +75,7 @@ extern "C" int pi_kv_copy(const pi_kv_cache *cache, const int32_t *copies, int32
     if (n == 0) return PI_OK;
     if (!copies) return PI_ERR_NULL;
     const int64_t units = (int64_t)cache->n_kv * cache->page * cache->head_dim / 8;
-    const KvCopyArgs a{copies, cache->n_pages, units, static_cast<uint4 *>(cache->k_pages), static_cast<uint4 *>(cache->v_pages)};
+    const KvCopyArgs a{copies, cache->n_pages, units, static_cast<f32x4 *>(cache->k_pages), static_cast<f32x4 *>(cache->v_pages)};
     // 16 KB a round: as many workgroups for a page as make 4096 of them all, the rounds shared out evenly
     const int64_t rounds = (units + 1023) / 1024, most = std::max<int64_t>(1, 4096 / (2 * (int64_t)n));
     const int64_t each = (rounds + most - 1) / most, parts = (rounds + each - 1) / each;

@@ -22,7 +22,7 @@ int check_rope(const pi_kv_cache *c, const pi_kv_rope *r) {
 
 template <class T, int HD>
 void launch(const KvRopeArgs &a, bool pairs, dim3 grid, hipStream_t st) {
-    const size_t lds = (size_t)a.v_tile * (HD / 2 + 1) * sizeof(uint32_t);
+    const size_t lds = std::max<size_t>(a.v_tile * (HD / 2 + 1), 4 * HD) * sizeof(uint32_t);
     if (pairs) hipLaunchKernelGGL((k_kv_rope<T, HD, true>), grid, dim3(256), lds, st, a);
     else hipLaunchKernelGGL((k_kv_rope<T, HD, false>), grid, dim3(256), lds, st, a);
 }
@@ -77,19 +77,15 @@ extern "C" int pi_kv_rope_append(const pi_kv_cache *cache, const pi_kv_batch *ba
     a.slots = slots, a.q_start = batch->q_start, a.kv_len = batch->kv_len;
     a.q_out = static_cast<uint16_t *>(q_out), a.k_pages = static_cast<uint16_t *>(cache->k_pages);
     a.v_pages = static_cast<uint16_t *>(cache->v_pages);
-    // Lane groups of a wave: tokens side by side, as many as there are, and heads for the rest.
-    const int groups = 64 / (cache->head_dim / 16);
-    while ((2 << a.tok_log) <= groups && (1 << a.tok_log) < total_q) ++a.tok_log;
-    const int side = groups >> a.tok_log;
+    // a wave per token and round of heads, until there are many: then rounds one after another for the angles' sake
+    const int side = 64 / (cache->head_dim / 16), rounds = (n_q + a.n_kv + side - 1) / side;
     a.per_wave = 1;
-    const int64_t tokens = (total_q + (1 << a.tok_log) - 1) >> a.tok_log;
-    // enough waves to fill the chip, then heads one after another for the angles' sake
-    while (a.per_wave < 8 && tokens * (n_q + a.n_kv) / (a.per_wave * side) > 16384) a.per_wave *= 2;
-    a.q_parts = (n_q + a.per_wave * side - 1) / (a.per_wave * side), a.k_parts = (a.n_kv + a.per_wave * side - 1) / (a.per_wave * side);
+    while (a.per_wave < 4 && (int64_t)total_q * rounds > (int64_t)a.per_wave * 8192) a.per_wave *= 2;
+    a.parts = (rounds + a.per_wave - 1) / a.per_wave;
     // values: tiles as of pi_kv_append
     a.v_tile = (int64_t)((total_q + 63) / 64) * cache->n_kv >= 2 * kCus ? 64 : 16;
     a.v_groups = (total_q + a.v_tile - 1) / a.v_tile * a.n_kv;
-    const int64_t waves = tokens * (a.q_parts + a.k_parts);
+    const int64_t waves = (int64_t)total_q * a.parts;
     const dim3 grid((uint32_t)(a.v_groups + (waves + 3) / 4));
     hipStream_t st = static_cast<hipStream_t>(stream);
     const bool pairs = rope->layout == PI_ROPE_PAIRS;

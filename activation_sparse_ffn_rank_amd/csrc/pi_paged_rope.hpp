@@ -12,9 +12,7 @@ namespace pik {
 
 struct KvRopeArgs {
     int n_req, total_q, n_q, n_kv, page_log, n_slots, rot, norm;
-    int tok_log;                      // log2 of the tokens that a wave takes side by side
-    int per_wave;                     // heads that a group of lanes takes one after another
-    int q_parts, k_parts;             // waves that share out the query heads of a token group, and the kv heads
+    int per_wave, parts;              // heads that a group of lanes takes one after another; waves that share out a token's heads
     int v_groups, v_tile;             // workgroups that transpose values, numbered first, and tokens of each
     float scale, eps;
     int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;
@@ -24,39 +22,26 @@ struct KvRopeArgs {
     uint16_t *q_out, *k_pages, *v_pages;
 };
 
+// Where packed row t stands (in: it belongs to a request).  q_start is searched 64 entries at a time, by all lanes of a wave.
 struct KvPlace {
-    bool in;             // the row belongs to a request
+    bool in;
     int64_t pos;
 };
-// Where the packed rows t0, t0 + 1, .. of a wave's lane groups stand; `mine` is this lane's.  q_start is searched 64 entries
-// at a time.
-__device__ __forceinline__ KvPlace kv_place(const KvRopeArgs &a, int t0, int tokens, int mine, int lane) {
-    KvPlace x{false, 0};
-    const int step = (a.n_req + 63) / 64;
-    const int s1 = lane * step < a.n_req ? a.q_start[lane * step] : INT32_MAX;
-    const int e1 = lane < a.n_req ? a.q_start[lane + 1] : 0, m1 = lane < a.n_req ? a.kv_len[lane] : 0;
-    for (int i = 0; i < tokens; ++i) {
-        const int t = t0 + i;
-        int r = __popcll(__ballot(s1 <= t)) - 1;
-        if (r < 0) continue;
-        int start = bcast(s1, r), end, m;
-        if (step == 1) {
-            end = bcast(e1, r), m = bcast(m1, r);
-        } else {
-            const int at = r * step + lane;
-            const int s2 = lane < step && at < a.n_req ? a.q_start[at] : INT32_MAX;
-            const int l = __popcll(__ballot(s2 <= t)) - 1;
-            if (l < 0) continue;                         // (starts that decrease)
-            start = bcast(s2, l);
-            r = r * step + l;
-            end = a.q_start[r + 1], m = a.kv_len[r];
-        }
-        if (i == mine) {
-            x.in = start >= 0 && t >= start && t < end && end <= a.total_q;
-            x.pos = (int64_t)m - end + t;
-        }
+__device__ __forceinline__ KvPlace kv_place(const KvRopeArgs &a, int t, int lane) {
+    const int step = (a.n_req + 63) / 64, at = lane * step;
+    int start = at < a.n_req ? a.q_start[at] : INT32_MAX;
+    int end = step == 1 && at < a.n_req ? a.q_start[at + 1] : 0, m = step == 1 && at < a.n_req ? a.kv_len[at] : 0;
+    int l = __popcll(__ballot(start <= t)) - 1;
+    if (l < 0) return {false, 0};
+    if (step > 1) {
+        const int r = l * step + lane;
+        const bool in = lane < step && r < a.n_req;
+        start = in ? a.q_start[r] : INT32_MAX, end = in ? a.q_start[r + 1] : 0, m = in ? a.kv_len[r] : 0;
+        l = __popcll(__ballot(start <= t)) - 1;
+        if (l < 0) return {false, 0};                    // (starts that decrease)
     }
-    return x;
+    start = bcast(start, l), end = bcast(end, l), m = bcast(m, l);
+    return {start >= 0 && t >= start && t < end && end <= a.total_q, (int64_t)m - end + t};
 }
 
 template <class T>
@@ -110,78 +95,75 @@ __device__ __forceinline__ void kv_values(const KvRopeArgs &a, uint32_t *s_v) {
     }
 }
 
-// Workgroups below v_groups take values.  The others: a wave takes 2^tok_log tokens and, one after another, some of their query or
-// key heads, whose angles it computes once.
+// Workgroups below v_groups take values.  The others: a wave takes one token and some of its query and key heads, 64 / L side by
+// side, which it finds next to one another, some of them one after another.  Its lanes compute the cosines and sines of a pair each
+// (heads of 256: two) and hand them round through LDS.
 template <class T, int HD, bool PAIRS>
 __global__ __launch_bounds__(256) void k_kv_rope(KvRopeArgs a) {
-    constexpr int L = HD / 16;
-    extern __shared__ uint32_t s_v[];                // [v_tile][HD/2 + 1]
+    constexpr int L = HD / 16, kSide = 64 / L;
+    extern __shared__ uint32_t s_v[];                // values: [v_tile][HD/2 + 1]; others: [wave][2][HD/2] cosines, sines
     if ((int)blockIdx.x < a.v_groups) {
         if (a.v_tile == 64) kv_values<HD, 64>(a, s_v);
         else kv_values<HD, 16>(a, s_v);
         return;
     }
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int w = ((int)blockIdx.x - a.v_groups) * 4 + (tid >> 6), parts = a.q_parts + a.k_parts;
-    const int tokens = 1 << a.tok_log, side = (64 / L) >> a.tok_log;        // heads side by side
-    const int part = w % parts, t0 = w / parts << a.tok_log;
-    if (t0 >= a.total_q) return;
-    const int l = lane & (L - 1), g = lane / L, mine = g & (tokens - 1), t = min(t0 + mine, a.total_q - 1);
-    const bool keys = part >= a.q_parts;
-    const int heads = keys ? a.n_kv : a.n_q, n = a.per_wave * side;
-    const int hp = (keys ? part - a.q_parts : part) * n, h0 = hp + (g >> a.tok_log), h1 = min(hp + n, heads);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int w = ((int)blockIdx.x - a.v_groups) * 4 + wave;
+    const int part = w % a.parts, t = w / a.parts;
+    if (t >= a.total_q) return;
+    const int l = lane & (L - 1), g = lane / L, heads = a.n_q + a.n_kv;
+    const int hp = part * a.per_wave * kSide, h0 = hp + g, h1 = min(hp + a.per_wave * kSide, heads);
     const int rest = l - a.rot / 16;                                        // of those not turned
     const bool turned0 = PAIRS ? 8 * l < a.rot : rest < 0, turned1 = PAIRS ? HD / 2 + 8 * l < a.rot : rest < 0;
     const int at0 = PAIRS || rest < 0 ? 8 * l : a.rot + 8 * rest;
     const int at1 = at0 + (PAIRS ? HD / 2 : rest < 0 ? a.rot / 2 : (HD - a.rot) / 2);
-    const uint16_t *const src = keys ? a.k + t * a.k_ts : a.q + t * a.q_ts;
-    const int64_t src_hs = keys ? a.k_hs : a.q_hs;
-    // the first head's elements, frequencies and weights are on their way while the row's place is found
-    uint4 r0 = ld16(src + min(h0, heads - 1) * src_hs + at0), r1 = ld16(src + min(h0, heads - 1) * src_hs + at1);
-    uint32_t slot = keys ? (uint32_t)a.slots[t] : 0u;
-    double freq[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) freq[i] = 0.0;
-    if (turned0)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) freq[i] = a.freq[(PAIRS ? 4 : 8) * l + i];
-    if (turned1)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) freq[4 + i] = a.freq[(PAIRS ? HD / 4 + 4 * l : 8 * l + 4) + i];
-    float w0[8], w1[8];
-    const uint16_t *const weight = keys ? a.k_weight : a.q_weight;
-    if (a.norm && weight) {
-        kv_floats<T>(ld16(weight + at0), w0);
-        kv_floats<T>(ld16(weight + at1), w1);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w0[i] = w1[i] = 1.f;
+    const uint16_t *const qs = a.q + t * a.q_ts, *const ks = a.k + t * a.k_ts;
+    auto source = [&](int h) { return h < a.n_q ? qs + h * a.q_hs : ks + (h - a.n_q) * a.k_hs; };
+    // the first heads' elements, frequencies, weights and slot are on their way while the row's place is found
+    uint4 r0 = zero4(), r1 = zero4(), qw0 = zero4(), qw1 = zero4(), kw0 = zero4(), kw1 = zero4();
+    if (h0 < h1) {
+        r0 = ld16(source(h0) + at0);
+        r1 = ld16(source(h0) + at1);
     }
-    const KvPlace place = kv_place(a, t0, tokens, mine, lane);
-    if (!place.in || (keys && slot >= (uint32_t)a.n_slots)) return;
+    const uint32_t slot = (uint32_t)a.slots[t];
+    constexpr int kPer = HD == 256 ? 2 : 1;
+    double freq[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) freq[i] = 2 * (lane + 64 * i) < a.rot ? a.freq[lane + 64 * i] : 0.0;
+    if (a.norm && a.q_weight) qw0 = ld16(a.q_weight + at0), qw1 = ld16(a.q_weight + at1);
+    if (a.norm && a.k_weight) kw0 = ld16(a.k_weight + at0), kw1 = ld16(a.k_weight + at1);
+    const KvPlace place = kv_place(a, t, lane);
+    if (!place.in) return;
     float c[8], s[8];
+    if (a.rot) {
+        float *const cs = reinterpret_cast<float *>(s_v) + wave * HD, *const ss = cs + HD / 2;
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
-        if (half ? turned1 : turned0) {
-#pragma unroll
-            for (int i = 4 * half; i < 4 * half + 4; ++i) {
-                // the angle in turns, less whole ones, in 64 bits: far positions have few bits behind the point
-                double x = (double)place.pos * (freq[i] * 0.15915494309189535);
-                x -= rint(x);
-                sincospif(2.f * (float)x, &s[i], &c[i]);
-                s[i] *= a.scale, c[i] *= a.scale;
-            }
+        for (int i = 0; i < kPer; ++i) {
+            // the angle in turns, less whole ones, in 64 bits: far positions have few bits behind the point
+            double x = (double)place.pos * (freq[i] * 0.15915494309189535);
+            x -= rint(x);
+            float sine, cosine;
+            sincospif(2.f * (float)x, &sine, &cosine);
+            if (2 * (lane + 64 * i) < HD) cs[lane + 64 * i] = cosine * a.scale, ss[lane + 64 * i] = sine * a.scale;
         }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        const int p0 = PAIRS ? 4 * l : turned0 ? 8 * l : 0, p1 = PAIRS ? HD / 4 + 4 * l : p0 + 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = cs[p0 + i], s[i] = ss[p0 + i], c[4 + i] = cs[p1 + i], s[4 + i] = ss[p1 + i];
+    }
+    const bool stored = slot < (uint32_t)a.n_slots;
     const int64_t pg = slot >> a.page_log, off = slot & ((1u << a.page_log) - 1);
-    uint16_t *const dst = keys ? a.k_pages + (((pg * a.n_kv) << a.page_log) + off) * HD : a.q_out + t * a.o_ts;
-    const int64_t dst_hs = keys ? (int64_t)HD << a.page_log : a.o_hs;
-    for (int h = h0; h < h1; h += side) {
+    uint16_t *const qd = a.q_out + t * a.o_ts, *const kd = a.k_pages + (((pg * a.n_kv) << a.page_log) + off) * HD;
+    for (int h = h0; h < h1; h += kSide) {
+        const bool key = h >= a.n_q;
         float x0[8], x1[8];
         kv_floats<T>(r0, x0);
         kv_floats<T>(r1, x1);
-        if (h + side < h1) {                                                // the next head's
-            r0 = ld16(src + (h + side) * src_hs + at0);
-            r1 = ld16(src + (h + side) * src_hs + at1);
+        if (h + kSide < h1) {                                               // the next heads'
+            r0 = ld16(source(h + kSide) + at0);
+            r1 = ld16(source(h + kSide) + at1);
         }
         if (a.norm) {
             float sum = 0.f;
@@ -189,7 +171,14 @@ __global__ __launch_bounds__(256) void k_kv_rope(KvRopeArgs a) {
             for (int i = 0; i < 8; ++i) sum += x0[i] * x0[i] + x1[i] * x1[i];
             const float f = 1.f / sqrtf(kv_lane_sum<L>(sum) * (1.f / HD) + a.eps);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x0[i] *= f * w0[i], x1[i] *= f * w1[i];
+            for (int i = 0; i < 8; ++i) x0[i] *= f, x1[i] *= f;
+            if (key ? a.k_weight != nullptr : a.q_weight != nullptr) {
+                float w0[8], w1[8];
+                kv_floats<T>(key ? kw0 : qw0, w0);
+                kv_floats<T>(key ? kw1 : qw1, w1);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x0[i] *= w0[i], x1[i] *= w1[i];
+            }
         }
         auto turn = [&](float &p, float &q, int i) {
             const float u = p * c[i] - q * s[i], v = p * s[i] + q * c[i];
@@ -206,8 +195,10 @@ __global__ __launch_bounds__(256) void k_kv_rope(KvRopeArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) turn(x0[i], x1[i], i);
         }
-        *reinterpret_cast<uint4 *>(dst + h * dst_hs + at0) = kv_halves<T>(x0);
-        *reinterpret_cast<uint4 *>(dst + h * dst_hs + at1) = kv_halves<T>(x1);
+        if (key && !stored) continue;
+        uint16_t *const dst = key ? kd + ((int64_t)(h - a.n_q) << a.page_log) * HD : qd + h * a.o_hs;
+        *reinterpret_cast<uint4 *>(dst + at0) = kv_halves<T>(x0);
+        *reinterpret_cast<uint4 *>(dst + at1) = kv_halves<T>(x1);
     }
 }
 
