@@ -197,8 +197,8 @@ __global__ __launch_bounds__(256) void k_kv_rope(KvRopeArgs a) {
         }
         if (key && !stored) continue;
         uint16_t *const dst = key ? kd + ((int64_t)(h - a.n_q) << a.page_log) * HD : qd + h * a.o_hs;
-        *reinterpret_cast<uint4 *>(dst + at0) = kv_halves<T>(x0);
-        *reinterpret_cast<uint4 *>(dst + at1) = kv_halves<T>(x1);
+        __builtin_nontemporal_store(__builtin_bit_cast(f32x4, kv_halves<T>(x0)), reinterpret_cast<f32x4 *>(dst + at0));
+        __builtin_nontemporal_store(__builtin_bit_cast(f32x4, kv_halves<T>(x1)), reinterpret_cast<f32x4 *>(dst + at1));
     }
 }
 
