@@ -57,7 +57,7 @@ extern "C" int pi_kv_append(const pi_kv_cache *cache, const void *k, int64_t k_t
 
 extern "C" size_t pi_kv_attn_workspace_bytes(const pi_kv_cache *cache, const pi_kv_batch *batch, int32_t total_q, int32_t n_q) {
     if (check_cache(cache) || check_batch(batch) || check_rows(cache, total_q, n_q)) return 0;
-    return attn_plan(cache, batch, total_q, n_q, batch->max_kv).bytes;
+    return attn_plan(cache, batch, total_q, n_q, batch->max_kv, false).bytes;
 }
 
 extern "C" int pi_kv_attn(const pi_kv_cache *cache, const pi_kv_batch *batch, const void *q, int64_t q_token_stride,
@@ -70,5 +70,5 @@ extern "C" int pi_kv_attn(const pi_kv_cache *cache, const pi_kv_batch *batch, co
     if (!q || !out) return PI_ERR_NULL;
     if (window < 0 || !(scale > 0.f) || !std::isfinite(scale)) return PI_ERR_SHAPE;
     return run_attn<false>(cache, batch, q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, total_q, n_q,
-                           scale, window, 0, batch->max_kv, ws, ws_bytes, static_cast<hipStream_t>(stream));
+                           scale, window, 0, batch->max_kv, false, ws, ws_bytes, static_cast<hipStream_t>(stream));
 }

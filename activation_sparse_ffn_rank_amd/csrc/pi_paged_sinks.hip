@@ -12,6 +12,9 @@ int most_keys(const pi_kv_batch *b, int32_t window, int32_t sinks) {
     return (int)std::min<int64_t>(keys, b->max_kv);
 }
 
+// Of requests of up to twice as many keys as they read or more, most read that many.
+bool even_ranges(const pi_kv_batch *b, int32_t window, int32_t sinks) { return b->max_kv / 2 >= most_keys(b, window, sinks); }
+
 int check_window(int32_t window, int32_t sinks) {
     return window < 0 || sinks < 0 || (window == 0 && sinks > 0) ? PI_ERR_SHAPE : PI_OK;
 }
@@ -22,7 +25,7 @@ extern "C" size_t pi_kv_attn_sinks_workspace_bytes(const pi_kv_cache *cache, con
                                                    int32_t window, int32_t sinks) {
     if (sinks == 0 && window >= 0) return pi_kv_attn_workspace_bytes(cache, batch, total_q, n_q);
     if (check_cache(cache) || check_batch(batch) || check_rows(cache, total_q, n_q) || check_window(window, sinks)) return 0;
-    return attn_plan(cache, batch, total_q, n_q, most_keys(batch, window, sinks)).bytes;
+    return attn_plan(cache, batch, total_q, n_q, most_keys(batch, window, sinks), even_ranges(batch, window, sinks)).bytes;
 }
 
 extern "C" int pi_kv_attn_sinks(const pi_kv_cache *cache, const pi_kv_batch *batch, const void *q, int64_t q_token_stride,
@@ -39,5 +42,5 @@ extern "C" int pi_kv_attn_sinks(const pi_kv_cache *cache, const pi_kv_batch *bat
     if (!q || !out) return PI_ERR_NULL;
     if (!(scale > 0.f) || !std::isfinite(scale)) return PI_ERR_SHAPE;
     return run_attn<true>(cache, batch, q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, total_q, n_q,
-                          scale, window, sinks, most_keys(batch, window, sinks), ws, ws_bytes, static_cast<hipStream_t>(stream));
+                          scale, window, sinks, most_keys(batch, window, sinks), even_ranges(batch, window, sinks), ws, ws_bytes, static_cast<hipStream_t>(stream));
 }
