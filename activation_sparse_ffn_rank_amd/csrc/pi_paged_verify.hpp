@@ -160,6 +160,9 @@ __device__ __forceinline__ int kv_first_or_last(int first, int last, int *found)
     return low != INT32_MAX ? low : high;
 }
 
+// Bound by HBM for many requests (96 of them, two rows of 100003 each, 77 MB: 19.1 us a pass, of which the row sums end at about
+// 14), by latency for few: one request, 32000 tokens, 7.3 us, of which verdict 1, sums 1.5, their way to the last workgroup 2, its
+// sums, piece and draw 2.
 // Workgroup (group of pieces, request).  The last one of a request draws: an entry without weight is never taken, and where
 // rounding leaves none above the mark it is the last one with weight.
 static __global__ __launch_bounds__(256) void k_kv_verify(KvVerifyArgs a) {

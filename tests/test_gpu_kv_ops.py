@@ -1,7 +1,9 @@
 """The operators around paged attention on the GPU against plain 64-bit references: rotary positions and head norms
 with the append, attention over a window and the first tokens, drafted tokens, pages given back, shared and copied, and all of
 them together in a replayed graph."""
+import importlib.util
 import math
+import os
 import random
 
 import pytest
@@ -11,6 +13,7 @@ import activation_sparse_ffn_rank_amd as pi
 from activation_sparse_ffn_rank_amd import _abi, _kv
 import kv_ops_util as U
 import kv_util
+import synth
 from gpu_util import announce
 
 pytestmark = pytest.mark.gpu
@@ -794,6 +797,46 @@ def test_drafting_forking_steps_in_a_replayed_graph(page):
                 assert old >= 0 and int(a.table[long, (held - back) // page]) == new and torch.equal(a.k[old], a.k[new])
                 copied += 1
     assert cut > 20 and copied > 0
+
+
+def test_example_streams_past_its_window():
+    """The example with rotary positions, a window and first tokens: replayed steps equal eager ones, attention equals the
+    reference on the pages of the last step, and no page is lost."""
+    announce("paged decode example, streaming")
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "paged_decode.py")
+    spec = importlib.util.spec_from_file_location("paged_decode_streaming", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    cfg = synth.custom_config(1024, 2048, 64, layers=2, seed=3)
+    opts = dict(head_dim=64, kv_heads=4, rope=True, window=20, sinks=3)
+    graph, eager, _ = example.generate(cfg, 2, [5, 70, 33], 30, **opts)
+    assert torch.isfinite(eager).all() and torch.equal(graph, eager)
+    st = example.PagedStack(cfg, 2, 3, 120, **opts)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    free = []
+    for fresh in ([5, 70, 33], *[[1, 1, 1]] * 25):
+        st.fresh.copy_(dev(fresh))
+        p = st.plan(sum(fresh), max(fresh), 120)
+        real, seen = example.pi.pi_kv_attn_sinks, []
+
+        def attn(cache, batch, q, out, ws, **kw):
+            real(cache, batch, q, out, ws, **kw)
+            seen.append((st.caches.index(cache), q.cpu(), out.cpu(), st.table.tolist(), st.q_start.tolist(), st.kv_len.tolist()))
+
+        example.pi.pi_kv_attn_sinks = attn
+        try:
+            st.step(p, torch.randn((sum(fresh), cfg.d), generator=gen, device="cuda"))
+        finally:
+            example.pi.pi_kv_attn_sinks = real
+        assert st.counts.tolist()[3] == 0
+        l, q, out, table, starts, kv = seen[-1]
+        k, v = (t.cpu() for t in st.caches[l]._keep)
+        want, mag = U.sinks_reference(dict(table=table, starts=starts, kv=kv, k=k, v=v, q=q, scale=1 / 8), 20, 3)
+        assert bool(((out.double() - want).abs() <= kv_util.attn_tolerance(want, mag, torch.float16, 64, partial=16.0)).all())
+        U.check_owned(dict(cached=st.cached.tolist(), table=st.table.tolist(), ring=st.ring.tolist(), pool=st.pool.tolist(),
+                           shares=st.pages._keep[4].tolist(), page=st.page))
+        free.append(st.pool.tolist()[1])
+    assert free[-1] >= free[1] - 3            # longer requests hold no more pages: the first one's, the window's, one in between
 
 
 def test_on_another_stream():
