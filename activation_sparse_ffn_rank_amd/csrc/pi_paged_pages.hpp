@@ -63,13 +63,15 @@ struct KvReleaseWs {
     static constexpr int kInts = kFresh + PI_KV_MAX_REQ;
 };
 
-// Entries e0 .. e0 + kKvEach - 1: their places in the table, pages (-1: none, or out of range), and whether they become -1.
+// Entries of a thread: their places in the table, pages (-1: none, or out of range), and whether they become -1.
+template <int N>
 struct KvEntries {
-    int *at[kKvEach], p[kKvEach];
-    bool middle[kKvEach];
+    int *at[N], p[N];
+    bool middle[N];
 };
-__device__ __forceinline__ KvEntries kv_entries(const KvPagesArgs &a, const uint32_t *first, const int *col, uint32_t total, uint32_t e0) {
-    KvEntries x;
+// Those numbered e0 .. e0 + kKvEach - 1.
+__device__ __forceinline__ KvEntries<kKvEach> kv_entries(const KvPagesArgs &a, const uint32_t *first, const int *col, uint32_t total, uint32_t e0) {
+    KvEntries<kKvEach> x;
 #pragma unroll
     for (int i = 0; i < kKvEach; ++i) x.p[i] = -1, x.middle[i] = false, x.at[i] = a.table;
     if (e0 >= total) return x;
@@ -93,7 +95,7 @@ __device__ __forceinline__ KvEntries kv_entries(const KvPagesArgs &a, const uint
 template <class F>
 __device__ __forceinline__ void kv_walk(const KvPagesArgs &a, const uint32_t *first, const int *col, uint32_t total, uint32_t e0,
                                         F &&each) {
-    const KvEntries x = kv_entries(a, first, col, total, e0);
+    const KvEntries<kKvEach> x = kv_entries(a, first, col, total, e0);
 #pragma unroll
     for (int i = 0; i < kKvEach; ++i)
         if (x.p[i] >= 0) each(i, e0 + i, x.at[i], x.p[i], x.middle[i]);
@@ -146,47 +148,47 @@ __device__ __forceinline__ uint32_t kv_push(const KvPagesArgs &a, const uint32_t
     return back;
 }
 
-// The same passes by one workgroup over a list of one round, with the entries read once.  Where no page that is given up has
+// The same passes by one workgroup over a list of one round, N entries per thread in order, read before.  Where no page that is given up has
 // further owners and none is named twice -- every count was 0 -- all of them go back, and the second pass and its reads are left out;
 // likewise where those with further owners keep some.
-__device__ __forceinline__ uint32_t kv_one_round(const KvPagesArgs &a, const uint32_t *first, const int *col, uint32_t total,
-                                                 int64_t at, uint32_t *part, uint32_t &given) {
-    const uint32_t e0 = threadIdx.x * kKvEach;
-    const KvEntries x = kv_entries(a, first, col, total, e0);
-    int before[kKvEach];
+template <int N>
+__device__ __forceinline__ uint32_t kv_one_round(const KvPagesArgs &a, const KvEntries<N> &x, int64_t at, uint32_t *part,
+                                                 uint32_t &given) {
+    const uint32_t e0 = threadIdx.x * N;
+    int before[N];
     uint32_t mine = 0, wins = 0;
     bool plain = true, odd = false;
 #pragma unroll
-    for (int i = 0; i < kKvEach; ++i) before[i] = x.p[i] >= 0 ? KvShares<false>::less(a.shares + x.p[i]) : 0;
+    for (int i = 0; i < N; ++i) before[i] = x.p[i] >= 0 ? KvShares<false>::less(a.shares + x.p[i]) : 0;
 #pragma unroll
-    for (int i = 0; i < kKvEach; ++i) mine += x.p[i] >= 0, plain = plain && before[i] == 0;
-    bool won[kKvEach];
+    for (int i = 0; i < N; ++i) mine += x.p[i] >= 0, plain = plain && before[i] == 0;
+    bool won[N];
 #pragma unroll
-    for (int i = 0; i < kKvEach; ++i) won[i] = x.p[i] >= 0 && before[i] == 0;
+    for (int i = 0; i < N; ++i) won[i] = x.p[i] >= 0 && before[i] == 0;
     if (!__syncthreads_and(plain)) {
-        int left[kKvEach];
+        int left[N];
 #pragma unroll
-        for (int i = 0; i < kKvEach; ++i) left[i] = x.p[i] >= 0 ? KvShares<false>::load(a.shares + x.p[i]) : 0;
+        for (int i = 0; i < N; ++i) left[i] = x.p[i] >= 0 ? KvShares<false>::load(a.shares + x.p[i]) : 0;
 #pragma unroll
-        for (int i = 0; i < kKvEach; ++i) odd = odd || (left[i] < 0 && (left[i] != -1 || before[i] != 0));
+        for (int i = 0; i < N; ++i) odd = odd || (left[i] < 0 && (left[i] != -1 || before[i] != 0));
         if (__syncthreads_or(odd)) {
 #pragma unroll
-            for (int i = 0; i < kKvEach; ++i)
+            for (int i = 0; i < N; ++i)
                 if (left[i] < 0) KvShares<false>::lower(a.shares + x.p[i], INT32_MIN + (int)(e0 + i));
             kv_lds_wait();
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < kKvEach; ++i)
+            for (int i = 0; i < N; ++i)
                 won[i] = left[i] < 0 && KvShares<false>::load(a.shares + x.p[i]) == INT32_MIN + (int)(e0 + i);
         }
     }
 #pragma unroll
-    for (int i = 0; i < kKvEach; ++i) wins += won[i];
+    for (int i = 0; i < N; ++i) wins += won[i];
     uint32_t all;                              // both numbers in one scan: at most 4096 each
     uint32_t rank = kv_block_scan(wins | mine << 16, part, &all) & 0xffff;
     given = all >> 16, all &= 0xffff;
 #pragma unroll
-    for (int i = 0; i < kKvEach; ++i) {
+    for (int i = 0; i < N; ++i) {
         if (x.middle[i] && x.p[i] >= 0) *x.at[i] = -1;
         if (!won[i]) continue;
         a.ring[(at + rank++) % a.n_pages] = x.p[i];
@@ -210,7 +212,7 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_release(KvRelease
     const int pool0 = a.pool[0], pool1 = a.pool[1];
     if (tid == 0) s_denied = 0;
 
-    int c[kKvReqPerThread], f[kKvReqPerThread], t[kKvReqPerThread], old[kKvReqPerThread];
+    int c[kKvReqPerThread], f[kKvReqPerThread], t[kKvReqPerThread], old[kKvReqPerThread], end[kKvReqPerThread];
     bool bad[kKvReqPerThread], tail[kKvReqPerThread], split[kKvReqPerThread];
 #pragma unroll
     for (int k = 0; k < kKvReqPerThread; ++k) {
@@ -227,6 +229,16 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_release(KvRelease
         bad[k] = c[k] < 0 || c[k] > room;
         tail[k] = k < per && r < n && !bad[k] && t[k] >= c[k] && f[k] < c[k];
         old[k] = tail[k] && (f[k] & (page - 1)) ? a.table[(int64_t)r * a.table_stride + (f[k] >> a.page_log)] : -1;
+        end[k] = k >= per || r >= n || bad[k] || f[k] >= c[k] ? 0 : tail[k] ? (c[k] + page - 1) >> a.page_log : max(t[k], 0) >> a.page_log;
+    }
+    // With a request per thread the first pages that it gives up are read at once: there may be no others.
+    int early[3] = {-1, -1, -1};
+    if (per == 1) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int col = (f[0] >> a.page_log) + i;
+            if (col < end[0]) early[i] = a.table[(int64_t)tid * a.table_stride + col];
+        }
     }
     int head = pool0 % a.n_pages;
     if (head < 0) head += a.n_pages;
@@ -254,14 +266,44 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_release(KvRelease
         }
         denied += refused;
         const int first = split[k] ? f[k] >> a.page_log : (int)(((int64_t)f[k] + page - 1) >> a.page_log);
-        const int end = f[k] >= c[k] ? 0 : tail[k] ? (c[k] + page - 1) >> a.page_log : max(t[k], 0) >> a.page_log;
-        if (!refused) mine[k] = (uint32_t)max(end - first, 0);
+        if (!refused) mine[k] = (uint32_t)max(end[k] - first, 0);
         split[k] = split[k] && !refused;
         tail[k] = tail[k] && !refused;
         s_col[r] = first | (tail[k] ? 0 : kKvMiddle);
         entries += mine[k];
     }
     if (denied) atomicAdd(&s_denied, denied);
+    const uint32_t taken = min(total_asks, (uint32_t)count);
+    if (per == 1 && __syncthreads_and(mine[0] <= 2)) {
+        // two pages of a request at most
+        const int skip = split[0] || !(f[0] & (page - 1)) ? 0 : 1;
+        KvEntries<2> e;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            e.at[i] = a.table + (int64_t)tid * a.table_stride + (f[0] >> a.page_log) + skip + i;
+            e.p[i] = (uint32_t)i < mine[0] ? skip ? early[i + 1] : early[i] : -1;
+            if ((uint32_t)e.p[i] >= (uint32_t)a.n_pages) e.p[i] = -1;
+            e.middle[i] = !tail[0];
+        }
+        uint32_t given;
+        const uint32_t back = kv_one_round(a, e, (int64_t)head + count, s_part, given);
+        if (tid < n) {
+            x.copies[2 * tid] = split[0] ? old[0] : -1;
+            x.copies[2 * tid + 1] = split[0] ? fresh[0] : -1;
+            a.cached_next[tid] = tail[0] ? f[0] : c[0];
+            if (split[0]) a.table[(int64_t)tid * a.table_stride + (f[0] >> a.page_log)] = fresh[0];
+        }
+        if (tid == 0) {
+            a.pool_next[0] = (int)(((int64_t)head + taken) % a.n_pages);
+            a.pool_next[1] = (int)min((int64_t)count - taken + back, (int64_t)a.n_pages);
+            a.counts[0] = (int)given;
+            a.counts[1] = (int)back;
+            a.counts[2] = (int)taken;
+            a.counts[3] = (int)s_denied;
+            if (x.ws) x.ws[KvReleaseWs::kTotal] = 0;
+        }
+        return;
+    }
     uint32_t at = kv_block_scan(entries, s_part, &total);       // (its barriers order s_col and the reads of the ring, too)
     const bool go_on = x.ws && total > blockDim.x * kKvShortList;
 #pragma unroll
@@ -280,7 +322,6 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_release(KvRelease
         at += mine[k];
     }
     __syncthreads();
-    const uint32_t taken = min(total_asks, (uint32_t)count);
     if (x.ws && tid == 0) {
         x.ws[KvReleaseWs::kTotal] = go_on ? (int)total : 0;
         x.ws[KvReleaseWs::kHead] = head;
@@ -292,7 +333,7 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_release(KvRelease
     if (go_on) return;
     uint32_t back = 0, given = 0;
     if (total && total <= blockDim.x * kKvEach) {
-        back = kv_one_round(a, s_first, s_col, total, (int64_t)head + count, s_part, given);
+        back = kv_one_round(a, kv_entries(a, s_first, s_col, total, tid * kKvEach), (int64_t)head + count, s_part, given);
         __syncthreads();
     } else if (total) {
         const uint32_t mine = kv_give<false>(a, s_first, s_col, 0, total);
