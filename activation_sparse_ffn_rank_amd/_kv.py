@@ -149,9 +149,10 @@ def _rows(fn: str, t, cache: pi_kv_cache) -> tuple[int, int, int, int, int]:
         raise PiError(fn, PI_ERR_NULL)
     if KV_DTYPES.get(t.dtype) != cache.dtype:
         raise PiError(fn, PI_ERR_DTYPE)
-    if t.dim() != 3:
+    shape = t.shape
+    if len(shape) != 3:
         raise PiError(fn, PI_ERR_SHAPE)
-    n, heads, hd = t.shape
+    n, heads, hd = shape
     ts, hs, one = t.stride()
     if hd != cache.head_dim or one != 1:
         raise PiError(fn, PI_ERR_SHAPE)
@@ -337,14 +338,15 @@ def pi_kv_rope_append(cache: pi_kv_cache, batch: pi_kv_batch, rope: pi_kv_rope, 
     qp, qt, qh, n, heads = _rows(fn, q, cache)
     kp, kt, kh, n_k, heads_k = _rows(fn, k, cache)
     vp, vt, vh, n_v, heads_v = _rows(fn, v, cache)
-    op, ot, oh, n_o, heads_o = _rows(fn, q_out, cache)
-    if n_k != n or n_v != n or n_o != n or heads_k != cache.n_kv or heads_v != heads_k or heads_o != heads or n >= 2 ** 31 or heads >= 2 ** 31:
+    op, ot, oh, n_o, heads_o = (qp, qt, qh, n, heads) if q_out is q else _rows(fn, q_out, cache)
+    if not n == n_k == n_v == n_o or heads_o != heads or not heads_k == heads_v == cache.n_kv or n >= 2 ** 31 or heads >= 2 ** 31:
         raise PiError(fn, PI_ERR_SHAPE)
-    if rope._weights is not None and rope._weights != (q.dtype, cache.head_dim):
-        raise PiError(fn, PI_ERR_DTYPE if rope._weights[0] != q.dtype else PI_ERR_SHAPE)
-    at, device = _ints(fn, slots, n), cache._device
-    if (q.get_device() != device or k.get_device() != device or v.get_device() != device or q_out.get_device() != device
-            or slots.get_device() != device or batch._device != device or rope._device not in (None, device)):
+    weights = rope._weights
+    if weights is not None and weights != (q.dtype, cache.head_dim):
+        raise PiError(fn, PI_ERR_DTYPE if weights[0] != q.dtype else PI_ERR_SHAPE)
+    at, device, on = _ints(fn, slots, n), cache._device, rope._device
+    if not (q.get_device() == k.get_device() == v.get_device() == q_out.get_device() == slots.get_device() == batch._device == device
+            and (on is None or on == device)):
         raise PiError(fn, PI_ERR_NULL)
     stream = _current_stream(device) if stream is None and device >= 0 else _raw_stream(fn, stream, device)
     if _current_device() != device:
@@ -446,19 +448,22 @@ def pi_kv_verify(drafts: pi_kv_drafts, accepted: torch.Tensor, next: torch.Tenso
     fn = "pi_kv_verify"
     n, device = drafts.n_req, drafts._device
     ap, np_ = _ints(fn, accepted, n), _ints(fn, next, n)
-    lp, kp = (None if t is None else _ints(fn, t, n) for t in (kv_len, keep))
+    lp, kp = None if kv_len is None else _ints(fn, kv_len, n), None if keep is None else _ints(fn, keep, n)
     wp, wn = None, 0
     if ws is not None:
         if not ws.is_contiguous():
             raise PiError(fn, PI_ERR_WORKSPACE)
         wp, wn = ws.data_ptr(), ws.nbytes
-    if any(t is not None and t.get_device() != device for t in (accepted, next, ws, kv_len, keep)):
-        raise PiError(fn, PI_ERR_NULL)
+    for t in (accepted, next, ws, kv_len, keep):
+        if t is not None and t.get_device() != device:
+            raise PiError(fn, PI_ERR_NULL)
     stream = _raw_stream(fn, stream, device)
     if _current_device() != device:
         with torch.cuda.device(device):
             return pi_kv_verify(drafts, accepted, next, ws, kv_len=kv_len, keep=keep, stream=stream)
-    _check(fn, kv_lib().pi_kv_verify(drafts, lp, ap, np_, kp, wp, wn, stream))
+    rc = (_kv_lib or kv_lib()).pi_kv_verify(drafts, lp, ap, np_, kp, wp, wn, stream)
+    if rc != PI_OK:
+        raise PiError(fn, rc)
 
 
 # ------------------------------------------------------------------------------ pages given back, shared and copied
@@ -505,8 +510,9 @@ def _copies(fn: str, t, n: int) -> int:
 
 
 def _on(fn: str, device: int, *tensors) -> None:
-    if any(t.get_device() != device for t in tensors):
-        raise PiError(fn, PI_ERR_NULL)
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise PiError(fn, PI_ERR_NULL)
 
 
 def pi_kv_release(pages: pi_kv_pages, drop_from: torch.Tensor, drop_to: torch.Tensor | None, copies: torch.Tensor, stream=None) -> None:
@@ -515,7 +521,7 @@ def pi_kv_release(pages: pi_kv_pages, drop_from: torch.Tensor, drop_to: torch.Te
     fn = "pi_kv_release"
     n, device = pages.n_req, pages._device
     fp, tp, cp = _ints(fn, drop_from, n), None if drop_to is None else _ints(fn, drop_to, n), _copies(fn, copies, n)
-    _on(fn, device, *(t for t in (drop_from, drop_to, copies) if t is not None))
+    _on(fn, device, drop_from, drop_to, copies)
     stream = _raw_stream(fn, stream, device)
     if _current_device() != device:
         with torch.cuda.device(device):
