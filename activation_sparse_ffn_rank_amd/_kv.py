@@ -1,5 +1,6 @@
-"""ctypes binding of the C ABI in include/pi_paged_kv.h: the paged key/value cache, its block tables and
-the attention that reads it (argument marshalling only, as in ``_abi``).
+"""ctypes binding of the C ABI in include/pi_paged_kv.h: the paged key/value cache, its block tables, the append with
+rotary positions or without, the attention that reads it, drafted tokens, and pages given back, shared and copied
+(argument marshalling only, as in ``_abi``).
 
 What only a tensor knows -- element type, shape, strides -- is checked here and refused with the same
 codes that the library uses (``PiError``), and so are numbers that do not fit its 32-bit arguments, which

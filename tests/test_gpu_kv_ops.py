@@ -858,6 +858,97 @@ def test_on_another_stream():
     check_state(d, U.release_reference(st, at, to))
 
 
+def test_calls_of_no_rows():
+    announce("calls of no rows")
+    k, v = torch.ones((4, 2, 16, 64), dtype=torch.float16, device="cuda"), torch.ones((4, 2, 64, 16), dtype=torch.float16, device="cuda")
+    cache, none = pi.make_kv_cache(k, v), torch.empty((0, 2, 64), dtype=torch.float16, device="cuda")
+    batch = pi.make_kv_batch(dev([[0], [1]]), dev([0, 0, 0]), dev([5, 0]), max_q=1, max_kv=16)
+    rope = pi.make_kv_rope(pi.pi_rope_frequencies(64).cuda(), norm=True)
+    q = torch.empty((0, 4, 64), dtype=torch.float16, device="cuda")
+    pi.pi_kv_rope_append(cache, batch, rope, q, none, none, dev([]), q.clone())
+    pi.pi_kv_attn_sinks(cache, batch, q, q.clone(), torch.empty(16, dtype=torch.uint8, device="cuda"), scale=1.0, window=3, sinks=2)
+    pi.pi_kv_copy(cache, torch.empty((0, 2), dtype=torch.int32, device="cuda"))
+    # rows that belong to no request, and requests without rows
+    x, out = torch.ones((3, 2, 64), dtype=torch.float16, device="cuda"), torch.full((3, 4, 64), 7.0, dtype=torch.float16, device="cuda")
+    pi.pi_kv_rope_append(cache, batch, rope, torch.ones_like(out), x + 1, x + 1, dev([0, 1, 2]), out)
+    torch.cuda.synchronize()
+    assert bool((k == 1).all()) and bool((v == 1).all()) and bool((out == 7).all())
+
+
+def test_two_graphs_share_a_workspace():
+    """Verification and attention captured twice over the same workspaces, replayed in turn with eager calls between."""
+    announce("two graphs, one workspace")
+    cases = [verify_case(s, [3, 2, 1, 4] * 5, vocab) for s, vocab in ((1, 9000), (2, 40001))]
+    drafts = [pi.make_kv_drafts(dev(c[0]), dev(c[1]), c[2].cuda(), c[3].cuda(), dev(c[4], torch.float32), dev(c[5], torch.float32)) for c in cases]
+    vws = torch.zeros(max(pi.pi_kv_verify_workspace_bytes(d) for d in drafts), dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros((2, 20), dtype=torch.int32, device="cuda") for _ in cases]
+    attn = []
+    for seed, lens in ((1, [(5, 9000), (1, 4000)]), (2, [(1, 20000), (2, 9000)])):
+        c = kv_util.attn_case(seed, lens, 16, 2, 64, 16, "f16")
+        batch = pi.make_kv_batch(dev(c["table"]), dev(c["starts"]), dev(c["kv"]), max_q=5, max_kv=20000)
+        attn.append((pi.make_kv_cache(c["k"].cuda(), c["v"].cuda()), batch, c["q"].cuda(), torch.zeros_like(c["q"], device="cuda")))
+    args = dict(window=5000, sinks=70)
+    ws = torch.empty(max(pi.pi_kv_attn_sinks_workspace_bytes(a[0], a[1], len(a[2]), 16, *args.values()) for a in attn), dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 1 << 16               # key ranges are cut: partial sums pass through it
+
+    def call(i):
+        pi.pi_kv_verify(drafts[i], outs[i][0], outs[i][1], vws)
+        pi.pi_kv_attn_sinks(*attn[i], ws, scale=0.125, **args)
+    want = []
+    for i in (0, 1):
+        call(i)
+        torch.cuda.synchronize()
+        want.append((outs[i].clone(), attn[i][3].clone()))
+        assert want[i][0].tolist() == [list(x) for x in U.verify_reference(*cases[i])[:2]]
+    graphs = [torch.cuda.CUDAGraph() for _ in (0, 1)]
+    for i, g in enumerate(graphs):
+        with torch.cuda.graph(g):
+            call(i)
+    for it in range(6):
+        for i in (it % 2, 1 - it % 2):
+            outs[i].zero_()
+            attn[i][3].zero_()
+            graphs[i].replay()
+            call(1 - i)
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            assert torch.equal(outs[i], want[i][0]) and torch.equal(attn[i][3], want[i][1]), (it, i)
+
+
+def test_release_of_long_lists_in_a_replayed_graph():
+    announce("release in a graph")
+    states = [U.pages_state(s, 700, 16, 70) for s in range(4)]
+    n_pages = max(len(s["ring"]) for s in states) + 5
+    for s in states:                          # one size of pool for all
+        extra = list(range(len(s["ring"]), n_pages))
+        head, count = s["pool"]
+        old = s["ring"]
+        s["ring"] = [old[(head + i) % len(old)] for i in range(count)] + extra + [-1] * (len(old) - count)
+        s["pool"], s["shares"] = [0, count + len(extra)], s["shares"] + [0] * len(extra)
+    d = device_state(states[0], True)
+    at, to, copies = (torch.zeros(x, dtype=torch.int32, device="cuda") for x in ((700,), (700,), (700, 2)))
+    d["copies"] = copies
+
+    def put(s, r):
+        for name, value in (("cached", s["cached"]), ("free_ring", s["ring"]), ("pool", s["pool"]), ("block_table", s["table"]), ("shares", s["shares"])):
+            d[name].copy_(dev(value))
+        at.copy_(dev(r[0]))
+        to.copy_(dev(r[1]))
+    put(states[0], U.release_ranges(0, states[0]))
+    pi.pi_kv_release(d["pages"], at, to, copies)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pi.pi_kv_release(d["pages"], at, to, copies)
+    for it in range(8):
+        s = states[it % 4]
+        # lists of all lengths: everything at once, the usual ranges, and a token each
+        r = (U.release_ranges(it, s), ([0] * 700, [U.ALL] * 700), ([max(c - 1, 0) for c in s["cached"]], [U.ALL] * 700))[it % 3]
+        put(s, r)
+        graph.replay()
+        check_state(d, U.release_reference(s, *r))
+
+
 def test_host_tensors_are_refused():
     host, gpu = torch.zeros(3, dtype=torch.int32), torch.zeros(3, dtype=torch.int32, device="cuda")
     st = U.pages_state(1, 3, 16, 4)
