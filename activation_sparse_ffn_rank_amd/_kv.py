@@ -336,15 +336,25 @@ def pi_kv_rope_append(cache: pi_kv_cache, batch: pi_kv_batch, rope: pi_kv_rope, 
     """k (normed, rotated) and v [total_q][n_kv][head_dim] into slots [total_q], and q [total_q][n_q][head_dim] (normed,
     rotated) to q_out, which may be q.  Positions follow from the batch."""
     fn = "pi_kv_rope_append"
-    qp, qt, qh, n, heads = _rows(fn, q, cache)
-    kp, kt, kh, n_k, heads_k = _rows(fn, k, cache)
-    vp, vt, vh, n_v, heads_v = _rows(fn, v, cache)
-    op, ot, oh, n_o, heads_o = (qp, qt, qh, n, heads) if q_out is q else _rows(fn, q_out, cache)
-    if not n == n_k == n_v == n_o or heads_o != heads or not heads_k == heads_v == cache.n_kv or n >= 2 ** 31 or heads >= 2 ** 31:
+    if q is None or k is None or v is None or q_out is None:
+        raise PiError(fn, PI_ERR_NULL)
+    dt = q.dtype
+    if KV_DTYPES.get(dt) != cache.dtype or k.dtype != dt or v.dtype != dt or q_out.dtype != dt:
+        raise PiError(fn, PI_ERR_DTYPE)
+    shape, shape_k, width = q.shape, k.shape, cache.head_dim
+    if len(shape) != 3 or len(shape_k) != 3 or v.shape != shape_k or q_out.shape != shape:
         raise PiError(fn, PI_ERR_SHAPE)
+    n, heads, hd = shape
+    if shape_k != (n, cache.n_kv, hd) or hd != width or n >= 2 ** 31 or heads >= 2 ** 31:
+        raise PiError(fn, PI_ERR_SHAPE)
+    (qt, qh, q1), (kt, kh, k1), (vt, vh, v1), (ot, oh, o1) = q.stride(), k.stride(), v.stride(), q_out.stride()
+    if not q1 == k1 == v1 == o1 == 1:
+        raise PiError(fn, PI_ERR_SHAPE)
+    if n <= 1 or heads <= 1 or shape_k[1] <= 1:              # the stride along an axis of one element is never used
+        (_, qt, qh, _, _), (_, kt, kh, _, _), (_, vt, vh, _, _), (_, ot, oh, _, _) = (_rows(fn, t, cache) for t in (q, k, v, q_out))
     weights = rope._weights
-    if weights is not None and weights != (q.dtype, cache.head_dim):
-        raise PiError(fn, PI_ERR_DTYPE if weights[0] != q.dtype else PI_ERR_SHAPE)
+    if weights is not None and weights != (dt, width):
+        raise PiError(fn, PI_ERR_DTYPE if weights[0] != dt else PI_ERR_SHAPE)
     at, device, on = _ints(fn, slots, n), cache._device, rope._device
     if not (q.get_device() == k.get_device() == v.get_device() == q_out.get_device() == slots.get_device() == batch._device == device
             and (on is None or on == device)):
@@ -353,7 +363,8 @@ def pi_kv_rope_append(cache: pi_kv_cache, batch: pi_kv_batch, rope: pi_kv_rope, 
     if _current_device() != device:
         with torch.cuda.device(device):
             return pi_kv_rope_append(cache, batch, rope, q, k, v, slots, q_out, stream)
-    rc = (_kv_lib or kv_lib()).pi_kv_rope_append(cache, batch, rope, qp, qt, qh, kp, kt, kh, vp, vt, vh, at, op, ot, oh, n, heads, stream)
+    rc = (_kv_lib or kv_lib()).pi_kv_rope_append(cache, batch, rope, q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+                                                 at, q_out.data_ptr(), ot, oh, n, heads, stream)
     if rc != PI_OK:
         raise PiError(fn, rc)
 

@@ -313,7 +313,7 @@ struct KvReq {
     int q0, n, m;          // first packed row, new tokens, keys
     int rows;              // query rows per kv head
     int lo, hi;            // keys that any of its rows may see
-    int first;             // SINKS: and the keys [0, first) before lo, whole blocks of 64; 0: lo is 0 or there are none
+    int first;             // SINKS: and the keys [0, first) before lo, whole blocks; 0: lo is 0 or there are none
     __device__ __forceinline__ int keys() const { return first + hi - lo; }
 };
 
@@ -322,9 +322,17 @@ struct KvReq {
 // nothing between them is read and no block holds keys of both.  Single tokens of 16 requests, 4 first keys and a window of 4096,
 // 32 heads of 128, 1.07 GB: 185 us (5.8 TB/s); a chunk of 4096 tokens, 64 and 2048, the same heads: 178 to 185 us, 780 TFLOP/s of
 // products that count, at 36 blocks a tile of which five are masked.
-__device__ __forceinline__ int kv_first_blocks(const KvAttnArgs &a, int hi) { return (min(a.sinks, hi) + 63) & ~63; }
+// Blocks of the first keys: 32 for kernels of 16-row tiles (4 first keys and a window of 500: one request of 16 heads of 64 8.3 us
+// with 64 and 7.8 with 32, 64 requests of 32 heads of 128 111.6 and 110.7), 64 for wide ones.
+constexpr int kKvRowTile = 16;          // query rows of a k_kv_rows workgroup
+constexpr int kKvWideTile = 128;        // ... and of a k_kv_tile workgroup
+template <int TR>
+__device__ __forceinline__ int kv_first_blocks(const KvAttnArgs &a, int hi) {
+    constexpr int kBlock = TR == kKvRowTile ? 32 : 64;
+    return (min(a.sinks, hi) + kBlock - 1) & ~(kBlock - 1);
+}
 
-template <bool SINKS>
+template <int TR, bool SINKS>
 __device__ __forceinline__ KvReq kv_req(const KvAttnArgs &a, int r) {
     KvReq x;
     const int q0 = a.q_start[r], q1 = a.q_start[r + 1];
@@ -337,7 +345,7 @@ __device__ __forceinline__ KvReq kv_req(const KvAttnArgs &a, int r) {
     x.lo = a.window ? min(max(x.m - x.n - a.window + 1, 0), x.hi) & ~63 : 0;
     x.first = 0;
     if constexpr (SINKS) {
-        x.first = kv_first_blocks(a, x.hi);
+        x.first = kv_first_blocks<TR>(a, x.hi);
         if (x.first >= x.lo) x.lo = x.first = 0;
     }
     return x;
@@ -350,14 +358,14 @@ struct KvSpan {
     int a0, a1, lo, hi;
     __device__ __forceinline__ int after(int kb, int step) const { return kb + step == a1 ? lo : kb + step; }
 };
-template <bool SINKS, int KT>
+template <int TR, bool SINKS, int KT>
 __device__ __forceinline__ KvSpan kv_span(const KvAttnArgs &a, const KvReq &q, int tile_lo, int tile_hi, int splits, int split,
                                           int piece) {
     KvSpan x;
     x.a0 = x.a1 = -1;
     x.lo = max(tile_lo & ~(KT - 1), q.lo), x.hi = tile_hi;
     if constexpr (SINKS) {
-        const int past = q.lo - q.first, first = kv_first_blocks(a, q.hi);    // key = place on the axis + past, in [lo, hi)
+        const int past = q.lo - q.first, first = kv_first_blocks<TR>(a, q.hi);    // key = place on the axis + past, in [lo, hi)
         const bool apart = x.lo - past > first && tile_hi > 0;
         if (apart) x.a0 = 0, x.a1 = first;
         else x.lo = q.first ? q.lo : 0;
@@ -379,8 +387,6 @@ __device__ __forceinline__ KvSpan kv_span(const KvAttnArgs &a, const KvReq &q, i
     return x;
 }
 
-constexpr int kKvRowTile = 16;          // query rows of a k_kv_rows workgroup
-constexpr int kKvWideTile = 128;        // ... and of a k_kv_tile workgroup
 constexpr int kKvMinPiece = 256;        // keys of a piece, about, at least
 // Ranges of fewer keys (256 KB of keys and values) are not cut: one workgroup reads them at about 50 GB/s, and a
 // join costs 5 to 7 us (16 x 100..500 keys, 32 heads of 128: 29.3 us cut from 512 on in pieces of 256, 20.5 uncut).
@@ -405,7 +411,7 @@ __device__ __forceinline__ KvCut kv_cut(const KvAttnArgs &a, int lane) {
     for (int r0 = 0; r0 < a.n_req; r0 += 64) {
         float x = 0.f, y = 0.f;
         if (r0 + lane < a.n_req) {
-            const KvReq q = kv_req<SINKS>(a, r0 + lane);
+            const KvReq q = kv_req<TR, SINKS>(a, r0 + lane);
             x = (float)((q.rows + TR - 1) / TR) * (float)q.keys();
             y = q.keys() >= kv_min_cut(HD) ? (float)q.rows : 0.f;
         }
@@ -448,7 +454,7 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs &a, int want, KvCut a
         KvReq q{};
         int tiles = 0, splits = 1, piece = 1;
         if (r0 + lane < a.n_req) {
-            q = kv_req<SINKS>(a, r0 + lane);
+            q = kv_req<TR, SINKS>(a, r0 + lane);
             tiles = (q.rows + TR - 1) / TR;
             piece = kv_piece<HD, TR>(q.keys(), aim);
             splits = max((q.keys() + piece - 1) / piece, 1);
@@ -550,12 +556,12 @@ __device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &
     const int tile_hi = min(pos_b + 1, rq.hi), tile_lo = a.window ? max(pos_a - a.window + 1, 0) : 0;
     // every row of the tile sees keys in [all_lo, all_hi)
     const int all_hi = min(pos_a + 1, rq.hi), all_lo = a.window ? max(pos_b - a.window + 1, 0) : 0;
-    const KvSpan sp = kv_span<SINKS, 32>(a, rq, tile_lo, tile_hi, it.splits, it.split, it.piece);
+    const KvSpan sp = kv_span<TR, SINKS, 32>(a, rq, tile_lo, tile_hi, it.splits, it.split, it.piece);
     // this wave's part
     const int before = SINKS && sp.a1 >= 0 ? sp.a1 - sp.a0 : 0, all = before + sp.hi - sp.lo;
     const int part = max((((all + kWaves - 1) / kWaves) + 31) & ~31, 32);
     int k_lo = sp.lo + wave * part, k_hi = min(k_lo + part, sp.hi);
-    if constexpr (SINKS) {               // (whole blocks of 64 keys are before)
+    if constexpr (SINKS) {               // (whole blocks are before)
         const int from = wave * part, to = min(from + part, all);
         k_lo = from < before ? sp.a0 + from : sp.lo + from - before;
         k_hi = to <= before ? sp.a0 + to : sp.lo + to - before;
@@ -895,7 +901,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
     // keys that some row of the workgroup sees, within the item's chunk
     const int pos_first = past + tile * kKvWideTile / a.group;
     const int pos_last = past + (min((tile + 1) * kKvWideTile, rq.rows) - 1) / a.group;
-    const KvSpan sp = kv_span<SINKS, KT>(a, rq, a.window ? max(pos_first - a.window + 1, 0) : 0, min(pos_last + 1, rq.hi), it.splits,
+    const KvSpan sp = kv_span<kKvWideTile, SINKS, KT>(a, rq, a.window ? max(pos_first - a.window + 1, 0) : 0, min(pos_last + 1, rq.hi), it.splits,
                                          it.split, it.piece);
     const int lo = SINKS && sp.a1 >= 0 ? sp.a0 : sp.lo, hi = sp.hi, sinks = SINKS ? a.sinks : 0;
     // keys that some row of this wave sees, and those that all of them see
