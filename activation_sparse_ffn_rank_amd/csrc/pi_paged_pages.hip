@@ -18,13 +18,18 @@ int check_pages(const pi_kv_pages *p) {
     return PI_OK;
 }
 
-// Entries of all requests at most beyond which the list may be long: the launches for that follow.
-constexpr int64_t kShortTables = 32768;
-bool long_lists(const pi_kv_pages *p) { return (int64_t)p->n_req * p->max_pages > kShortTables; }
+// By the entries that all tables have together: up to the first number a workgroup of few threads where requests are few, for its
+// barriers' sake; up to the second one of many, as a list of thousands may come; past it, launches over the whole chip for long
+// lists follow, which cost where there is none.  64 requests of 1024 pages, one workgroup and with the launches: 6.5 us and 11.2
+// where a step gives nothing up, 18 and 26 where four requests end, 56 and 28 where sixteen do.  A list of 400 entries with 256
+// threads 5.0 us, with 1024 6.5; one of 4096 46 and 18.
+constexpr int64_t kFewEntries = 32768, kManyEntries = 131072;
+int64_t entries_of(const pi_kv_pages *p) { return (int64_t)p->n_req * p->max_pages; }
+bool long_lists(const pi_kv_pages *p) { return entries_of(p) > kManyEntries; }
 
 size_t bytes_of(const pi_kv_pages *p) { return long_lists(p) ? KvReleaseWs::kInts * sizeof(int32_t) : 16; }
 
-// Threads of a workgroup that holds four requests or forks each at most: few where there are few, for the barriers' sake.
+// Threads of a workgroup that holds four requests or forks each at most.
 int threads_for(int n) { return n <= 256 ? 256 : kKvTableThreads; }
 
 KvPagesArgs args_of(const pi_kv_pages *p) {
@@ -45,7 +50,8 @@ extern "C" int pi_kv_release(const pi_kv_pages *pages, const int32_t *drop_from,
     const bool more = long_lists(pages);
     const KvReleaseArgs a{args_of(pages), drop_from, drop_to, copies, more ? static_cast<int32_t *>(pages->ws) : nullptr};
     hipStream_t st = static_cast<hipStream_t>(stream);
-    hipLaunchKernelGGL(k_kv_release, dim3(1), dim3(threads_for(pages->n_req)), 0, st, a);
+    const int threads = entries_of(pages) <= kFewEntries ? threads_for(pages->n_req) : kKvTableThreads;
+    hipLaunchKernelGGL(k_kv_release, dim3(1), dim3(threads), 0, st, a);
     if (more) {
         hipLaunchKernelGGL(k_kv_release_pass<0>, dim3(kKvReleaseGroups), dim3(256), 0, st, a);
         hipLaunchKernelGGL(k_kv_release_pass<1>, dim3(kKvReleaseGroups), dim3(256), 0, st, a);

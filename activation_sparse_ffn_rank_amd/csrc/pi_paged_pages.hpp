@@ -51,8 +51,6 @@ __device__ __forceinline__ int kv_owner_of(const uint32_t *first, int n, uint32_
 constexpr int kKvMiddle = INT32_MIN;       // flag of a first column: the entries become -1
 constexpr int kKvEach = 4;                 // entries per thread and round
 constexpr int kKvReleaseGroups = 256;      // workgroups of a long list
-// Lists longer than this many entries per thread of the first workgroup go on to the launches behind it.
-constexpr int kKvShortList = 8;
 
 // What the first launch leaves for the ones behind it: ints at these places.
 struct KvReleaseWs {
@@ -102,15 +100,24 @@ __device__ __forceinline__ void kv_walk(const KvPagesArgs &a, const uint32_t *fi
 }
 
 // The three passes over the entries, for a range [from, to) of them in rounds of a workgroup:
-//  1. one owner less for each (whole numbers: any order gives the same); returns this thread's number of valid ones,
+//  1. one owner less for each (whole numbers: any order gives the same); returns this thread's number of valid ones, and, in one
+//     workgroup, clears `plain` if a page had further owners or was named before: if its count was not 0 (over many workgroups
+//     the counts' way back and a word for all cost 3 us, as much as the pass that they save),
 template <bool MANY>
-__device__ __forceinline__ uint32_t kv_give(const KvPagesArgs &a, const uint32_t *first, const int *col, uint32_t from, uint32_t to) {
+__device__ __forceinline__ uint32_t kv_give(const KvPagesArgs &a, const uint32_t *first, const int *col, uint32_t from, uint32_t to,
+                                            bool &plain) {
     uint32_t given = 0;
-    for (uint32_t e = from + threadIdx.x * kKvEach; e < to; e += blockDim.x * kKvEach)
-        kv_walk(a, first, col, to, e, [&](int, uint32_t, int *, int p, bool) {
-            KvShares<MANY>::less(a.shares + p);
+    for (uint32_t e = from + threadIdx.x * kKvEach; e < to; e += blockDim.x * kKvEach) {
+        int before[kKvEach] = {};
+        kv_walk(a, first, col, to, e, [&](int i, uint32_t, int *, int p, bool) {
+            before[i] = KvShares<MANY>::less(a.shares + p);
             ++given;
         });
+        if constexpr (!MANY) {
+#pragma unroll
+            for (int i = 0; i < kKvEach; ++i) plain = plain && before[i] == 0;
+        }
+    }
     return given;
 }
 //  2. of the pages that have run out of owners the first entry that names it, as the minimum over INT32_MIN + entry,
@@ -121,10 +128,11 @@ __device__ __forceinline__ void kv_lead(const KvPagesArgs &a, const uint32_t *fi
             if (KvShares<MANY>::load(a.shares + p) < 0) KvShares<MANY>::lower(a.shares + p, INT32_MIN + (int)e);
         });
 }
-//  3. the pages of those entries behind the free ones, from place `at` of the ring on; returns how many.
+//  3. the pages of those entries behind the free ones, from place `at` of the ring on; returns how many.  plain: every page was
+//     named once and had no further owners, so all of them.
 template <bool MANY>
 __device__ __forceinline__ uint32_t kv_push(const KvPagesArgs &a, const uint32_t *first, const int *col, uint32_t from, uint32_t to,
-                                            int64_t at, uint32_t *part) {
+                                            int64_t at, uint32_t *part, bool plain) {
     uint32_t back = 0;
     for (uint32_t base = from; base < to; base += blockDim.x * kKvEach) {
         int won[kKvEach];
@@ -132,7 +140,7 @@ __device__ __forceinline__ uint32_t kv_push(const KvPagesArgs &a, const uint32_t
 #pragma unroll
         for (int i = 0; i < kKvEach; ++i) won[i] = -1;
         kv_walk(a, first, col, to, base + threadIdx.x * kKvEach, [&](int i, uint32_t e, int *place, int p, bool middle) {
-            if (KvShares<MANY>::load(a.shares + p) == INT32_MIN + (int)e) won[i] = p, ++wins;
+            if (plain || KvShares<MANY>::load(a.shares + p) == INT32_MIN + (int)e) won[i] = p, ++wins;
             if (middle) *place = -1;
         });
         uint32_t all;
@@ -305,7 +313,8 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_release(KvRelease
         return;
     }
     uint32_t at = kv_block_scan(entries, s_part, &total);       // (its barriers order s_col and the reads of the ring, too)
-    const bool go_on = x.ws && total > blockDim.x * kKvShortList;
+    // More than one round goes on to the launches behind, where there are any: 4100 entries 27 us, in two rounds here 29.
+    const bool go_on = x.ws && total > blockDim.x * kKvEach;
 #pragma unroll
     for (int k = 0; k < kKvReqPerThread; ++k) {
         const int r = tid * per + k;
@@ -336,14 +345,17 @@ static __global__ __launch_bounds__(kKvTableThreads) void k_kv_release(KvRelease
         back = kv_one_round(a, kv_entries(a, s_first, s_col, total, tid * kKvEach), (int64_t)head + count, s_part, given);
         __syncthreads();
     } else if (total) {
-        const uint32_t mine = kv_give<false>(a, s_first, s_col, 0, total);
+        bool plain = true;
+        const uint32_t mine = kv_give<false>(a, s_first, s_col, 0, total, plain);
         kv_block_scan(mine, s_part, &given);
         kv_lds_wait();
-        __syncthreads();
-        kv_lead<false>(a, s_first, s_col, 0, total);
-        kv_lds_wait();
-        __syncthreads();
-        back = kv_push<false>(a, s_first, s_col, 0, total, (int64_t)head + count, s_part);
+        plain = __syncthreads_and(plain);
+        if (!plain) {
+            kv_lead<false>(a, s_first, s_col, 0, total);
+            kv_lds_wait();
+            __syncthreads();
+        }
+        back = kv_push<false>(a, s_first, s_col, 0, total, (int64_t)head + count, s_part, plain);
         __syncthreads();
     }
 #pragma unroll
@@ -379,7 +391,8 @@ __global__ __launch_bounds__(256) void k_kv_release_pass(KvReleaseArgs x) {
     const uint32_t from = min(b * share, total), to = min(from + share, total);
     __syncthreads();
     if constexpr (PASS == 0) {
-        const uint32_t given = kv_give<true>(a, s_first, s_col, from, to);
+        bool plain = false;
+        const uint32_t given = kv_give<true>(a, s_first, s_col, from, to, plain);
         uint32_t all;
         kv_block_scan(given, s_part, &all);
         if (tid == 0 && all) atomicAdd(x.ws + KvReleaseWs::kGiven, (int)all);
@@ -400,7 +413,7 @@ __global__ __launch_bounds__(256) void k_kv_release_pass(KvReleaseArgs x) {
         before = s_part[0];
         __syncthreads();
         const int head = x.ws[KvReleaseWs::kHead], count = x.ws[KvReleaseWs::kCount];
-        kv_push<true>(a, s_first, s_col, from, to, (int64_t)head + count + before, s_part);
+        kv_push<true>(a, s_first, s_col, from, to, (int64_t)head + count + before, s_part, false);
         __syncthreads();
         // pages in the place of those that were cut inside of: by the workgroup whose entries begin with them
         for (int r = tid; r < a.n_req; r += 256) {

@@ -583,7 +583,7 @@ def check_state(d, want):
     assert bool((d["wide"][:, d["wide"].shape[1] - d["slack"]:] == -7).all())
 
 
-PAGE_CASES = [(1, 16, 1), (1, 256, 5), (9, 16, 6), (64, 32, 40), (200, 16, 9), (1025, 64, 4), (1500, 16, 30), (2000, 32, 64), (4096, 16, 5), (4096, 16, 9)]
+PAGE_CASES = [(1, 16, 1), (1, 256, 5), (9, 16, 6), (64, 32, 40), (200, 16, 9), (1025, 64, 4), (1500, 16, 30), (2000, 32, 64), (4096, 16, 5), (4096, 16, 9), (3000, 16, 100)]
 
 
 @pytest.mark.parametrize("in_place", (False, True))
@@ -915,9 +915,10 @@ def test_two_graphs_share_a_workspace():
             assert torch.equal(outs[i], want[i][0]) and torch.equal(attn[i][3], want[i][1]), (it, i)
 
 
-def test_release_of_long_lists_in_a_replayed_graph():
-    announce("release in a graph")
-    states = [U.pages_state(s, 700, 16, 70) for s in range(4)]
+@pytest.mark.parametrize("n", (700, 4000))          # in one launch, and in several
+def test_release_of_long_lists_in_a_replayed_graph(n):
+    announce(f"release in a graph, n={n}")
+    states = [U.pages_state(s, n, 16, 70, forks=0.0 if s == 2 else 0.4) for s in range(4)]
     n_pages = max(len(s["ring"]) for s in states) + 5
     for s in states:                          # one size of pool for all
         extra = list(range(len(s["ring"]), n_pages))
@@ -926,7 +927,7 @@ def test_release_of_long_lists_in_a_replayed_graph():
         s["ring"] = [old[(head + i) % len(old)] for i in range(count)] + extra + [-1] * (len(old) - count)
         s["pool"], s["shares"] = [0, count + len(extra)], s["shares"] + [0] * len(extra)
     d = device_state(states[0], True)
-    at, to, copies = (torch.zeros(x, dtype=torch.int32, device="cuda") for x in ((700,), (700,), (700, 2)))
+    at, to, copies = (torch.zeros(x, dtype=torch.int32, device="cuda") for x in ((n,), (n,), (n, 2)))
     d["copies"] = copies
 
     def put(s, r):
@@ -943,7 +944,7 @@ def test_release_of_long_lists_in_a_replayed_graph():
     for it in range(8):
         s = states[it % 4]
         # lists of all lengths: everything at once, the usual ranges, and a token each
-        r = (U.release_ranges(it, s), ([0] * 700, [U.ALL] * 700), ([max(c - 1, 0) for c in s["cached"]], [U.ALL] * 700))[it % 3]
+        r = (U.release_ranges(it, s), ([0] * n, [U.ALL] * n), ([max(c - 1, 0) for c in s["cached"]], [U.ALL] * n))[it % 3]
         put(s, r)
         graph.replay()
         check_state(d, U.release_reference(s, *r))
