@@ -68,6 +68,19 @@ __device__ __forceinline__ float kv_lane_sum(float x) {
     return x;
 }
 
+// Whether row t lies in a range that leaves the rows, and so in no request (q_start does not decrease; first and last entry: those of
+// q_start).  Not looked for where there is none.
+__device__ __forceinline__ bool kv_cut_range(const KvRopeArgs &a, int t, int first, int last) {
+    if (first >= 0 && last <= a.total_q) return false;
+    int lo = 0, hi = a.n_req;                        // the last range that begins at t or before
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.q_start[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    return a.q_start[lo] < 0 || a.q_start[lo + 1] > a.total_q;
+}
+
 // TT tokens of one kv head's values, transposed through LDS as k_kv_append does.
 template <int HD, int TT>
 __device__ __forceinline__ void kv_values(const KvRopeArgs &a, uint32_t *s_v) {
@@ -85,7 +98,7 @@ __device__ __forceinline__ void kv_values(const KvRopeArgs &a, uint32_t *s_v) {
         d[0] = x.x, d[1] = x.y, d[2] = x.z, d[3] = x.w;
     }
     __syncthreads();
-    if (slot >= (uint32_t)a.n_slots || t0 + t < first || t0 + t >= end) return;
+    if (slot >= (uint32_t)a.n_slots || t0 + t < first || t0 + t >= end || kv_cut_range(a, t0 + t, first, end)) return;
     const int64_t pg = slot >> a.page_log, off = slot & ((1u << a.page_log) - 1);
     uint16_t *const vp = a.v_pages + (((pg * a.n_kv + h) * HD) << a.page_log) + off;
     for (int d = tid / TT; d < HD / 2; d += 256 / TT) {

@@ -174,6 +174,26 @@ def test_rope_append_row_ranges_out_of_bounds():
     assert torch.equal(c["qkv"][:, :4], want)
 
 
+@pytest.mark.parametrize("heads,hd", [((4, 2), 64), ((80, 80), 128)])      # values in tiles of 16 tokens and of 64
+def test_rope_append_leaves_keys_and_values_of_cut_ranges_alone(heads, hd):
+    """A range that leaves the rows belongs to no request: neither keys nor values of its rows are appended."""
+    announce(f"rope append cut ranges {heads}")
+    n = 120
+    c = rope_case(4, [(n, n), (n, 2 * n), (n, 300)], *heads, hd, 64, "f16", hd, 0, False, pad=4 if hd == 64 else 64)
+    n_q, n_kv = heads
+    for starts in ([-4, n, 2 * n, 3 * n], [-9, -4, n, 2 * n], [0, n, 2 * n, 3 * n + 99], [0, n, 3 * n + 99, 3 * n + 99], [-1, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1],
+                   [-2 ** 31, n, n, n], [0, 7, 7, 9]):
+        got = run_rope(c, starts=starts)
+        k_kept, v_kept = torch.ones(c["k"].shape[0], c["page"], dtype=torch.bool), c["v"].clone()
+        for t, slot in enumerate(c["slots"]):
+            if any(0 <= a <= t < b <= c["rows"] for a, b in zip(starts, starts[1:])) and 0 <= slot < k_kept.numel():
+                k_kept[slot // c["page"], slot % c["page"]] = False
+                v_kept[slot // c["page"], :, :, slot % c["page"]] = c["qkv"][t, n_q + n_kv:]
+        assert torch.equal(got[2].view(torch.int16), v_kept.view(torch.int16)), ("values", starts)
+        same = (got[1].view(torch.int16) == c["k"].view(torch.int16)).all(-1).all(1)
+        assert torch.equal(same, k_kept), ("keys", starts)
+
+
 @pytest.mark.parametrize("bad", (math.nan, math.inf, -math.inf))
 def test_rope_append_keeps_bad_numbers_in_their_head(bad):
     announce(f"rope append {bad}")
