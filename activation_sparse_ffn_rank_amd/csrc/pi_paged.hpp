@@ -901,8 +901,8 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 128 ? 2 : 3) void k_kv_t
     // keys that some row of the workgroup sees, within the item's chunk
     const int pos_first = past + tile * kKvWideTile / a.group;
     const int pos_last = past + (min((tile + 1) * kKvWideTile, rq.rows) - 1) / a.group;
-    const KvSpan sp = kv_span<kKvWideTile, SINKS, KT>(a, rq, a.window ? max(pos_first - a.window + 1, 0) : 0, min(pos_last + 1, rq.hi), it.splits,
-                                         it.split, it.piece);
+    const KvSpan sp = kv_span<kKvWideTile, SINKS, KT>(a, rq, a.window ? max(pos_first - a.window + 1, 0) : 0,
+                                                      min(pos_last + 1, rq.hi), it.splits, it.split, it.piece);
     const int lo = SINKS && sp.a1 >= 0 ? sp.a0 : sp.lo, hi = sp.hi, sinks = SINKS ? a.sinks : 0;
     // keys that some row of this wave sees, and those that all of them see
     const int wrow = tile * kKvWideTile + wave * 32;

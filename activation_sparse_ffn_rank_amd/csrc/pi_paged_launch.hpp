@@ -68,7 +68,8 @@ inline AttnPlan attn_plan(const pi_kv_cache *c, const pi_kv_batch *b, int total_
     const bool whole = reqs == 1 && 4 * target < 7 * all;
     // Ranges of one length need no evening out: with as many as the chip holds they are read whole, and no join follows (16 x
     // 4100 of 8 to 30 thousand keys, 32 heads of 128: 195 us in halves).
-    if (!p.shorts && !p.single && !whole && !(even && all >= split_target(c->head_dim)) && all < 8 * target && max_kv >= kv_min_cut(c->head_dim)) {
+    const bool full = even && all >= split_target(c->head_dim);
+    if (!p.shorts && !p.single && !whole && !full && all < 8 * target && max_kv >= kv_min_cut(c->head_dim)) {
         p.target = target;
         p.items += target / c->n_kv + 2;             // 2: the device sums the work in fp32
         p.slots = std::min(p.items, 2 * target / c->n_kv + 4);

@@ -42,5 +42,6 @@ extern "C" int pi_kv_attn_sinks(const pi_kv_cache *cache, const pi_kv_batch *bat
     if (!q || !out) return PI_ERR_NULL;
     if (!(scale > 0.f) || !std::isfinite(scale)) return PI_ERR_SHAPE;
     return run_attn<true>(cache, batch, q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, total_q, n_q,
-                          scale, window, sinks, most_keys(batch, window, sinks), even_ranges(batch, window, sinks), ws, ws_bytes, static_cast<hipStream_t>(stream));
+                          scale, window, sinks, most_keys(batch, window, sinks), even_ranges(batch, window, sinks), ws, ws_bytes,
+                          static_cast<hipStream_t>(stream));
 }
