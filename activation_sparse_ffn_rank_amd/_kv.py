@@ -456,7 +456,7 @@ def pi_kv_verify_workspace_bytes(drafts: pi_kv_drafts) -> int:
 def pi_kv_verify(drafts: pi_kv_drafts, accepted: torch.Tensor, next: torch.Tensor, ws: torch.Tensor, *,
                  kv_len: torch.Tensor | None = None, keep: torch.Tensor | None = None, stream=None) -> None:
     """accepted [n_req] drafts of each request, the next token [n_req] behind them, and with kv_len the positions that
-    stay, keep [n_req] (int32)."""
+    stay, keep [n_req] (int32; of a request that the step refused INT32_MAX, and its last token is the next one again)."""
     fn = "pi_kv_verify"
     n, device = drafts.n_req, drafts._device
     ap, np_ = _ints(fn, accepted, n), _ints(fn, next, n)

@@ -170,16 +170,22 @@ static __global__ __launch_bounds__(256) void k_kv_verify(KvVerifyArgs a) {
     __shared__ int s_found[2][8], s_end;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = blockIdx.y;
     const float u_next = a.u_next[r];
+    // Every workgroup has read this before the last one writes `keep`, which may lie in its place (tickets between).
+    const int keys = a.kv_len ? a.kv_len[r] : INT32_MAX;
     const KvVerdict v = kv_verdict(a, r, lane);
-    if (tid == 0 && blockIdx.x == 0) {
-        a.accepted[r] = v.accepted;
-        if (a.keep) a.keep[r] = a.kv_len[r] - max(v.rows - 1 - v.accepted, 0);
-        if (v.rows == 0) a.next[r] = -1;
+    if (v.rows == 0) {                     // (no tickets: this workgroup's lengths are its own)
+        if (tid == 0 && blockIdx.x == 0) {
+            a.accepted[r] = 0;
+            a.next[r] = -1;
+            if (a.keep) a.keep[r] = keys > 0 ? keys : INT32_MAX;
+        }
+        return;
     }
-    if (v.rows == 0) return;
+    // A step that refuses a request gives it no keys: its scores stand for nothing, and its cache has none of its rows.
+    const bool refused = keys < v.rows;
     KvWeights w = kv_weights_of(a, v, v.rejected);
     double *const sums = a.sums + (int64_t)r * a.pieces;
-    {
+    if (!refused) {
         const int from = (blockIdx.x * 4 + wave) * a.per_wave, to = min(from + a.per_wave, a.pieces);
         for (int i = from; i < to; ++i) {
             const double sum = kv_piece_sum(w, i, lane);
@@ -194,6 +200,12 @@ static __global__ __launch_bounds__(256) void k_kv_verify(KvVerifyArgs a) {
         if (!s_end) return;
         if (tid == 0) a.tickets[r] = 0;
     }
+    if (tid == 0) {
+        a.accepted[r] = refused ? 0 : v.accepted;
+        if (refused) a.next[r] = a.tokens[a.q_start[r]];
+        if (a.keep) a.keep[r] = refused ? INT32_MAX : keys - (v.rows - 1 - v.accepted);
+    }
+    if (refused) return;
     const int per = (a.pieces + 255) / 256, i0 = tid * per, i1 = min(i0 + per, a.pieces);
     double upto, total, one;               // one: of the thread's first piece, most often its only one
     for (bool again = false;; again = true) {

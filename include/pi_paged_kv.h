@@ -181,7 +181,12 @@ int pi_kv_attn_sinks(const pi_kv_cache *cache, const pi_kv_batch *batch, const v
  * at or above 1) it is the last one with a weight above 0.  tokens outside [0, vocab) are rejected, and have no part of w.
  * accepted [n_req] = a; next [n_req], -1 if all weights are 0 or the request has no rows (q_start negative,
  * decreasing or past `rows` included); keep [n_req], with kv_len the keys of the step's attention, = kv_len - (n - 1 - a), the
- * positions that stay (pi_kv_release's drop_from).  kv_len and keep: both or neither NULL, and keep may be kv_len. */
+ * positions that stay (pi_kv_release's drop_from).
+ * A request that pi_kv_step refused (kv_len 0, or fewer keys than rows) holds none of its rows, and attention gave them zeros:
+ * a = 0, next = its own last token tokens[q_start[r]], so that the next step asks for the same again (-1 if it has no rows), and
+ * keep = INT32_MAX, which as drop_from drops nothing; it is no length (those behind the step are pi_kv_release's
+ * cached_next).  Without kv_len such a request is taken for one that was served.
+ * kv_len and keep: both or neither NULL, and keep may be kv_len. */
 #define PI_KV_MAX_VOCAB (1 << 22)
 typedef struct pi_kv_drafts {
     int32_t n_req, rows, vocab;

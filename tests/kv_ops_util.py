@@ -78,7 +78,8 @@ def sinks_reference(c, window, sinks, rows=None):
 # ------------------------------------------------------------------------------ drafted tokens
 
 def verify_reference(starts, tokens, target, draft, u_accept, u_next, kv_len=None, rows=None):
-    """(accepted, next, keep) by the rules, one request after the other; lists, and CPU tensors [rows][vocab]."""
+    """(accepted, next, keep) by the rules, one request after the other; lists, and CPU tensors [rows][vocab].  A request
+    with fewer keys than rows, or none, was refused by its step: it keeps all that it holds (ALL)."""
     rows, vocab = len(tokens) if rows is None else rows, target.shape[1]
     accepted, nxt, keep = [], [], []
     for r in range(len(starts) - 1):
@@ -87,7 +88,12 @@ def verify_reference(starts, tokens, target, draft, u_accept, u_next, kv_len=Non
         if a < 0 or n <= 0 or b > rows:
             accepted.append(0)
             nxt.append(-1)
-            keep.append(None if kv_len is None else kv_len[r])
+            keep.append(None if kv_len is None else kv_len[r] if kv_len[r] > 0 else ALL)
+            continue
+        if kv_len is not None and kv_len[r] < n:
+            accepted.append(0)
+            nxt.append(tokens[a])
+            keep.append(ALL)
             continue
         i = 0
         while i < n - 1:

@@ -988,3 +988,98 @@ def test_host_tensors_are_refused():
     assert code(lambda: pi.pi_kv_rope_append(cache, batch, pi.make_kv_rope(freq), x, x, x, s, x.clone())) == _abi.PI_ERR_NULL
     assert code(lambda: pi.pi_kv_rope_append(cache, batch, pi.make_kv_rope(freq.cuda()), x, x.cpu(), x, s, x.clone())) == _abi.PI_ERR_NULL
     assert code(lambda: pi.make_kv_drafts(gpu, s, torch.zeros((2, 5), device="cuda"), None, torch.zeros(2), torch.zeros(2, device="cuda"))) == _abi.PI_ERR_NULL
+
+
+# ------------------------------------------------------------------------------ requests that a step refused
+
+@pytest.mark.parametrize("vocab", (61, 1024, 5000))          # in one workgroup of a request and in several
+@pytest.mark.parametrize("with_draft", (True, False))
+def test_verify_of_refused_requests(vocab, with_draft):
+    """Fewer keys than rows, or none: nothing is accepted, the last token is the next one again, and all positions stay."""
+    announce(f"verify refused vocab={vocab} draft={with_draft}")
+    counts = [3, 1, 0, 5, 2, 1, 0, 70, 4, 5]
+    kv = [0, 0, 0, 4, 2, -1, 9, 0, -2 ** 31, 5]
+    starts, tokens, target, draft, u, un = verify_case(vocab, counts, vocab)
+    u = [0.3 * x for x in u]
+    tokens[starts[1]] = -9                   # whatever token it was
+    got = run_verify(starts, tokens, target, draft if with_draft else None, u, un, kv)
+    assert got == U.verify_reference(starts, tokens, target, draft if with_draft else None, u, un, kv)
+    for r in (0, 1, 3, 5, 7, 8):
+        assert (got[0][r], got[1][r], got[2][r]) == (0, tokens[starts[r]], U.ALL), r
+    assert got[2][2] == U.ALL and got[1][2] == -1 and got[2][6] == 9 and got[2][9] == 5 - 4 + got[0][9]
+    # without lengths a refused request is one as any other
+    got = run_verify(starts, tokens, target, draft if with_draft else None, u, un)
+    assert got == U.verify_reference(starts, tokens, target, draft if with_draft else None, u, un)
+
+
+@pytest.mark.parametrize("page", (16, 32))
+def test_refused_requests_keep_their_cache_in_a_replayed_graph(page):
+    """Steps over a pool that runs out, eager and replayed: a request without pages for its tokens keeps its positions and
+    pages and asks again, and goes on once another one has ended."""
+    announce(f"refused requests page={page}")
+    n, drafts, max_pages = 6, 4, 12
+    rng = random.Random(page)
+    gen = torch.Generator().manual_seed(page)
+    a, b = (Drafting(n, drafts, page, max_pages, 19) for _ in range(2))
+    for st in (a, b):
+        st.fresh.fill_(1 + drafts)
+    saved = a.state()
+    a.step()
+    torch.cuda.synchronize()
+    for name, value in saved.items():
+        getattr(a, name).copy_(value)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.step()
+    waits, refused, again = [0] * n, 0, 0
+    for it in range(80):
+        u, un = torch.rand(a.rows, generator=gen).cuda() * 0.3, torch.rand(n, generator=gen).cuda()
+        for st in (a, b):
+            st.u.copy_(u)
+            st.un.copy_(un)
+        torch.cuda.synchronize()
+        before = a.state()
+        graph.replay()
+        b.step()
+        torch.cuda.synchronize()
+        x, y = a.state(), b.state()
+        for name in x:
+            assert torch.equal(x[name], y[name]), (it, name)
+        listed = lambda s, name: s[name].cpu().tolist()
+        # the chain by its references
+        step = kv_util.step_reference(listed(before, "cached"), [1 + drafts] * n, listed(before, "ring"), listed(before, "pool"),
+                                      listed(before, "table"), page, a.rows)
+        assert (listed(x, "kv_len"), listed(x, "q_start"), listed(x, "slots")) == (step["kv_len"], step["q_start"], step["slots"])
+        tokens = listed(x, "tokens")
+        want = U.verify_reference(step["q_start"], tokens, a.target.cpu(), a.draft.cpu(), u.cpu().tolist(), un.cpu().tolist(), step["kv_len"])
+        assert (listed(x, "accepted"), listed(x, "next"), listed(x, "keep")) == want
+        state = dict(cached=step["cached_next"], table=step["block_table"], ring=step["free_ring"], pool=step["pool_next"],
+                     shares=listed(before, "shares"), page=page)
+        after = U.release_reference(state, want[2], None)
+        for name, key in (("cached", "cached_next"), ("table", "block_table"), ("ring", "free_ring"), ("pool", "pool_next"), ("shares", "shares")):
+            assert listed(x, name) == after[key], (it, name)
+        U.check_owned(dict(cached=after["cached_next"], table=after["block_table"], ring=after["free_ring"], pool=after["pool_next"],
+                           shares=after["shares"], page=page))
+        for r in range(n):
+            if step["kv_len"][r]:
+                again += waits[r] > 0
+                waits[r] = 0
+                assert after["cached_next"][r] == int(before["cached"][r]) + 1 + want[0][r]
+                continue
+            refused += 1
+            waits[r] += 1
+            held = kv_util.ceil_div(int(before["cached"][r]), page)
+            assert after["cached_next"][r] == int(before["cached"][r]) and int(x["next"][r]) == int(before["next"][r])
+            assert torch.equal(x["table"][r, :held], before["table"][r, :held])
+            for t in ("k", "v"):
+                ids = before["table"][r, :held].long()
+                assert torch.equal(x[t][ids], before[t][ids])
+        if max(waits) > 2 or max(after["cached_next"]) > (max_pages - 2) * page:
+            # the longest of those that were served ends
+            long = max((r for r in range(n) if not waits[r]), key=lambda r: after["cached_next"][r], default=0)
+            for st in (a, b):
+                st.cut(long, int(st.cached[long]))
+                st.next[long] = rng.randrange(a.vocab) if st is a else a.next[long]
+            torch.cuda.synchronize()
+    assert refused >= 10 and again > 3       # (the pool ran out, and requests went on)
