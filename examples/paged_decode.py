@@ -107,8 +107,8 @@ class PagedStack:
                 b = min(FFN_TOKENS, rows - t)
                 pi.pi_ffn_layer(ffn.pred, ffn.ffn, h[t: t + b], b, p["y"][t: t + b], None, None, None, self.ffn_ws[b])
             x = x + p["y"]
-        if self.window:                # the next token sees the keys from kv_len - window + 1 on
-            torch.sub(self.kv_len, self.window - 1, out=self.drop_to)
+        if self.window:                # the next token sees the keys from kv_len - window + 1 on; a drop to kv_len would be a cut
+            torch.sub(self.kv_len, max(self.window - 1, 1), out=self.drop_to)
             pi.pi_kv_release(self.pages, self.drop_from, self.drop_to, self.copies)
         return x
 

@@ -240,6 +240,8 @@ size_t pi_kv_pages_workspace_bytes(const pi_kv_pages *pages);
  *    (pi_kv_copy makes the copy, before the next append), else {-1, -1}.  Such a request is refused, and nothing of it
  *    changes, if the free pages do not suffice; requests are served in order.
  *  - drop_to < cached drops from the middle: cached_next = cached, the dropped entries become -1 (pages without keys).
+ *    What a window has passed goes this way: drop_from = the first tokens that stay, drop_to = min(c - window + 1, c - 1) of a
+ *    request of c positions whose next token stands at position c, so that it ends below c with a window of one token too.
  * A page given up once more than it has further owners goes behind the free ones, in the order of first mention (requests in order,
  * a page given up for a copy before the later ones); entries outside [0, n_pages) are skipped.  cached outside [0, max_pages * page]
  * is refused.  counts = {entries given up, pages gone back, pages taken, requests refused}. */

@@ -1083,3 +1083,42 @@ def test_refused_requests_keep_their_cache_in_a_replayed_graph(page):
                 st.next[long] = rng.randrange(a.vocab) if st is a else a.next[long]
             torch.cuda.synchronize()
     assert refused >= 10 and again > 3       # (the pool ran out, and requests went on)
+
+
+@pytest.mark.parametrize("window", (1, 2))
+def test_example_streams_with_the_smallest_windows(window):
+    """A token that sees itself and the first tokens only, or one token more: requests keep their lengths, and
+    attention equals the reference."""
+    announce(f"paged decode example, window {window}")
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "paged_decode.py")
+    spec = importlib.util.spec_from_file_location("paged_decode_small_windows", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    cfg = synth.custom_config(1024, 2048, 64, layers=1, seed=3)
+    opts = dict(head_dim=64, kv_heads=4, rope=True, window=window, sinks=3)
+    lengths = [5, 70, 32, 1]
+    graph, eager, _ = example.generate(cfg, 1, lengths, 20, **opts)
+    assert torch.isfinite(eager).all() and torch.equal(graph, eager)
+    st = example.PagedStack(cfg, 1, len(lengths), 120, **opts)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    real, seen = example.pi.pi_kv_attn_sinks, []
+
+    def attn(cache, batch, q, out, ws, **kw):
+        real(cache, batch, q, out, ws, **kw)
+        seen.append((q.cpu(), out.cpu(), st.table.tolist(), st.q_start.tolist(), st.kv_len.tolist()))
+
+    example.pi.pi_kv_attn_sinks = attn
+    try:
+        for it in range(20):
+            fresh = lengths if it == 0 else [1] * len(lengths)
+            st.fresh.copy_(dev(fresh))
+            st.step(st.plan(sum(fresh), max(fresh), 120), torch.randn((sum(fresh), cfg.d), generator=gen, device="cuda"))
+            q, out, table, starts, kv = seen[-1]
+            assert kv == [m + it for m in lengths] and st.cached.tolist() == kv
+            k, v = (t.cpu() for t in st.caches[0]._keep)
+            want, mag = U.sinks_reference(dict(table=table, starts=starts, kv=kv, k=k, v=v, q=q, scale=1 / 8), window, 3)
+            assert bool(((out.double() - want).abs() <= kv_util.attn_tolerance(want, mag, torch.float16, 64, partial=16.0)).all())
+            U.check_owned(dict(cached=st.cached.tolist(), table=st.table.tolist(), ring=st.ring.tolist(), pool=st.pool.tolist(),
+                               shares=st.pages._keep[4].tolist(), page=st.page))
+    finally:
+        example.pi.pi_kv_attn_sinks = real
