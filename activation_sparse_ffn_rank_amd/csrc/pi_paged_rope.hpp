@@ -22,26 +22,66 @@ struct KvRopeArgs {
     uint16_t *q_out, *k_pages, *v_pages;
 };
 
-// Where packed row t stands (in: it belongs to a request).  q_start is searched 64 entries at a time, by all lanes of a wave.
+// q_start is searched 64 entries at a time, by all lanes of a wave: the number of starts at or before a row names its request.  For
+// a row's heads and for its values alike, so that with starts that decrease, where a search may miss a row's range, both
+// leave it out.  This lane's share of the first search: the start of every step-th request, with one request a lane its end and
+// keys, too.
+struct KvStarts {
+    int step, start, end, m;
+};
+__device__ __forceinline__ KvStarts kv_starts(const KvRopeArgs &a, int lane) {
+    const int step = (a.n_req + 63) / 64, at = lane * step;
+    const bool in = at < a.n_req, all = step == 1 && in;
+    return {step, in ? a.q_start[at] : INT32_MAX, all ? a.q_start[at + 1] : 0, all ? a.kv_len[at] : 0};
+}
+__device__ __forceinline__ int kv_starts_upto(int start, int t) { return __popcll(__ballot(start <= t)); }
+__device__ __forceinline__ bool kv_in_range(const KvRopeArgs &a, int t, int start, int end) {
+    return start >= 0 && t >= start && t < end && end <= a.total_q;
+}
+
+// Where packed row t stands (in: it belongs to a request).
 struct KvPlace {
     bool in;
     int64_t pos;
 };
 __device__ __forceinline__ KvPlace kv_place(const KvRopeArgs &a, int t, int lane) {
-    const int step = (a.n_req + 63) / 64, at = lane * step;
-    int start = at < a.n_req ? a.q_start[at] : INT32_MAX;
-    int end = step == 1 && at < a.n_req ? a.q_start[at + 1] : 0, m = step == 1 && at < a.n_req ? a.kv_len[at] : 0;
-    int l = __popcll(__ballot(start <= t)) - 1;
+    const KvStarts s = kv_starts(a, lane);
+    int start = s.start, end = s.end, m = s.m;
+    int l = kv_starts_upto(start, t) - 1;
     if (l < 0) return {false, 0};
-    if (step > 1) {
-        const int r = l * step + lane;
-        const bool in = lane < step && r < a.n_req;
+    if (s.step > 1) {
+        const int r = l * s.step + lane;
+        const bool in = lane < s.step && r < a.n_req;
         start = in ? a.q_start[r] : INT32_MAX, end = in ? a.q_start[r + 1] : 0, m = in ? a.kv_len[r] : 0;
-        l = __popcll(__ballot(start <= t)) - 1;
+        l = kv_starts_upto(start, t) - 1;
         if (l < 0) return {false, 0};                    // (starts that decrease)
     }
     start = bcast(start, l), end = bcast(end, l), m = bcast(m, l);
-    return {start >= 0 && t >= start && t < end && end <= a.total_q, (int64_t)m - end + t};
+    return {kv_in_range(a, t, start, end), (int64_t)m - end + t};
+}
+
+// Which of rows t .. t + n - 1 (n <= 32) belong to one, a bit each, by the same searches; the second one in 64 requests from the
+// first group on, a window that the next rows' groups mostly lie in.
+__device__ __forceinline__ uint32_t kv_rows_in(const KvRopeArgs &a, const KvStarts &s, int t, int n, int lane) {
+    int start = s.start, end = s.end, base = INT32_MIN / 2;
+    uint32_t in = 0;
+    for (int i = 0; i < n; ++i) {
+        int l = kv_starts_upto(s.start, t + i) - 1;
+        if (l < 0) continue;
+        if (s.step > 1) {
+            int off = l * s.step - base;
+            if (off < 0 || off + s.step > 64) {
+                base = l * s.step, off = 0;
+                const int r = base + lane;
+                start = r < a.n_req ? a.q_start[r] : INT32_MAX, end = r < a.n_req ? a.q_start[r + 1] : 0;
+            }
+            l = __popcll(__ballot(start <= t + i) & ((~0ull >> (64 - s.step)) << off)) - 1;
+            if (l < 0) continue;
+            l += off;
+        }
+        in |= (uint32_t)kv_in_range(a, t + i, bcast(start, l), bcast(end, l)) << i;
+    }
+    return in;
 }
 
 template <class T>
@@ -68,27 +108,16 @@ __device__ __forceinline__ float kv_lane_sum(float x) {
     return x;
 }
 
-// Whether row t lies in a range that leaves the rows, and so in no request (q_start does not decrease; first and last entry: those of
-// q_start).  Not looked for where there is none.
-__device__ __forceinline__ bool kv_cut_range(const KvRopeArgs &a, int t, int first, int last) {
-    if (first >= 0 && last <= a.total_q) return false;
-    int lo = 0, hi = a.n_req;                        // the last range that begins at t or before
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.q_start[mid] <= t) lo = mid;
-        else hi = mid;
-    }
-    return a.q_start[lo] < 0 || a.q_start[lo + 1] > a.total_q;
-}
-
 // TT tokens of one kv head's values, transposed through LDS as k_kv_append does.
 template <int HD, int TT>
 __device__ __forceinline__ void kv_values(const KvRopeArgs &a, uint32_t *s_v) {
-    constexpr int per = HD / 8, kLdsRow = HD / 2 + 1;
-    const int tid = threadIdx.x, h = blockIdx.x % a.n_kv, t0 = blockIdx.x / a.n_kv * TT, nt = min(TT, a.total_q - t0);
+    constexpr int per = HD / 8, kLdsRow = HD / 2 + 1, kRows = TT / 4;
+    __shared__ uint32_t s_in[4];                     // rows that belong to a request, by the waves that look for them
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int h = blockIdx.x % a.n_kv, t0 = blockIdx.x / a.n_kv * TT, nt = min(TT, a.total_q - t0);
     const int t = tid & (TT - 1);
     const uint32_t slot = t < nt ? (uint32_t)a.slots[t0 + t] : 0xffffffffu;
-    const int first = a.q_start[0], end = a.q_start[a.n_req];
+    const KvStarts starts = kv_starts(a, lane);
 #pragma unroll
     for (int i = tid; i < TT * per; i += 256) {
         const int u = i / per, ch = i - u * per;
@@ -97,8 +126,16 @@ __device__ __forceinline__ void kv_values(const KvRopeArgs &a, uint32_t *s_v) {
         uint32_t *const d = s_v + u * kLdsRow + ch * 4;
         d[0] = x.x, d[1] = x.y, d[2] = x.z, d[3] = x.w;
     }
+    // Most tiles lie in one request, and the numbers of starts grow with the rows.  (Each row looked for in turn, whatever the
+    // ends of the tile say: 4096 tokens of 96 heads 124.8 us.)
+    const int whole = starts.step == 1 ? kv_starts_upto(starts.start, t0) - 1 : -1;
+    const bool one = whole >= 0 && whole == kv_starts_upto(starts.start, t0 + nt - 1) - 1;
+    bool in = false;
+    if (one) in = kv_in_range(a, t0 + t, bcast(starts.start, whole), bcast(starts.end, whole));
+    else s_in[wave] = kv_rows_in(a, starts, t0 + wave * kRows, kRows, lane);
     __syncthreads();
-    if (slot >= (uint32_t)a.n_slots || t0 + t < first || t0 + t >= end || kv_cut_range(a, t0 + t, first, end)) return;
+    if (!one) in = s_in[t / kRows] >> (t % kRows) & 1;
+    if (slot >= (uint32_t)a.n_slots || !in) return;
     const int64_t pg = slot >> a.page_log, off = slot & ((1u << a.page_log) - 1);
     uint16_t *const vp = a.v_pages + (((pg * a.n_kv + h) * HD) << a.page_log) + off;
     for (int d = tid / TT; d < HD / 2; d += 256 / TT) {

@@ -147,7 +147,7 @@ typedef struct pi_kv_rope {
 /* pi_kv_append of new keys turned as `rope` says and of new values, and the step's queries turned the same way to q_out, in
  * one pass.  Row q_start[r] + i of the packed rows stands at position kv_len[r] - n + i (of batch, max_q and max_kv bound
  * nothing here and the table is not read).  Rows that belong to no request are left alone: not appended, q_out not written.
- * q_start must not decrease (rows of ranges that do may be left out).  Slots, strides and pointers are as in pi_kv_append and
+ * q_start must not decrease (rows of ranges that do may be left out, query, key and value together).  Slots, strides and pointers are as in pi_kv_append and
  * pi_kv_attn; q_out may be q itself with the same strides, and overlaps no other argument.  total_q = 0 does nothing. */
 int pi_kv_rope_append(const pi_kv_cache *cache, const pi_kv_batch *batch, const pi_kv_rope *rope, const void *q,
                       int64_t q_token_stride, int64_t q_head_stride, const void *k, int64_t k_token_stride,

@@ -1122,3 +1122,34 @@ def test_example_streams_with_the_smallest_windows(window):
                                shares=st.pages._keep[4].tolist(), page=st.page))
     finally:
         example.pi.pi_kv_attn_sinks = real
+
+
+@pytest.mark.parametrize("heads,hd", [((4, 2), 64), ((80, 80), 128)])      # values in tiles of 16 tokens and of 64
+@pytest.mark.parametrize("n_req", (3, 64, 65, 500, 4096))
+def test_rope_append_writes_all_of_a_row_or_nothing(heads, hd, n_req):
+    """Row starts that decrease: a row's query, key and value are written together or not at all, and those of no
+    range's rows are not."""
+    announce(f"rope append of decreasing starts {heads} n_req={n_req}")
+    rng = random.Random(n_req)
+    rows = 480 if hd == 128 else 200
+    c = rope_case(9, [(rows - 4, 900)], *heads, hd, 64, "f16", hd, 0, False)
+    n_q, n_kv = heads
+    c["kv"] = [rng.randint(1, 5000) for _ in range(n_req)]
+    kinds = [[rng.randint(-3, rows + 3) for _ in range(n_req + 1)], [r * rows // n_req for r in range(n_req, -1, -1)],
+             [(r * 2 % n_req) * rows // n_req for r in range(n_req + 1)], [0, *(rng.randint(0, rows) for _ in range(n_req))]]
+    if n_req == 3:
+        kinds += [[0, 4, 2, 6], [5, 100, 60, rows], [0, rows, 0, rows], [100, 0, rows, 50]]
+    total = c["rows"]
+    for starts in kinds:
+        got = run_rope(c, starts=starts)
+        ranges = [(x, y) for x, y in zip(starts, starts[1:]) if 0 <= x < y <= total]
+        query = (got[0] != 7.0).flatten(1).any(1)
+        for t, slot in enumerate(c["slots"]):
+            if not any(x <= t < y for x, y in ranges):
+                assert not bool(query[t]), (starts[:9], t)
+            if not 0 <= slot < c["k"].shape[0] * c["page"]:
+                continue
+            p, i = divmod(slot, c["page"])
+            key = bool((got[1][p, :, i] != c["k"][p, :, i]).any())
+            value = bool((got[2][p, :, :, i] != c["v"][p, :, :, i]).any())
+            assert key == value == bool(query[t]), (starts[:9], t, key, value)
