@@ -644,33 +644,22 @@ __device__ __forceinline__ void kv_rows_item(const KvAttnArgs &a, const KvItem &
         uint32_t odd_keys = 0;                           // keys of the block with an infinite or NaN value somewhere
         if ((kb < all_lo && (!SINKS || kb + 32 > sinks)) || kb + 32 > all_hi || dead0 || dead1) {
             const bool dead = g & 2 ? dead1 : dead0;
-            uint32_t kept = 0;                           // SINKS: values that some row of the tile sees, a bit each
-            if constexpr (SINKS) {
-                // (as bits: with a branch around each score, as below, one of them stayed unmasked in the code built for
-                // heads of 64)
-                const int j0 = kb + 8 * g;
-                auto below = [&](int end) { return (1u << min(max(end - j0, 0), 8)) - 1u; };
-                const uint32_t first = below(sinks), live = dead ? 0u : 0xffu;
-                const uint32_t seen = live & below(see_hi) & (~below(see_lo) | first);
-                kept = live & below(tile_hi) & (~below(tile_lo) | first);
+            // As bits of the lane's eight keys.  (Not a branch around each score: with the condition of SINKS hipcc 7.2 made one per
+            // score for heads of 64, and the block that masks the eighth came out empty -- s_and_saveexec, s_or of exec -- so that
+            // this score stayed.  No kernel built here has such an empty block.)
+            const int j0 = kb + 8 * g;
+            auto below = [&](int end) { return (1u << min(max(end - j0, 0), 8)) - 1u; };
+            const uint32_t first = SINKS ? below(sinks) : 0u, live = dead ? 0u : 0xffu;
+            const uint32_t seen = live & below(see_hi) & (~below(see_lo) | first);
+            const uint32_t kept = live & below(tile_hi) & (~below(tile_lo) | first);     // values that some row of the tile sees
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s[e] = seen >> e & 1 ? s[e] : -INFINITY;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int j = kb + 8 * g + e;
-                    if (dead || j < see_lo || j >= see_hi) s[e] = -INFINITY;
-                }
-            }
+            for (int e = 0; e < 8; ++e) s[e] = seen >> e & 1 ? s[e] : -INFINITY;
             // Values that no row of the tile sees are cleared (0 x infinity would be NaN); those
             // that some rows see and others do not, and that are not finite, are added row by row.
             uint32_t odd = 0;
 #pragma unroll
             for (int e2 = 0; e2 < 4; ++e2) {
-                const int j = kb + 8 * g + 2 * e2;
-                const uint32_t keep = SINKS ? (kept >> (2 * e2) & 1 ? 0xffffu : 0u) | (kept >> (2 * e2) & 2 ? 0xffff0000u : 0u)
-                                            : (dead || j < tile_lo || j >= tile_hi ? 0u : 0xffffu) |
-                                                  (dead || j + 1 < tile_lo || j + 1 >= tile_hi ? 0u : 0xffff0000u);
+                const uint32_t keep = (kept >> (2 * e2) & 1 ? 0xffffu : 0u) | (kept >> (2 * e2) & 2 ? 0xffff0000u : 0u);
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
                     uint32_t &w = e2 == 0 ? vf[t].x : e2 == 1 ? vf[t].y : e2 == 2 ? vf[t].z : vf[t].w;

@@ -1153,3 +1153,43 @@ def test_rope_append_writes_all_of_a_row_or_nothing(heads, hd, n_req):
             key = bool((got[1][p, :, i] != c["k"][p, :, i]).any())
             value = bool((got[2][p, :, :, i] != c["v"][p, :, :, i]).any())
             assert key == value == bool(query[t]), (starts[:9], t, key, value)
+
+
+# ------------------------------------------------------------------------------ masks at every place of a block
+
+def plant(c, window, sinks):
+    """Keys that the single token of a request does not see score far above those that it sees, and their values are large;
+    such places lie at every offset of the blocks at the window's and the keys' ends."""
+    page, n_kv = c["page"], c["k"].shape[1]
+    for r, m in enumerate(c["kv"]):
+        t = c["starts"][r]
+        if c["starts"][r + 1] - t != 1:
+            continue
+        q = c["q"][t].view(n_kv, -1, c["q"].shape[2]).float().sum(1).to(c["q"].dtype)
+        low = max(m - window, 0)
+        held = kv_util.ceil_div(m, page) * page
+        for j in [*range(min(sinks, low), low), *range(m, held)]:
+            p = c["table"][r][j // page]
+            c["k"][p, :, j % page] = q
+            c["v"][p, :, :, j % page] = 1000.0
+
+
+@pytest.mark.parametrize("dtype", ("f16", "bf16"))
+@pytest.mark.parametrize("sinks", (0, 5, 39))
+@pytest.mark.parametrize("n_q,n_kv,hd,page", [(4, 4, 64, 16), (4, 2, 128, 32), (2, 2, 256, 64)])
+def test_no_score_outside_the_masks_counts(n_q, n_kv, hd, page, sinks, dtype):
+    """For the kernels of every number of waves and the one of chunks: lengths that put both ends of the window at
+    every offset of a block of 32 keys."""
+    few, many = [200 + i for i in range(33)], [90 + i % 33 for i in range(300)]
+    cases = [("four waves", [(1, m) for m in few], None), ("more waves", [(1, m + 100) for m in few], 400), ("one wave", [(1, m) for m in many], 256),
+             ("cut", [(1, m + 2500) for m in few], 9000), ("beside a chunk", [(300, 300)] + [(1, m) for m in few], None)]
+    for name, lens, max_kv in cases:
+        for window in {"cut": (2200,), "more waves": (7, 250)}.get(name, (7, 45)):
+            announce(f"masks {name} heads={n_q}/{n_kv} hd={hd} page={page} {dtype} window={window} sinks={sinks}")
+            c = kv_util.attn_case(hd + sinks, lens, n_q, n_kv, hd, page, dtype)
+            plant(c, window, sinks)
+            rows = {c["starts"][r] for r, (n, _) in enumerate(lens) if n == 1}
+            pick = rows if name != "cut" else set(sorted(rows)[::4])
+            got = run_sinks(c, window, sinks, max_kv=max_kv)
+            assert torch.isfinite(got).all() and float(got[sorted(rows)].abs().max()) < 100, "a masked key counts"
+            check_sinks(c, window, sinks, got, rows=pick)
