@@ -1193,3 +1193,23 @@ def test_no_score_outside_the_masks_counts(n_q, n_kv, hd, page, sinks, dtype):
             got = run_sinks(c, window, sinks, max_kv=max_kv)
             assert torch.isfinite(got).all() and float(got[sorted(rows)].abs().max()) < 100, "a masked key counts"
             check_sinks(c, window, sinks, got, rows=pick)
+
+
+@pytest.mark.parametrize("dtype", ("f16", "bf16"))
+@pytest.mark.parametrize("n_q,n_kv,hd,page,lens,window,sinks", [
+    (16, 16, 64, 16, [(1, m) for m in range(2, 70, 2)], 20, 5),                  # few short ranges
+    (24, 12, 128, 32, [(1, 2 + r % 150) for r in range(90)], 60, 33),            # many short ranges
+    (8, 2, 64, 16, [(1, 9000), (1, 3), (1, 5200), (2, 700)], 3000, 130),         # cut and joined
+    (4, 2, 256, 64, [(1, 12), (2, 500), (1, 300), (3, 40)], 90, 4),
+    (4, 4, 128, 16, [(150, 150)] + [(1, 2 + 9 * r) for r in range(30)], 50, 4)])  # beside a chunk
+def test_sinks_single_tokens_lose_no_bits_of_their_weights(n_q, n_kv, hd, page, lens, window, sinks, dtype):
+    """Off by no more than the output's own rounding and what 32-bit scores leave."""
+    announce(f"sinks precision heads={n_q}/{n_kv} hd={hd} page={page} {dtype} window={window} sinks={sinks}")
+    c = kv_util.attn_case(hd + len(lens), lens, n_q, n_kv, hd, page, dtype)
+    kv_util.past_end(c, math.nan)
+    got = run_sinks(c, window, sinks)
+    rows = [c["starts"][r] + i for r, (n, _) in enumerate(lens) if n <= 3 for i in range(n)]
+    want, mag = U.sinks_reference(c, window, sinks, set(rows))
+    tol = kv_util.attn_tolerance_of_few_rows(want, mag, c["q"].dtype, hd)[rows]
+    err = (got.double() - want).abs()[rows]
+    assert bool((err <= tol).all()), f"worst {float((err / tol).max()):.3f} of the tolerance"
