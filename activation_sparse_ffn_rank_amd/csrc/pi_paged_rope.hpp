@@ -65,6 +65,7 @@ __device__ __forceinline__ KvPlace kv_place(const KvRopeArgs &a, int t, int lane
 __device__ __forceinline__ uint32_t kv_rows_in(const KvRopeArgs &a, const KvStarts &s, int t, int n, int lane) {
     int start = s.start, end = s.end, base = INT32_MIN / 2;
     uint32_t in = 0;
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
         int l = kv_starts_upto(s.start, t + i) - 1;
         if (l < 0) continue;
@@ -111,30 +112,35 @@ __device__ __forceinline__ float kv_lane_sum(float x) {
 // TT tokens of one kv head's values, transposed through LDS as k_kv_append does.
 template <int HD, int TT>
 __device__ __forceinline__ void kv_values(const KvRopeArgs &a, uint32_t *s_v) {
-    constexpr int per = HD / 8, kLdsRow = HD / 2 + 1, kRows = TT / 4;
+    constexpr int per = HD / 8, kLdsRow = HD / 2 + 1, kRows = TT / 4, kLoads = (TT * per + 255) / 256;
     __shared__ uint32_t s_in[4];                     // rows that belong to a request, by the waves that look for them
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = blockIdx.x % a.n_kv, t0 = blockIdx.x / a.n_kv * TT, nt = min(TT, a.total_q - t0);
     const int t = tid & (TT - 1);
-    const uint32_t slot = t < nt ? (uint32_t)a.slots[t0 + t] : 0xffffffffu;
     const KvStarts starts = kv_starts(a, lane);
+    const uint32_t slot = t < nt ? (uint32_t)a.slots[t0 + t] : 0xffffffffu;
+    uint4 x[kLoads];
 #pragma unroll
-    for (int i = tid; i < TT * per; i += 256) {
-        const int u = i / per, ch = i - u * per;
-        if (u >= nt) break;
-        const uint4 x = ld16(a.v + (t0 + u) * a.v_ts + h * a.v_hs + ch * 8);
-        uint32_t *const d = s_v + u * kLdsRow + ch * 4;
-        d[0] = x.x, d[1] = x.y, d[2] = x.z, d[3] = x.w;
+    for (int k = 0; k < kLoads; ++k) {
+        const int i = tid + 256 * k, u = i / per, ch = i - u * per;
+        if (u < nt) x[k] = ld16(a.v + (t0 + u) * a.v_ts + h * a.v_hs + ch * 8);
     }
-    // Most tiles lie in one request, and the numbers of starts grow with the rows.  (Each row looked for in turn, whatever the
-    // ends of the tile say: 4096 tokens of 96 heads 124.8 us.)
-    const int whole = starts.step == 1 ? kv_starts_upto(starts.start, t0) - 1 : -1;
-    const bool one = whole >= 0 && whole == kv_starts_upto(starts.start, t0 + nt - 1) - 1;
-    bool in = false;
-    if (one) in = kv_in_range(a, t0 + t, bcast(starts.start, whole), bcast(starts.end, whole));
-    else s_in[wave] = kv_rows_in(a, starts, t0 + wave * kRows, kRows, lane);
+    // With a request a lane it takes one vote to see that no start decreases; then all rows between the first and the last of them
+    // belong to one, if no range leaves the rows.  (Each row looked for in turn, whatever the starts: 4096 tokens of 96 heads
+    // 124.8 us a pass and 122 so, 16 of 32 heads 4.4 us of kernel and 4.1.)
+    const int first = bcast(starts.start, 0), end = bcast(starts.end, (a.n_req - 1) & 63);
+    const bool plain = starts.step == 1 && !__any(lane < a.n_req && starts.start > starts.end) && first >= 0 && end <= a.total_q;
+    bool in = t0 + t >= first && t0 + t < end;
+    if (!plain) s_in[wave] = kv_rows_in(a, starts, t0 + wave * kRows, kRows, lane);
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+        const int i = tid + 256 * k, u = i / per, ch = i - u * per;
+        if (u >= nt) break;
+        uint32_t *const d = s_v + u * kLdsRow + ch * 4;
+        d[0] = x[k].x, d[1] = x[k].y, d[2] = x[k].z, d[3] = x[k].w;
+    }
     __syncthreads();
-    if (!one) in = s_in[t / kRows] >> (t % kRows) & 1;
+    if (!plain) in = s_in[t / kRows] >> (t % kRows) & 1;
     if (slot >= (uint32_t)a.n_slots || !in) return;
     const int64_t pg = slot >> a.page_log, off = slot & ((1u << a.page_log) - 1);
     uint16_t *const vp = a.v_pages + (((pg * a.n_kv + h) * HD) << a.page_log) + off;
@@ -149,7 +155,9 @@ __device__ __forceinline__ void kv_values(const KvRopeArgs &a, uint32_t *s_v) {
 // side, which it finds next to one another in memory, some rounds of them one after another.  Its lanes compute the cosines and
 // sines of a pair each (heads of 256: two) and hand them round through LDS.  (A wave of 16 tokens side by side, each lane with the
 // angles of its own pairs, was slower: 24 ragged requests of 2440 tokens, 128/8 heads of 64, 36 us and 30 so; 16 tokens of 32 + 32
-// heads 5.1 and 3.7.)  Queries and keys are stored past the caches: the same ragged rows 30 -> 24 us.  Norms and rotations are fp32,
+// heads 5.1 and 3.7, the least of a trace.)  Queries and keys are stored past the caches: the same ragged rows 30 -> 24 us by
+// themselves; together with an attention that reads them at once 2440 ragged rows on 3000 keys take 225 us and 219 with ordinary
+// stores of the queries, 1024 rows of 32 heads on 2048 keys 96 and 97.  Norms and rotations are fp32,
 // rounded once.  Bound by HBM: 4096 tokens of 96 + 96 heads of 128, 604 MB in 122 us (4.9 TB/s), the ragged rows 115 MB in 24;
 // few tokens by the chain q_start -> place -> sines -> store.
 template <class T, int HD, bool PAIRS>
