@@ -208,7 +208,7 @@ __device__ __forceinline__ uint32_t kv_one_round(const KvPagesArgs &a, const KvE
 
 // The first launch, one workgroup: ranges of entries per request by scans; then, if the list is short, all of it.  Bound by the
 // latency of its chain lengths -> table -> shares -> scans -> entries -> counts -> scan -> ring: 64 requests after a drafted
-// step, two pages each at most, 4.7 us (with a list 7.9); a list of 1024 entries 9.4, of 16384 without further owners 55 (with a
+// step, two pages each at most, 5.0 us (with a list 7.9); a list of 1024 entries 9.4, of 16384 without further owners 55 (with a
 // search for first mentions 123).  Nothing but these ranges is kept in scratch memory: a page's count of further owners below
 // zero says that it is free, and serves as the place of the minimum.  At most 4096 * 2^17 = 2^29 entries.
 static __global__ __launch_bounds__(kKvTableThreads) void k_kv_release(KvReleaseArgs x) {

@@ -147,8 +147,9 @@ typedef struct pi_kv_rope {
 /* pi_kv_append of new keys turned as `rope` says and of new values, and the step's queries turned the same way to q_out, in
  * one pass.  Row q_start[r] + i of the packed rows stands at position kv_len[r] - n + i (of batch, max_q and max_kv bound
  * nothing here and the table is not read).  Rows that belong to no request are left alone: not appended, q_out not written.
- * q_start must not decrease (rows of ranges that do may be left out, query, key and value together).  Slots, strides and pointers are as in pi_kv_append and
- * pi_kv_attn; q_out may be q itself with the same strides, and overlaps no other argument.  total_q = 0 does nothing. */
+ * q_start must not decrease (rows of ranges that do may be left out, query, key and value together).  Slots, strides and
+ * pointers are as in pi_kv_append and pi_kv_attn; q_out may be q itself with the same strides, and overlaps no other argument.
+ * total_q = 0 does nothing. */
 int pi_kv_rope_append(const pi_kv_cache *cache, const pi_kv_batch *batch, const pi_kv_rope *rope, const void *q,
                       int64_t q_token_stride, int64_t q_head_stride, const void *k, int64_t k_token_stride,
                       int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,
@@ -161,7 +162,8 @@ int pi_kv_rope_append(const pi_kv_cache *cache, const pi_kv_batch *batch, const 
  *   j <= p  and  (j > p - window  or  j < sinks).
  * sinks >= 0 (0: pi_kv_attn with this window), window > 0 with sinks.  Pages between the first tokens and the windows of a step's tokens
  * are not read: their table entries may be out of range (pi_kv_release).  All else, the workspace included, is as in
- * pi_kv_attn; its size depends on window and sinks. */
+ * pi_kv_attn; its size depends on window and sinks.  Keys are taken as they were appended: positions that pi_kv_rope_append
+ * gave the first tokens stay theirs, and the distance to them grows with the request. */
 size_t pi_kv_attn_sinks_workspace_bytes(const pi_kv_cache *cache, const pi_kv_batch *batch, int32_t total_q, int32_t n_q,
                                         int32_t window, int32_t sinks);
 int pi_kv_attn_sinks(const pi_kv_cache *cache, const pi_kv_batch *batch, const void *q, int64_t q_token_stride,
@@ -242,6 +244,8 @@ size_t pi_kv_pages_workspace_bytes(const pi_kv_pages *pages);
  *  - drop_to < cached drops from the middle: cached_next = cached, the dropped entries become -1 (pages without keys).
  *    What a window has passed goes this way: drop_from = the first tokens that stay, drop_to = min(c - window + 1, c - 1) of a
  *    request of c positions whose next token stands at position c, so that it ends below c with a window of one token too.
+ *    The columns stay used, so a request holds at most max_pages * page positions, dropped ones included; tokens appended to
+ *    a dropped page (after a cut back into it) have no slot.
  * A page given up once more than it has further owners goes behind the free ones, in the order of first mention (requests in order,
  * a page given up for a copy before the later ones); entries outside [0, n_pages) are skipped.  cached outside [0, max_pages * page]
  * is refused.  counts = {entries given up, pages gone back, pages taken, requests refused}. */
